@@ -631,6 +631,129 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
                          float *dW_gu, float *dW_down, int forget, int B, int T, int d_model, int d_ff, float eps,
                          void *ws, size_t ws_bytes, slstm_stream_t stream);
 
+/*
+ * Linear attention with a decay for each head: the recurrence with a matrix
+ * state beside the cell's, in the same forms (whole sequences, packed ones,
+ * gradients, single tokens).  Per sequence and value head:
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T   (d_k x d_v, fp32; S_{-1} = s0)
+ *   o_t = scale * S_t^T q_t
+ * The H value heads (v, o, g, the states) share the H_qk query and key heads
+ * in order: head h reads query and key head h / (H / H_qk).
+ *   q, k   (B, T, H_qk, d_k), v (B, T, H, d_v) of `dtype`: the heads and
+ *          features of a token are contiguous, consecutive tokens ld_q, ld_k,
+ *          ld_v elements apart (so that they can be slices of one projection)
+ *          and consecutive sequences T tokens
+ *   g      fp32 log decays, (B, T, H) for SLSTM_DECAY_TOKEN or (H,) for
+ *          SLSTM_DECAY_HEAD.  -inf (and anything below -87.3, whose factor is
+ *          no normal fp32 number) clears the state before its token.
+ *   s0     (B, H, d_k, d_v) fp32 or NULL (zeros); sT likewise, the state after
+ *          the last token, or NULL; sT may be s0
+ *   o      (B, T, H, d_v) of `dtype`, contiguous
+ * Sums and states are fp32; bf16 with d_k and d_v up to 128 and d_k, d_v and
+ * the strides multiples of 8 runs on the tensor cores (operands bf16, the
+ * states entering a product split into two bf16 terms wherever an fp32 output
+ * depends on it), everything else on the CUDA cores.  Gradients of q, k, v
+ * have `dtype` and are contiguous, those of g and s0 are fp32.
+ * A token whose q, k, v or g is not finite spoils its sequence, earlier tokens
+ * of its 128 included, never another sequence.
+ */
+typedef enum { SLSTM_DECAY_TOKEN = 0, SLSTM_DECAY_HEAD = 1 } slstm_decay;
+#define SLSTM_LA_MAX_DIM 256 /* largest d_k and d_v of the linear attention */
+
+typedef struct {
+    int H;                       /* value heads                               */
+    int H_qk;                    /* query and key heads, dividing H           */
+    int d_k, d_v;                /* 1 .. SLSTM_LA_MAX_DIM                     */
+    int dtype;                   /* SLSTM_F32 or SLSTM_BF16                   */
+    int decay;                   /* SLSTM_DECAY_TOKEN or SLSTM_DECAY_HEAD     */
+    float scale;
+    long long ld_q, ld_k, ld_v;  /* elements between tokens, at least the
+                                    heads x features of one                  */
+} slstm_linear_attention_config;
+
+/*
+ * Workspace bytes of the calls below (256-aligned), 0 for sizes they refuse.
+ * packed: B sequences in T packed tokens; backward: of the gradients.
+ */
+size_t slstm_linear_attention_workspace_size(const slstm_linear_attention_config *cfg, int B, int T, int packed,
+                                             int backward);
+
+/*
+ * The forward pass.  Pointers are 16-byte aligned where the tensor cores take
+ * the call (see above) and for the states, else aligned to their elements.
+ */
+int slstm_linear_attention_forward(const void *q, const void *k, const void *v, const float *g, const float *s0,
+                                   void *o, float *sT, const slstm_linear_attention_config *cfg, int B, int T,
+                                   void *ws, size_t ws_bytes, slstm_stream_t stream);
+
+/*
+ * Gradients of L = sum dO . o + sum dsT . sT: dq, dk (B, T, H_qk, d_k), dv
+ * (B, T, H, d_v) of `dtype`, summed over the heads that share; dg fp32 of g's
+ * shape or NULL; ds0 (B, H, d_k, d_v) fp32 or NULL.  dO (B, T, H, d_v) of
+ * `dtype`, contiguous; dsT fp32 or NULL (zeros).  The forward pass leaves
+ * nothing behind that this needs: the states are computed again.  dg is 0 at a
+ * token that clears the state.
+ */
+int slstm_linear_attention_backward(const void *q, const void *k, const void *v, const float *g, const float *s0,
+                                    const void *dO, const float *dsT, void *dq, void *dk, void *dv, float *dg,
+                                    float *ds0, const slstm_linear_attention_config *cfg, int B, int T, void *ws,
+                                    size_t ws_bytes, slstm_stream_t stream);
+
+/*
+ * Packed sequences: q, k (total_T, H_qk, d_k), v, o, dO (total_T, H, d_v), g
+ * (total_T, H) or (H,), states (n_seq, H, d_k, d_v), and cu_seqlens a device
+ * int32 array of n_seq + 1 exclusive-prefix offsets; a sequence may be empty
+ * (its sT is its s0).  Offsets are clamped into [0, total_T] and raised to the
+ * largest before them.  Tokens in front of the first offset or behind the last
+ * belong to no sequence: their rows of the outputs are left as they were.
+ */
+int slstm_linear_attention_forward_varlen(const void *q, const void *k, const void *v, const float *g,
+                                          const float *s0, const int *cu_seqlens, int n_seq, void *o, float *sT,
+                                          const slstm_linear_attention_config *cfg, int total_T, void *ws,
+                                          size_t ws_bytes, slstm_stream_t stream);
+int slstm_linear_attention_backward_varlen(const void *q, const void *k, const void *v, const float *g,
+                                           const float *s0, const int *cu_seqlens, int n_seq, const void *dO,
+                                           const float *dsT, void *dq, void *dk, void *dv, float *dg, float *ds0,
+                                           const slstm_linear_attention_config *cfg, int total_T, void *ws,
+                                           size_t ws_bytes, slstm_stream_t stream);
+
+/*
+ * One token of B sequences: q, k (B, H_qk, d_k) and v (B, H, d_v), rows ld_q,
+ * ld_k, ld_v apart, g (B, H) or (H,), s_prev (B, H, d_k, d_v) or NULL (zeros),
+ * o (B, H, d_v) contiguous; s_next may be s_prev itself but must not overlap it
+ * otherwise.  The states are 16-byte aligned, the rest to their elements.  One
+ * launch, no workspace, capturable.
+ */
+int slstm_linear_attention_step(const void *q, const void *k, const void *v, const float *g, const float *s_prev,
+                                float *s_next, void *o, const slstm_linear_attention_config *cfg, int B,
+                                slstm_stream_t stream);
+
+/*
+ * Layer norm over each of `groups` consecutive slices of d features of a row
+ * (groups = 1: the row; groups = H: each head of an attention's output):
+ *   y = (x - mean) * rstd * w + b,  rstd = 1 / sqrt(var + eps), var the mean of
+ *   (x - mean)^2
+ * x (rows, groups * d) of x_dtype, y of y_dtype, both contiguous; w and b
+ * (groups * d) fp32, b may be NULL; mean and rstd (rows, groups) fp32, which
+ * the backward pass takes.  1 <= d <= SLSTM_LN_MAX_DIM.  Pointers aligned to
+ * their elements; 16-byte aligned ones and d a multiple of 8 are faster.  y may
+ * be x when the types are the same.
+ */
+#define SLSTM_LN_MAX_DIM 16384 /* largest slice of the layer norm */
+int slstm_layer_norm_forward(const void *x, int x_dtype, const float *w, const float *b, void *y, int y_dtype,
+                             float *mean, float *rstd, long long rows, int groups, int d, float eps,
+                             slstm_stream_t stream);
+
+/*
+ * Gradients of sum dy . y: dx (rows, groups * d) of x_dtype, dw and db
+ * (groups * d) fp32.  dx may be dy when the types are the same.  The sums over
+ * the rows are taken in an order that the sizes alone decide.
+ */
+size_t slstm_layer_norm_workspace_size(long long rows, int groups, int d);
+int slstm_layer_norm_backward(const void *x, int x_dtype, const float *w, const void *dy, int y_dtype,
+                              const float *mean, const float *rstd, void *dx, float *dw, float *db, long long rows,
+                              int groups, int d, void *ws, size_t ws_bytes, slstm_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -48,6 +48,10 @@ SLSTM_GEMM_TILES_AUTO = 0
 SLSTM_GEMM_TILES_PAIR = 1
 SLSTM_GEMM_TILES_SINGLE = 2
 SLSTM_NOALLOC_SCRATCH_BYTES = 8 << 20
+SLSTM_DECAY_TOKEN = 0
+SLSTM_DECAY_HEAD = 1
+SLSTM_LA_MAX_DIM = 256
+SLSTM_LN_MAX_DIM = 16384
 
 
 class NewtonConfig(ctypes.Structure):
@@ -58,11 +62,19 @@ class NewtonConfig(ctypes.Structure):
                 ("events", ctypes.c_void_p), ("loop_from", ctypes.c_int)]
 
 
+class LinearAttentionConfig(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int), ("H_qk", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("decay", ctypes.c_int), ("scale", ctypes.c_float),
+                ("ld_q", ctypes.c_longlong), ("ld_k", ctypes.c_longlong), ("ld_v", ctypes.c_longlong)]
+
+
 STATS_BYTES = 4 * 4 + 2 * 4 * SLSTM_STATS_HISTORY + 2 * 4
 
 _V = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_longlong
+_LA = ctypes.POINTER(LinearAttentionConfig)
 
 # name -> (restype, argtypes); every function of include/slstm.h
 SIGNATURES = {
@@ -100,6 +112,15 @@ SIGNATURES = {
     "slstm_block_backward": (_I, [_V] * 18 + [_I, _I, _I, _I, _I, ctypes.c_float, _V, _Z, _V]),
     "slstm_block_forward": (_I, [_V, _V, _V, _V, _V, _V, _V, _V, _V, _V, ctypes.POINTER(NewtonConfig), _V,
                                  _I, _I, _I, _I, ctypes.c_float, _V, _Z, _V]),
+    "slstm_linear_attention_workspace_size": (_Z, [_LA, _I, _I, _I, _I]),
+    "slstm_linear_attention_forward": (_I, [_V] * 7 + [_LA, _I, _I, _V, _Z, _V]),
+    "slstm_linear_attention_backward": (_I, [_V] * 12 + [_LA, _I, _I, _V, _Z, _V]),
+    "slstm_linear_attention_forward_varlen": (_I, [_V] * 6 + [_I, _V, _V, _LA, _I, _V, _Z, _V]),
+    "slstm_linear_attention_backward_varlen": (_I, [_V] * 6 + [_I] + [_V] * 7 + [_LA, _I, _V, _Z, _V]),
+    "slstm_linear_attention_step": (_I, [_V] * 7 + [_LA, _I, _V]),
+    "slstm_layer_norm_forward": (_I, [_V, _I, _V, _V, _V, _I, _V, _V, _L, _I, _I, ctypes.c_float, _V]),
+    "slstm_layer_norm_workspace_size": (_Z, [_L, _I, _I]),
+    "slstm_layer_norm_backward": (_I, [_V, _I, _V, _V, _I, _V, _V, _V, _V, _V, _L, _I, _I, _V, _Z, _V]),
 }
 
 _lib = None

@@ -513,3 +513,304 @@ def newton_backward_head(x, Wx, P, R_head, s0, S, dH, *, forget="sigmoid", out: 
         _ptr(out["dWx"]), _ptr(out["dR_head"]), _ptr(out["db"]), _ptr(out.get("ds0")), forget_code(forget), B, T,
         d_in, d_h, dh, _ptr(ws), ws.numel(), _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------
+# linear attention with a decay for each head
+# ---------------------------------------------------------------------------
+def _need_tokens(t: torch.Tensor, name: str, lead, heads: int, d: int, dtype, device) -> int:
+    """Checks a (*lead, heads, d) tensor whose tokens are contiguous and evenly
+    spaced (a slice of a projection's output is); returns their spacing."""
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    shape = (*lead, heads, d)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    st = t.stride()
+    if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
+        raise ValueError(f"{name}: the heads and features of a token must be contiguous")
+    # the tokens' spacing, from the innermost leading dimension that has one
+    ld, span = None, 1
+    for n, s in zip(reversed(lead), reversed(st[:-2])):
+        if n > 1:
+            if ld is None:
+                ld = s
+                if span != 1 or s < heads * d:
+                    raise ValueError(f"{name}: tokens must not overlap")
+            elif s != ld * span:
+                raise ValueError(f"{name}: tokens must be evenly spaced (sequences T of them apart)")
+        span *= n
+    return heads * d if ld is None else ld
+
+
+def _la_config(q, k, v, g, lead, scale):
+    """Checks q, k, v and g; returns the C ABI's config."""
+    if v.dim() != len(lead) + 2 or q.dim() != len(lead) + 2:
+        raise ValueError(f"q, k and v must have {len(lead) + 2} dimensions")
+    Hqk, dk = q.shape[-2:]
+    H, dv = v.shape[-2:]
+    dev, dt = q.device, q.dtype
+    if dt not in _DTYPE:
+        raise ValueError(f"q, k and v must be float32 or bfloat16, got {dt}")
+    if Hqk < 1 or H % Hqk:
+        raise ValueError(f"the {H} value heads must be a multiple of the {Hqk} query and key heads")
+    if not (1 <= dk <= _lib.SLSTM_LA_MAX_DIM and 1 <= dv <= _lib.SLSTM_LA_MAX_DIM):
+        raise ValueError(f"d_k = {dk} and d_v = {dv} must lie in 1..{_lib.SLSTM_LA_MAX_DIM}")
+    ldq = _need_tokens(q, "q", lead, Hqk, dk, dt, dev)
+    ldk = _need_tokens(k, "k", lead, Hqk, dk, dt, dev)
+    ldv = _need_tokens(v, "v", lead, H, dv, dt, dev)
+    _need(g, "g", (H,) if g.dim() == 1 else (*lead, H))
+    if g.device != dev:
+        raise ValueError(f"g must be a CUDA tensor on {dev}")
+    decay = _lib.SLSTM_DECAY_HEAD if g.dim() == 1 else _lib.SLSTM_DECAY_TOKEN
+    return _lib.LinearAttentionConfig(H, Hqk, dk, dv, _DTYPE[dt], decay, dk ** -0.5 if scale is None else float(scale),
+                                      ldq, ldk, ldv)
+
+
+def _need_on(t, name, shape, dtype, device):
+    """_need for a tensor that has to be on the inputs' device; None passes."""
+    if t is not None:
+        _need(t, name, shape, dtype)
+        if t.device != device:
+            raise ValueError(f"{name} must be a CUDA tensor on {device}")
+
+
+def _la_workspace(cfg, B, T, packed, backward, ws, device):
+    n = int(load().slstm_linear_attention_workspace_size(ctypes.byref(cfg), B, T, int(packed), int(backward)))
+    if n == 0:
+        raise ValueError("unsupported sizes")
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if ws.device != device or ws.numel() * ws.element_size() < n:
+        raise ValueError(f"ws must hold {n} bytes on {device}")
+    return ws
+
+
+def linear_attention_workspace(q, v, g, *, n_seq: int = 0, backward: bool = False) -> torch.Tensor:
+    """A workspace for linear_attention_forward or _backward of tensors like
+    these (of their _varlen forms: n_seq sequences), to pass as ws."""
+    lead = q.shape[:-2]
+    cfg = _la_config(q, q, v, g, lead, None)
+    B, T = (n_seq, lead[0]) if n_seq else lead
+    return _la_workspace(cfg, B, T, n_seq > 0, backward, None, q.device)
+
+
+def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: torch.Tensor = None,
+                             sT: torch.Tensor = None, ws: torch.Tensor = None):
+    """S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t over B sequences of T tokens; returns
+    (o, sT).  q, k (B, T, H_qk, d_k) and v (B, T, H, d_v) of one dtype (float32 or bfloat16; slices of
+    one projection will do: a token's heads and features contiguous, the tokens evenly spaced), H a
+    multiple of H_qk (value head h reads query and key head h // (H // H_qk)); g float32 log decays
+    (B, T, H), or (H,) for one decay a head, -inf clearing the state; s0 (B, H, d_k, d_v) float32 or
+    None (zeros).  scale: d_k ** -0.5 by default.  sT, the state after the last token, may be s0."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
+    B, T = lead = tuple(q.shape[:2])
+    cfg = _la_config(q, k, v, g, lead, scale)
+    H, dv, dev = cfg.H, cfg.d_v, q.device
+    state = (B, H, cfg.d_k, dv)
+    _need_on(s0, "s0", state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty(B, T, H, dv, dtype=q.dtype, device=dev)
+        if sT is None:
+            sT = torch.empty(state, dtype=torch.float32, device=dev)
+        _need_on(o, "o", (B, T, H, dv), q.dtype, dev)
+        _need_on(sT, "sT", state, torch.float32, dev)
+        ws = _la_workspace(cfg, B, T, False, False, ws, dev)
+        check("slstm_linear_attention_forward", load().slstm_linear_attention_forward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(o), _ptr(sT), ctypes.byref(cfg), B, T, _ptr(ws),
+            ws.numel() * ws.element_size(), _stream()))
+    return o, sT
+
+
+def _la_grads(q, v, g, state, out, dev, with_dg):
+    if out is None:
+        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
+               "dk": torch.empty(q.shape, dtype=q.dtype, device=dev),
+               "dv": torch.empty(v.shape, dtype=v.dtype, device=dev),
+               "ds0": torch.empty(state, dtype=torch.float32, device=dev)}
+        if with_dg:
+            out["dg"] = torch.empty(g.shape, dtype=torch.float32, device=dev)
+    for name, like, dt in (("dq", q.shape, q.dtype), ("dk", q.shape, q.dtype), ("dv", v.shape, v.dtype),
+                           ("dg", g.shape, torch.float32), ("ds0", state, torch.float32)):
+        if name in ("dq", "dk", "dv") and out.get(name) is None:
+            raise ValueError(f"out needs {name}")
+        _need_on(out.get(name), name, like, dt, dev)
+    return out
+
+
+def linear_attention_backward(q, k, v, g, s0, dO, dsT=None, *, scale: float = None, with_dg: bool = True,
+                              out: dict = None, ws: torch.Tensor = None) -> dict:
+    """Gradients of sum(dO * o) + sum(dsT * sT) of linear_attention_forward at its inputs; returns dict
+    dq, dk, dv (of q's dtype, contiguous; dq and dk summed over the heads that share them), dg (float32,
+    of g's shape; left out without with_dg) and ds0.  dO (B, T, H, d_v) of q's dtype, contiguous; dsT
+    (B, H, d_k, d_v) float32 or None (zeros)."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
+    B, T = lead = tuple(q.shape[:2])
+    cfg = _la_config(q, k, v, g, lead, scale)
+    dev, state = q.device, (B, cfg.H, cfg.d_k, cfg.d_v)
+    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_on(dO, "dO", v.shape, q.dtype, dev)
+    _need_on(dsT, "dsT", state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        out = _la_grads(q, v, g, state, out, dev, with_dg)
+        ws = _la_workspace(cfg, B, T, False, True, ws, dev)
+        check("slstm_linear_attention_backward", load().slstm_linear_attention_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(dO), _ptr(dsT), _ptr(out["dq"]), _ptr(out["dk"]),
+            _ptr(out["dv"]), _ptr(out.get("dg")), _ptr(out.get("ds0")), ctypes.byref(cfg), B, T, _ptr(ws),
+            ws.numel() * ws.element_size(), _stream()))
+    return out
+
+
+def linear_attention_forward_varlen(q, k, v, g, s0, cu_seqlens, *, scale: float = None, o: torch.Tensor = None,
+                                    sT: torch.Tensor = None, ws: torch.Tensor = None):
+    """linear_attention_forward over packed sequences: q, k (total_T, H_qk, d_k), v (total_T, H, d_v),
+    g (total_T, H) or (H,), s0 (n_seq, H, d_k, d_v) or None, cu_seqlens int32 (n_seq + 1,)
+    exclusive-prefix offsets; returns (o, sT).  Rows of o outside the sequences are left as they were."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be (total_T, H_qk, d_k), got {tuple(q.shape)}")
+    lead = tuple(q.shape[:1])
+    n_seq = cu_seqlens.numel() - 1
+    cfg = _la_config(q, k, v, g, lead, scale)
+    H, dv, dev = cfg.H, cfg.d_v, q.device
+    state = (n_seq, H, cfg.d_k, dv)
+    _need_cu(cu_seqlens, n_seq)
+    _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
+    _need_on(s0, "s0", state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty(lead[0], H, dv, dtype=q.dtype, device=dev)
+        if sT is None:
+            sT = torch.empty(state, dtype=torch.float32, device=dev)
+        _need_on(o, "o", (lead[0], H, dv), q.dtype, dev)
+        _need_on(sT, "sT", state, torch.float32, dev)
+        ws = _la_workspace(cfg, n_seq, lead[0], True, False, ws, dev)
+        check("slstm_linear_attention_forward_varlen", load().slstm_linear_attention_forward_varlen(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(cu_seqlens), n_seq, _ptr(o), _ptr(sT),
+            ctypes.byref(cfg), lead[0], _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+    return o, sT
+
+
+def linear_attention_backward_varlen(q, k, v, g, s0, cu_seqlens, dO, dsT=None, *, scale: float = None,
+                                     with_dg: bool = True, out: dict = None, ws: torch.Tensor = None) -> dict:
+    """Gradients of linear_attention_forward_varlen; returns dict dq, dk, dv, dg, ds0 as
+    linear_attention_backward.  Rows outside the sequences are left as they were."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be (total_T, H_qk, d_k), got {tuple(q.shape)}")
+    lead = tuple(q.shape[:1])
+    n_seq = cu_seqlens.numel() - 1
+    cfg = _la_config(q, k, v, g, lead, scale)
+    dev, state = q.device, (n_seq, cfg.H, cfg.d_k, cfg.d_v)
+    _need_cu(cu_seqlens, n_seq)
+    _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
+    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_on(dO, "dO", v.shape, q.dtype, dev)
+    _need_on(dsT, "dsT", state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        out = _la_grads(q, v, g, state, out, dev, with_dg)
+        ws = _la_workspace(cfg, n_seq, lead[0], True, True, ws, dev)
+        check("slstm_linear_attention_backward_varlen", load().slstm_linear_attention_backward_varlen(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(cu_seqlens), n_seq, _ptr(dO), _ptr(dsT),
+            _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dg")), _ptr(out.get("ds0")),
+            ctypes.byref(cfg), lead[0], _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+    return out
+
+
+def linear_attention_step(q, k, v, g, s_prev=None, *, scale: float = None, o: torch.Tensor = None,
+                          out: torch.Tensor = None):
+    """One token of B sequences: q, k (B, H_qk, d_k), v (B, H, d_v), g (B, H) or (H,), s_prev
+    (B, H, d_k, d_v) float32 or None (zeros); returns (o, s_next), s_next written into `out` when given
+    (`out` may be `s_prev`)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be (B, H_qk, d_k), got {tuple(q.shape)}")
+    lead = tuple(q.shape[:1])
+    cfg = _la_config(q, k, v, g, lead, scale)
+    B, dev = lead[0], q.device
+    state = (B, cfg.H, cfg.d_k, cfg.d_v)
+    _need_on(s_prev, "s_prev", state, torch.float32, dev)
+    with torch.cuda.device(dev):
+        if o is None:
+            o = torch.empty(B, cfg.H, cfg.d_v, dtype=q.dtype, device=dev)
+        if out is None:
+            out = torch.empty(state, dtype=torch.float32, device=dev)
+        _need_on(o, "o", (B, cfg.H, cfg.d_v), q.dtype, dev)
+        _need_on(out, "out", state, torch.float32, dev)
+        check("slstm_linear_attention_step", load().slstm_linear_attention_step(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s_prev), _ptr(out), _ptr(o), ctypes.byref(cfg), B, _stream()))
+    return o, out
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+def _ln_dims(x, groups):
+    if x.device.type != "cuda" or not x.is_contiguous() or x.dim() < 1 or x.dtype not in _DTYPE:
+        raise ValueError("x must be a contiguous float32 or bfloat16 CUDA tensor")
+    D = x.shape[-1]
+    if groups < 1 or D < 1 or D % groups:
+        raise ValueError(f"groups = {groups} must divide the {D} features")
+    if D // groups > _lib.SLSTM_LN_MAX_DIM:
+        raise ValueError(f"a slice has {D // groups} features, at most {_lib.SLSTM_LN_MAX_DIM} are supported")
+    if x.numel() == 0:
+        raise ValueError("x has no rows")
+    return x.numel() // D, D
+
+
+def layer_norm_forward(x, w, b=None, *, groups: int = 1, eps: float = 1e-5, y_dtype=None, y: torch.Tensor = None):
+    """Layer norm over each of `groups` equal slices of the last dimension (groups = H: each head of an
+    attention's output); returns (y, mean, rstd).  x (..., D) float32 or bfloat16, w and b (D,) float32,
+    b may be None; y of y_dtype (x's by default), mean and rstd (..., groups) float32 for
+    layer_norm_backward.  y may be x."""
+    rows, D = _ln_dims(x, groups)
+    dev = x.device
+    y_dtype = (x.dtype if y is None else y.dtype) if y_dtype is None else y_dtype
+    if y_dtype not in _DTYPE:
+        raise ValueError(f"y must be float32 or bfloat16, got {y_dtype}")
+    _need_on(w, "w", (D,), torch.float32, dev)
+    _need_on(b, "b", (D,), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if y is None:
+            y = torch.empty(x.shape, dtype=y_dtype, device=dev)
+        _need_on(y, "y", x.shape, y_dtype, dev)
+        stats = torch.empty(2, *x.shape[:-1], groups, dtype=torch.float32, device=dev)
+        mean, rstd = stats[0], stats[1]
+        check("slstm_layer_norm_forward", load().slstm_layer_norm_forward(
+            _ptr(x), _DTYPE[x.dtype], _ptr(w), _ptr(b), _ptr(y), _DTYPE[y_dtype], _ptr(mean), _ptr(rstd), rows, groups,
+            D // groups, float(eps), _stream()))
+    return y, mean, rstd
+
+
+def layer_norm_backward(x, w, dy, mean, rstd, *, groups: int = 1, out: dict = None, ws: torch.Tensor = None) -> dict:
+    """Gradients of sum(dy * y) of layer_norm_forward, given its mean and rstd; returns dict dx (x's
+    dtype), dw and db (D,) float32.  dy (..., D) of y's dtype.  dx may be dy."""
+    rows, D = _ln_dims(x, groups)
+    dev = x.device
+    if dy.dtype not in _DTYPE:
+        raise ValueError(f"dy must be float32 or bfloat16, got {dy.dtype}")
+    _need_on(w, "w", (D,), torch.float32, dev)
+    _need_on(dy, "dy", x.shape, dy.dtype, dev)
+    _need_on(mean, "mean", (*x.shape[:-1], groups), torch.float32, dev)
+    _need_on(rstd, "rstd", (*x.shape[:-1], groups), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            dwb = torch.empty(2, D, dtype=torch.float32, device=dev)
+            out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dw": dwb[0], "db": dwb[1]}
+        _need_on(out["dx"], "dx", x.shape, x.dtype, dev)
+        _need_on(out["dw"], "dw", (D,), torch.float32, dev)
+        _need_on(out["db"], "db", (D,), torch.float32, dev)
+        n = int(load().slstm_layer_norm_workspace_size(rows, groups, D // groups))
+        if n == 0:
+            raise ValueError("unsupported sizes")
+        if ws is None:
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        if ws.device != dev or ws.numel() * ws.element_size() < n:
+            raise ValueError(f"ws must hold {n} bytes on {dev}")
+        check("slstm_layer_norm_backward", load().slstm_layer_norm_backward(
+            _ptr(x), _DTYPE[x.dtype], _ptr(w), _ptr(dy), _DTYPE[dy.dtype], _ptr(mean), _ptr(rstd), _ptr(out["dx"]),
+            _ptr(out["dw"]), _ptr(out["db"]), rows, groups, D // groups, _ptr(ws), ws.numel() * ws.element_size(),
+            _stream()))
+    return out

@@ -1,0 +1,62 @@
+// Linear attention with a decay for each head: the arguments shared by its
+// launchers (linear_attention.cu: any sizes and types on the CUDA cores;
+// linear_attention_tc.cu: bf16 on the tensor cores), behind the C ABI in
+// slstm_api.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "../../include/slstm.h"
+
+namespace slstm {
+
+// One call.  Rows are tokens: B sequences of T rows each, or (cu != null)
+// n_seq packed sequences over T rows.
+struct LaArgs {
+    int B, T;                 // dense: B x T rows; packed: B = n_seq, T = total rows
+    int H, Hqk, dk, dv;
+    long long ldq, ldk, ldv;  // elements between rows
+    int dtype;
+    int per_head;             // g is (H,), not (rows, H)
+    float scale;
+    const int *cu;            // packed offsets (n_seq + 1), or null
+    const void *q, *k, *v;
+    const float *g, *s0;
+    void *o;
+    float *sT;
+    // backward only
+    const void *dO;
+    const float *dsT;
+    void *dq, *dk_, *dv_;
+    float *dg, *ds0;
+};
+
+size_t la_simt_workspace(const LaArgs &a, bool backward);
+cudaError_t la_simt_forward(const LaArgs &a, void *ws, cudaStream_t st);
+cudaError_t la_simt_backward(const LaArgs &a, void *ws, cudaStream_t st);
+cudaError_t la_step_launch(const LaArgs &a, float *s_next, cudaStream_t st);
+
+// The chunks of C rows that the sequences are cut into, each sequence from its
+// own first row.  Dense sequences need no table; of packed ones, pos[k] is the
+// first row of sequence k (the offsets clamped into the rows and made
+// nondecreasing, so that malformed ones lead nowhere out of range) and coff[k]
+// the number of chunks before it.
+struct LaChunks {
+    int n_seq, T, C;          // T: rows of a dense sequence
+    int nc;                   // dense: chunks of a sequence
+    int total;                // an upper bound of the chunks (dense: the number)
+    const int *pos, *coff;    // packed: [n_seq + 1] each; else null
+};
+size_t la_table_bytes(const LaArgs &a);
+int la_chunk_bound(const LaArgs &a, int C);
+// Fill the table (packed) at `mem` on `st`.
+cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st);
+
+// Sums of the fp32 per-head partial gradients over the heads that share a
+// query and key head: out[row][hq][d] = sum over r of part[row][hq * rep + r][d].
+cudaError_t la_share_sum(const float *part, void *out, int dtype, const LaChunks &ch, const LaArgs &a, cudaStream_t st);
+// dg[h] = sum of part[c][h] over the chunks in order.
+cudaError_t la_head_sum(const float *part, float *dg, const LaChunks &ch, int H, cudaStream_t st);
+
+}  // namespace slstm

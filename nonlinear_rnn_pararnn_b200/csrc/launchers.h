@@ -149,6 +149,16 @@ void gemm_tc_waves(int *tile_rows, int *units);
 // out[i] = sum over z in order of part[z * n + i] (split-K partial sums).
 cudaError_t sum_splits(const float *part, float *out, long long n, int splits, cudaStream_t st);
 
+// Layer norm (layer_norm.cu): `groups` slices of d columns in each of `rows`
+// rows; x_dtype: of x and dx, y_dtype: of y and dy.  1 <= d <= SLSTM_LN_MAX_DIM.
+size_t layer_norm_workspace_bytes(long long rows, int groups, int d);
+cudaError_t layer_norm_forward(const void *x, int x_dtype, const float *w, const float *b, void *y, int y_dtype,
+                               float *mean, float *rstd, long long rows, int groups, int d, float eps,
+                               cudaStream_t st);
+cudaError_t layer_norm_backward(const void *x, int x_dtype, const float *w, const void *dy, int y_dtype,
+                                const float *mean, const float *rstd, void *dx, float *dw, float *db, long long rows,
+                                int groups, int d, void *ws, cudaStream_t st);
+
 // Input projection P = x Wx^T + bias (tcgen05 for bf16, CUDA cores for fp32).
 size_t preact_workspace_bytes(int B, int T, int d_in, int d_h, int dtype);
 cudaError_t preact_launch(const void *x, const void *Wx, int dtype, const float *bias, float *P,

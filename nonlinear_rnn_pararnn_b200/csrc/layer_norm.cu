@@ -1,0 +1,433 @@
+// Layer norm, forward and backward, over each of `groups` equal slices of a
+// row (one slice: the whole row; a slice for each head behind an attention):
+//   y = (x - mean) rstd w + b,  rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+//   dx = rstd (p - mean(p) - xhat mean(p xhat)),  p = dy w,  xhat = (x - mean) rstd
+//   dw = sum over rows of dy xhat,  db = sum over rows of dy
+// A slice is held in the registers of its TPR threads (NV pieces of 8 elements
+// each, 16-byte loads where the width and the pointers allow), so x (and dy)
+// are read once; the variance is the mean of the squared deviations from the
+// mean, not a difference of squares.  All sums are fp32.  Bound by the bytes of
+// the tensors.
+//
+// dw and db: a block keeps one slice index, walks a strided set of its rows and
+// sums them in the registers that hold its columns; the blocks' partial rows
+// are added up by a second launch in a fixed order, so the result does not
+// change from run to run.
+#include <cuda_bf16.h>
+
+#define SLSTM_FILE_ID 12
+#include "checked.cuh"
+#include "common.cuh"
+#include "launchers.h"
+
+namespace slstm {
+namespace {
+
+constexpr int LN_THREADS = 256;
+
+SLSTM_DEVINL float ln_f(float v) { return v; }
+SLSTM_DEVINL float ln_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+SLSTM_DEVINL void ln_put(float *p, float v) { *p = v; }
+SLSTM_DEVINL void ln_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+SLSTM_DEVINL void load8(const float *p, float (&v)[8])
+{
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x;
+    v[1] = a.y;
+    v[2] = a.z;
+    v[3] = a.w;
+    v[4] = b.x;
+    v[5] = b.y;
+    v[6] = b.z;
+    v[7] = b.w;
+}
+SLSTM_DEVINL void load8(const __nv_bfloat16 *p, float (&v)[8])
+{
+    const uint4 q = *reinterpret_cast<const uint4 *>(p);
+    const unsigned w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+SLSTM_DEVINL void store8(float *p, const float (&v)[8])
+{
+    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+SLSTM_DEVINL void store8(__nv_bfloat16 *p, const float (&v)[8])
+{
+    unsigned w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const unsigned *>(&r);
+    }
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Piece `i` of a slice's thread `t`: with VEC, 8 consecutive columns; without,
+// 8 columns TPR apart (so that the threads' single loads are consecutive).
+template <int TPR, bool VEC>
+SLSTM_DEVINL int ln_col(int t, int i, int e)
+{
+    return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
+}
+
+template <int TPR, int NV, bool VEC, typename T>
+SLSTM_DEVINL void ln_load(const T *p, int d, int t, float (&v)[NV][8])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (VEC) {
+            const int c = ln_col<TPR, VEC>(t, i, 0);
+            if (c < d) {
+                load8(p + c, v[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = ln_col<TPR, VEC>(t, i, e);
+                v[i][e] = c < d ? ln_f(p[c]) : 0.0f;
+            }
+        }
+    }
+}
+
+template <int TPR, int NV, bool VEC, typename T>
+SLSTM_DEVINL void ln_store(T *p, int d, int t, const float (&v)[NV][8])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (VEC) {
+            const int c = ln_col<TPR, VEC>(t, i, 0);
+            if (c < d) store8(p + c, v[i]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = ln_col<TPR, VEC>(t, i, e);
+                if (c < d) ln_put(p + c, v[i][e]);
+            }
+        }
+    }
+}
+
+// Sums of `a` and `b` over the TPR threads of a slice, to all of them.
+template <int TPR>
+SLSTM_DEVINL float2 ln_sum(float a, float b, float2 *red)
+{
+#pragma unroll
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    if (TPR <= 32) return make_float2(a, b);
+    constexpr int W = TPR / 32;
+    const int slot = threadIdx.x / TPR, w = (threadIdx.x % TPR) >> 5;
+    __syncthreads();   // the values of the last sum have been read
+    if ((threadIdx.x & 31) == 0) red[slot * W + w] = make_float2(a, b);
+    __syncthreads();
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const float2 r = red[slot * W + i];
+        s.x += r.x;
+        s.y += r.y;
+    }
+    return s;
+}
+
+template <int TPR>
+constexpr int ln_block()
+{
+    return TPR > LN_THREADS ? TPR : LN_THREADS;
+}
+
+template <typename TX, typename TY, int TPR, int NV, bool VEC>
+__global__ void __launch_bounds__(ln_block<TPR>())
+    ln_forward_kernel(const TX *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b, TY *y,
+                      float *mean, float *rstd, long long n, int groups, int d, float eps)
+{
+    constexpr int SLOTS = ln_block<TPR>() / TPR;
+    __shared__ float2 red[32];
+    const int t = threadIdx.x % TPR;
+    const long long r = (long long)blockIdx.x * SLOTS + threadIdx.x / TPR;
+    const bool on = r < n;
+    const long long at = (on ? r : 0) * d;
+    const int g0 = (int)((on ? r : 0) % groups) * d;
+    float v[NV][8];
+    ln_load<TPR, NV, VEC>(x + at, d, t, v);
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[i][e];
+    const float mu = ln_sum<TPR>(s, 0.0f, red).x / d;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[i][e] -= mu;
+            if (ln_col<TPR, VEC>(t, i, e) < d) q = fmaf(v[i][e], v[i][e], q);
+        }
+    const float rs = 1.0f / sqrtf(ln_sum<TPR>(q, 0.0f, red).x / d + eps);
+    if (!on) return;
+    if (t == 0) {
+        mean[r] = mu;
+        rstd[r] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        float wv[1][8], bv[1][8];
+        ln_load<TPR, 1, VEC>(w + g0 + i * TPR * 8, d - i * TPR * 8, t, wv);
+        if (b) ln_load<TPR, 1, VEC>(b + g0 + i * TPR * 8, d - i * TPR * 8, t, bv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[i][e] = v[i][e] * rs * wv[0][e];
+            if (b) v[i][e] += bv[0][e];
+        }
+    }
+    ln_store<TPR, NV, VEC>(y + at, d, t, v);
+}
+
+// part: [gridDim.x][2][groups d], the blocks' sums of dy xhat and dy.
+template <typename TX, typename TY, int TPR, int NV, bool VEC>
+__global__ void __launch_bounds__(ln_block<TPR>())
+    ln_backward_kernel(const TX *__restrict__ x, const float *__restrict__ w, const TY *__restrict__ dy,
+                       const float *__restrict__ mean, const float *__restrict__ rstd, TX *dx, float *part,
+                       long long rows, int groups, int d)
+{
+    constexpr int SLOTS = ln_block<TPR>() / TPR;
+    __shared__ float2 red[32];
+    __shared__ float join[SLOTS > 1 ? SLOTS : 1][SLOTS > 1 ? 8 * TPR : 1];
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int g = blockIdx.y;
+    float wv[NV][8], dw[NV][8], db[NV][8];
+    ln_load<TPR, NV, VEC>(w + (long long)g * d, d, t, wv);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
+    for (long long r0 = (long long)blockIdx.x * SLOTS; r0 < rows; r0 += (long long)gridDim.x * SLOTS) {
+        const long long r = r0 + slot;
+        const bool on = r < rows;
+        const long long n = (on ? r : 0) * groups + g;
+        float xv[NV][8], yv[NV][8];
+        ln_load<TPR, NV, VEC>(x + n * d, d, t, xv);
+        ln_load<TPR, NV, VEC>(dy + n * d, d, t, yv);
+        const float mu = mean[n], rs = rstd[n];
+        float sp = 0.0f, sx = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xh = (xv[i][e] - mu) * rs;
+                const float p = yv[i][e] * wv[i][e];   // 0 behind the slice: dy and w are
+                if (on) {
+                    dw[i][e] = fmaf(yv[i][e], xh, dw[i][e]);
+                    db[i][e] += yv[i][e];
+                }
+                sp += p;
+                sx = fmaf(p, xh, sx);
+                xv[i][e] = xh;
+                yv[i][e] = p;
+            }
+        const float2 s = ln_sum<TPR>(sp, sx, red);
+        const float mp = s.x / d, mx = s.y / d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xv[i][e] = rs * (yv[i][e] - mp - xv[i][e] * mx);
+        if (on) ln_store<TPR, NV, VEC>(dx + n * d, d, t, xv);
+    }
+    // the block's sums, its slots in order
+    float *pw = part + (long long)blockIdx.x * 2 * groups * d + (long long)g * d;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float(&v)[8] = z == 0 ? dw[i] : db[i];
+            if (SLOTS > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) join[slot][e * TPR + t] = v[e];
+                __syncthreads();
+                for (int j = threadIdx.x; j < 8 * TPR; j += ln_block<TPR>()) {
+                    float s = 0.0f;
+#pragma unroll 8
+                    for (int k = 0; k < SLOTS; ++k) s += join[k][j];
+                    const int c = ln_col<TPR, VEC>(j % TPR, i, j / TPR);
+                    if (c < d) pw[(long long)z * groups * d + c] = s;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int c = ln_col<TPR, VEC>(t, i, e);
+                    if (c < d) pw[(long long)z * groups * d + c] = v[e];
+                }
+            }
+        }
+    }
+}
+
+// out[c] = sum over k of part[k][c], c < 2 D (dw, then db): 32 columns and 8
+// strided shares of the partial rows a block, the shares in order.
+__global__ void __launch_bounds__(256) ln_reduce_kernel(const float *__restrict__ part, float *dw, float *db, int nb,
+                                                        long long D)
+{
+    __shared__ float s[8][33];
+    const long long c = (long long)blockIdx.x * 32 + (threadIdx.x & 31);
+    const int y = threadIdx.x >> 5;
+    float v = 0.0f;
+    if (c < 2 * D)
+#pragma unroll 8
+        for (int k = y; k < nb; k += 8) v += part[k * 2 * D + c];
+    s[y][threadIdx.x & 31] = v;
+    __syncthreads();
+    if (y == 0 && c < 2 * D) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
+        if (c < D) dw[c] = v;
+        else db[c - D] = v;
+    }
+}
+
+bool vec_ok(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Blocks that share the rows of one slice index in the backward pass: a few for
+// every SM over all slice indices, so that the partial rows stay small beside
+// the tensors.
+int backward_blocks(long long rows, int groups, int slots)
+{
+    const long long want = max((148LL * 4 + groups - 1) / groups, 1LL);
+    return (int)min(want, (rows + slots - 1) / slots);
+}
+
+// The threads and pieces of a slice of d columns: the least registers that
+// hold it.
+#define LN_DISPATCH(F)                                   \
+    (d <= 64     ? F<TX, TY, 8, 1, V>(a)                 \
+     : d <= 128  ? F<TX, TY, 16, 1, V>(a)                \
+     : d <= 256  ? F<TX, TY, 32, 1, V>(a)                \
+     : d <= 512  ? F<TX, TY, 32, 2, V>(a)                \
+     : d <= 1024 ? F<TX, TY, 128, 1, V>(a)               \
+     : d <= 2048 ? F<TX, TY, 256, 1, V>(a)               \
+     : d <= 4096 ? F<TX, TY, 256, 2, V>(a)               \
+     : d <= 8192 ? F<TX, TY, 1024, 1, V>(a)              \
+                 : F<TX, TY, 1024, 2, V>(a))
+
+struct LnArgs {
+    const void *x, *dy;
+    const float *w, *b, *mean_in, *rstd_in;
+    void *y, *dx;
+    float *mean, *rstd, *dw, *db, *part;
+    long long rows;
+    int groups, d;
+    float eps;
+    cudaStream_t st;
+};
+
+template <typename TX, typename TY, int TPR, int NV, bool VEC>
+cudaError_t ln_fwd(const LnArgs &a)
+{
+    constexpr int SLOTS = ln_block<TPR>() / TPR;
+    const long long n = a.rows * a.groups;
+    ln_forward_kernel<TX, TY, TPR, NV, VEC><<<(unsigned)((n + SLOTS - 1) / SLOTS), ln_block<TPR>(), 0, a.st>>>(
+        static_cast<const TX *>(a.x), a.w, a.b, static_cast<TY *>(a.y), a.mean, a.rstd, n, a.groups, a.d, a.eps);
+    return cudaGetLastError();
+}
+
+template <typename TX, typename TY, int TPR, int NV, bool VEC>
+cudaError_t ln_bwd(const LnArgs &a)
+{
+    constexpr int SLOTS = ln_block<TPR>() / TPR;
+    const int nb = backward_blocks(a.rows, a.groups, SLOTS);
+    ln_backward_kernel<TX, TY, TPR, NV, VEC><<<dim3(nb, a.groups), ln_block<TPR>(), 0, a.st>>>(
+        static_cast<const TX *>(a.x), a.w, static_cast<const TY *>(a.dy), a.mean_in, a.rstd_in,
+        static_cast<TX *>(a.dx), a.part, a.rows, a.groups, a.d);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long D = (long long)a.groups * a.d;
+    ln_reduce_kernel<<<(unsigned)((2 * D + 31) / 32), 256, 0, a.st>>>(a.part, a.dw, a.db, nb, D);
+    return cudaGetLastError();
+}
+
+template <typename TX, typename TY, bool V>
+cudaError_t ln_fwd_d(const LnArgs &a)
+{
+    const int d = a.d;
+    return LN_DISPATCH(ln_fwd);
+}
+template <typename TX, typename TY, bool V>
+cudaError_t ln_bwd_d(const LnArgs &a)
+{
+    const int d = a.d;
+    return LN_DISPATCH(ln_bwd);
+}
+
+}  // namespace
+
+size_t layer_norm_workspace_bytes(long long rows, int groups, int d)
+{
+    return (size_t)backward_blocks(rows, groups, 1) * 2 * groups * d * 4;
+}
+
+cudaError_t layer_norm_forward(const void *x, int x_dtype, const float *w, const float *b, void *y, int y_dtype,
+                               float *mean, float *rstd, long long rows, int groups, int d, float eps, cudaStream_t st)
+{
+    LnArgs a{};
+    a.x = x;
+    a.w = w;
+    a.b = b;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.rows = rows;
+    a.groups = groups;
+    a.d = d;
+    a.eps = eps;
+    a.st = st;
+    const bool v = d % 8 == 0 && vec_ok(x) && vec_ok(w) && vec_ok(y) && (b == nullptr || vec_ok(b));
+    const bool xf = x_dtype == SLSTM_F32, yf = y_dtype == SLSTM_F32;
+    typedef __nv_bfloat16 h;
+    if (xf && yf) return v ? ln_fwd_d<float, float, true>(a) : ln_fwd_d<float, float, false>(a);
+    if (xf) return v ? ln_fwd_d<float, h, true>(a) : ln_fwd_d<float, h, false>(a);
+    if (yf) return v ? ln_fwd_d<h, float, true>(a) : ln_fwd_d<h, float, false>(a);
+    return v ? ln_fwd_d<h, h, true>(a) : ln_fwd_d<h, h, false>(a);
+}
+
+cudaError_t layer_norm_backward(const void *x, int x_dtype, const float *w, const void *dy, int y_dtype,
+                                const float *mean, const float *rstd, void *dx, float *dw, float *db, long long rows,
+                                int groups, int d, void *ws, cudaStream_t st)
+{
+    LnArgs a{};
+    a.x = x;
+    a.w = w;
+    a.dy = dy;
+    a.mean_in = mean;
+    a.rstd_in = rstd;
+    a.dx = dx;
+    a.dw = dw;
+    a.db = db;
+    a.part = static_cast<float *>(ws);
+    a.rows = rows;
+    a.groups = groups;
+    a.d = d;
+    a.st = st;
+    const bool v = d % 8 == 0 && vec_ok(x) && vec_ok(w) && vec_ok(dy) && vec_ok(dx);
+    const bool xf = x_dtype == SLSTM_F32, yf = y_dtype == SLSTM_F32;
+    typedef __nv_bfloat16 h;
+    if (xf && yf) return v ? ln_bwd_d<float, float, true>(a) : ln_bwd_d<float, float, false>(a);
+    if (xf) return v ? ln_bwd_d<float, h, true>(a) : ln_bwd_d<float, h, false>(a);
+    if (yf) return v ? ln_bwd_d<h, float, true>(a) : ln_bwd_d<h, float, false>(a);
+    return v ? ln_bwd_d<h, h, true>(a) : ln_bwd_d<h, h, false>(a);
+}
+
+}  // namespace slstm

@@ -1,0 +1,768 @@
+// Linear attention with a decay for each head, on the CUDA cores: every size,
+// fp32 and bf16, dense and packed; the step of single tokens; and the small
+// kernels that the tensor-core path (linear_attention_tc.cu) shares.
+//
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// Over a chunk of C rows, with c_i the sum of the log decays up to row i:
+//   o_i     = scale (sum_{j<=i} D_ij (q_i . k_j) v_j + e^{c_i} S_n^T q_i),  D_ij = e^{c_i - c_j}
+//   S_{n+1} = e^{c_C} S_n + sum_j e^{c_C - c_j} k_j v_j^T
+// so three launches do it, all parallel over chunks but the second: what each
+// chunk adds to the state, the scan of the states over the chunks (one thread
+// for each state element), and the outputs.  The backward pass runs the same
+// first two launches on (q, dO) from the end for dS and one more for the rest:
+//   dq_i = scale (sum_j D_ij (dO_i . v_j) k_j + e^{c_i} S_n dO_i)
+//   dk_j = scale sum_i D_ij (dO_i . v_j) q_i + e^{c_C - c_j} dS_{n+1} v_j
+//   dv_j = scale sum_i D_ij (q_i . k_j) dO_i + e^{c_C - c_j} dS_{n+1}^T k_j
+//   dg_t = sum_{i>=t>j} W_ij + sum_{i>=t} u_i + sum_{j<t} w_j + e^{c_C} <S_n, dS_{n+1}>
+// with W_ij = scale D_ij (q_i . k_j)(dO_i . v_j), u_i = q_i . (the state part of
+// dq_i), w_j = k_j . (the state part of dk_j).  dg is put together inside its
+// chunk: the sum of q . dq - k . dk over all later rows is the same number, but
+// cancels over the whole row and keeps little of it.
+//
+// All products are fp32 fused multiply-adds over 64 x 64 tiles (8 x 4 for each
+// of 128 threads); fp32 in, fp32 out needs that, and sizes that are no multiple
+// of 8 come here too.  Bound: the FMA pipes.
+#include <cuda_bf16.h>
+
+#define SLSTM_FILE_ID 11
+#include "checked.cuh"
+#include "la.cuh"
+#include "launchers.h"
+
+namespace slstm {
+namespace {
+
+constexpr int LC = 64;        // rows of a chunk
+constexpr int KB = 32;        // depth of the tiles in shared memory
+constexpr int LDT = 68;       // padded row of a tile (floats)
+constexpr int NT = 128;
+
+SLSTM_DEVINL float to_f(float v) { return v; }
+SLSTM_DEVINL float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+SLSTM_DEVINL void put(float *p, float v) { *p = v; }
+SLSTM_DEVINL void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// An operand of a 64 x 64 product: element (m, k) at p[m sm + k sk] for
+// m < nm, k < nk, zero outside, times coef[k] where given.
+template <typename T>
+struct Op {
+    const T *p;
+    long long sm, sk;
+    int nm, nk;
+    const float *coef;
+};
+
+template <typename T>
+SLSTM_DEVINL void load_tile(float *dst, const Op<T> &a, int k0)
+{
+    const int t = threadIdx.x;
+    if (a.sk == 1) {   // k is contiguous
+#pragma unroll 4
+        for (int i = t; i < 64 * KB; i += NT) {
+            const int m = i / KB, k = i % KB;
+            float v = 0.0f;
+            if (m < a.nm && k0 + k < a.nk) {
+                v = to_f(a.p[m * a.sm + (k0 + k)]);
+                if (a.coef) v *= a.coef[k0 + k];
+            }
+            dst[k * LDT + m] = v;
+        }
+    } else {
+#pragma unroll 4
+        for (int i = t; i < 64 * KB; i += NT) {
+            const int m = i % 64, k = i / 64;
+            float v = 0.0f;
+            if (m < a.nm && k0 + k < a.nk) {
+                v = to_f(a.p[m * a.sm + (k0 + k) * a.sk]);
+                if (a.coef) v *= a.coef[k0 + k];
+            }
+            dst[k * LDT + m] = v;
+        }
+    }
+}
+
+// acc += A B^T over k < K: thread (ty, tx) = (t / 16, t % 16) holds rows
+// 8 ty .. and columns 4 tx ...
+template <typename TA, typename TB>
+SLSTM_DEVINL void product(float (&acc)[8][4], const Op<TA> &A, const Op<TB> &B, int K, float *sA, float *sB)
+{
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    for (int k0 = 0; k0 < K; k0 += KB) {
+        __syncthreads();
+        load_tile(sA, A, k0);
+        load_tile(sB, B, k0);
+        __syncthreads();
+#pragma unroll 8
+        for (int k = 0; k < KB; ++k) {
+            const float4 a0 = *reinterpret_cast<const float4 *>(sA + k * LDT + ty * 8);
+            const float4 a1 = *reinterpret_cast<const float4 *>(sA + k * LDT + ty * 8 + 4);
+            const float4 b = *reinterpret_cast<const float4 *>(sB + k * LDT + tx * 4);
+            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            const float bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        }
+    }
+}
+
+SLSTM_DEVINL void clear(float (&acc)[8][4])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+}
+
+struct Decays {
+    double cum[LC];
+    int first[LC];
+    float row[LC], col[LC];
+    float tot;
+};
+
+SLSTM_DEVINL void chunk_decays(Decays &d, const LaArgs &a, const LaChunk &c, int h)
+{
+    if (threadIdx.x < 32)
+        la_decays<LC / 32>(a.g, a.per_head ? h : c.row * a.H + h, a.per_head ? 0 : a.H, c.len, threadIdx.x, d.cum,
+                           d.first, d.row, d.col, &d.tot);
+    __syncthreads();
+}
+
+// e^{c_i - c_j} for j <= i < len of one run between clears, else 0.
+SLSTM_DEVINL float decay_ij(const Decays &d, int i, int j, int len)
+{
+    return (j <= i && i < len && j >= d.first[i]) ? exp2f((float)(d.cum[i] - d.cum[j])) : 0.0f;
+}
+
+// What a chunk adds to the state: out[c][h] (d_k x d_v) = sum_j w_j X_j Y_j^T,
+// with X = k, Y = v, w = e^{c_C - c_j} forward, or X = q, Y = dO,
+// w = scale e^{c_i} from the end.
+template <typename T>
+__global__ void __launch_bounds__(NT) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
+{
+    __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
+    __shared__ Decays d;
+    __shared__ float w[LC];
+    const int c = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const LaChunk ck = la_chunk(ch, c);
+    if (ck.len <= 0) return;
+    const int m0 = blockIdx.y * 64, n0 = blockIdx.z * 64;
+    chunk_decays(d, a, ck, h);
+    if (threadIdx.x < LC) w[threadIdx.x] = back ? a.scale * d.row[threadIdx.x] : d.col[threadIdx.x];
+    if (threadIdx.x == 0 && m0 == 0 && n0 == 0) tot[(long long)c * a.H + h] = d.tot;
+    const int hq = h / (a.H / a.Hqk);
+    const long long ldx = back ? a.ldq : a.ldk, ldy = back ? (long long)a.H * a.dv : a.ldv;
+    const T *X = static_cast<const T *>(back ? a.q : a.k) + ck.row * ldx + (long long)hq * a.dk + m0;
+    const T *Y = static_cast<const T *>(back ? a.dO : a.v) + ck.row * ldy + (long long)h * a.dv + n0;
+    float acc[8][4];
+    clear(acc);
+    product(acc, Op<T>{X, 1, ldx, a.dk - m0, ck.len, w}, Op<T>{Y, 1, ldy, a.dv - n0, ck.len, nullptr}, ck.len, sA, sB);
+    float *dst = out + ((long long)c * a.H + h) * a.dk * a.dv;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int m = m0 + ty * 8 + i, n = n0 + tx * 4 + j;
+            if (m < a.dk && n < a.dv) dst[(long long)m * a.dv + n] = acc[i][j];
+        }
+}
+
+// The states over the chunks of each sequence, one thread for an element: the
+// deltas in `buf` give way to the state that enters each chunk (forward) or the
+// gradient of the state that leaves it (back).  first: s0 or dsT (null: zero);
+// last: sT or ds0 (may be null).  Bound by the bytes of buf, read and written
+// once; eight chunks are loaded ahead of the eight that are being joined.
+__global__ void __launch_bounds__(256) la_scan_kernel(LaChunks ch, int H, int E, bool back, float *buf,
+                                                      const float *__restrict__ tot, const float *first, float *last)
+{
+    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int seq = blockIdx.x / H, h = blockIdx.x % H;
+    if (e >= E) return;
+    const int c0 = ch.pos ? ch.coff[seq] : seq * ch.nc;
+    const int n = ch.pos ? ch.coff[seq + 1] - c0 : ch.nc;
+    const long long at = ((long long)seq * H + h) * E + e;
+    float s = first ? first[at] : 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 8) {
+        float dl[8], tt[8];
+        const int m = min(8, n - i0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= m) break;
+            const long long c = back ? c0 + n - 1 - (i0 + i) : c0 + i0 + i;
+            dl[i] = buf[(c * H + h) * E + e];
+            tt[i] = tot[c * H + h];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i >= m) break;
+            const long long c = back ? c0 + n - 1 - (i0 + i) : c0 + i0 + i;
+            buf[(c * H + h) * E + e] = s;
+            s = fmaf(tt[i], s, dl[i]);
+        }
+    }
+    if (last) last[at] = s;
+}
+
+// The outputs of a chunk and head.
+template <typename T>
+__global__ void __launch_bounds__(NT) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
+{
+    __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
+    __shared__ float P[LC][LC + 1];
+    __shared__ Decays d;
+    const int c = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const LaChunk ck = la_chunk(ch, c);
+    if (ck.len <= 0) return;
+    chunk_decays(d, a, ck, h);
+    const int hq = h / (a.H / a.Hqk);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const T *q = static_cast<const T *>(a.q) + ck.row * a.ldq + (long long)hq * a.dk;
+    const T *k = static_cast<const T *>(a.k) + ck.row * a.ldk + (long long)hq * a.dk;
+    const T *v = static_cast<const T *>(a.v) + ck.row * a.ldv + (long long)h * a.dv;
+    const float *S = states + ((long long)c * a.H + h) * a.dk * a.dv;
+    T *o = static_cast<T *>(a.o) + ck.row * (long long)a.H * a.dv + (long long)h * a.dv;
+    float acc[8][4];
+    clear(acc);
+    product(acc, Op<T>{q, a.ldq, 1, ck.len, a.dk, nullptr}, Op<T>{k, a.ldk, 1, ck.len, a.dk, nullptr}, a.dk, sA, sB);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = ty * 8 + i, s = tx * 4 + j;
+            const float w = decay_ij(d, r, s, ck.len);
+            P[r][s] = w == 0.0f ? 0.0f : acc[i][j] * w;
+        }
+    for (int n0 = 0; n0 < a.dv; n0 += 64) {
+        clear(acc);
+        product(acc, Op<T>{q, a.ldq, 1, ck.len, a.dk, nullptr}, Op<float>{S + n0, 1, a.dv, a.dv - n0, a.dk, nullptr},
+                a.dk, sA, sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float r = d.row[ty * 8 + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] *= r;
+        }
+        product(acc, Op<float>{&P[0][0], LC + 1, 1, LC, ck.len, nullptr},
+                Op<T>{v + n0, 1, a.ldv, a.dv - n0, ck.len, nullptr}, ck.len, sA, sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                if (r < ck.len && n < a.dv) put(o + (long long)r * a.H * a.dv + n, acc[i][j] * a.scale);
+            }
+    }
+}
+
+// Sum over the 16 threads that share rows (half a warp).
+SLSTM_DEVINL float sum16(float v)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+struct BackShared {
+    float sA[KB * LDT], sB[KB * LDT];
+    float P[LC][LC + 1], Pd[LC][LC + 1];
+    float r[LC], u[LC], w[LC];
+    float cs[8][LC];      // column sums of W of each thread row
+    float red[NT / 32];
+    Decays d;
+};
+
+// The gradients of a chunk and head.  part_q, part_k: [row][h][d_k] fp32 where
+// heads share a query and key head; dgc: the chunk's sum of dg, [c][h], where
+// the decay belongs to the head.
+template <typename T>
+__global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states,
+                                                     const float *__restrict__ dstates, float *part_q, float *part_k,
+                                                     float *dgc)
+{
+    extern __shared__ __align__(16) char smem[];
+    BackShared &s = *reinterpret_cast<BackShared *>(smem);
+    const int c = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const LaChunk ck = la_chunk(ch, c);
+    if (ck.len <= 0) return;
+    chunk_decays(s.d, a, ck, h);
+    const int len = ck.len;
+    const int hq = h / (a.H / a.Hqk);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const long long ldo = (long long)a.H * a.dv;
+    const T *q = static_cast<const T *>(a.q) + ck.row * a.ldq + (long long)hq * a.dk;
+    const T *k = static_cast<const T *>(a.k) + ck.row * a.ldk + (long long)hq * a.dk;
+    const T *v = static_cast<const T *>(a.v) + ck.row * a.ldv + (long long)h * a.dv;
+    const T *g = static_cast<const T *>(a.dO) + ck.row * ldo + (long long)h * a.dv;
+    const float *S = states + ((long long)c * a.H + h) * a.dk * a.dv;
+    const float *dS = dstates + ((long long)c * a.H + h) * a.dk * a.dv;
+    for (int i = threadIdx.x; i < LC; i += NT) s.u[i] = s.w[i] = 0.0f;
+
+    // D (q k) and scale D (dO v), their products' sums over rows and columns
+    float p[8][4], t[8][4];
+    clear(p);
+    clear(t);
+    product(p, Op<T>{q, a.ldq, 1, len, a.dk, nullptr}, Op<T>{k, a.ldk, 1, len, a.dk, nullptr}, a.dk, s.sA, s.sB);
+    product(t, Op<T>{g, ldo, 1, len, a.dv, nullptr}, Op<T>{v, a.ldv, 1, len, a.dv, nullptr}, a.dv, s.sA, s.sB);
+    float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float rs = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = ty * 8 + i, m = tx * 4 + j;
+            const float w = a.scale * decay_ij(s.d, r, m, len);
+            const float P = w == 0.0f ? 0.0f : w * p[i][j], Pd = w == 0.0f ? 0.0f : w * t[i][j];
+            s.P[r][m] = P;
+            s.Pd[r][m] = Pd;
+            const float W = r > m && w != 0.0f ? P * t[i][j] : 0.0f;
+            rs += W;
+            cs[j] += W;
+        }
+        rs = sum16(rs);
+        if (tx == 0) s.r[ty * 8 + i] = rs;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.cs[ty][tx * 4 + j] = cs[j];
+
+    for (int n0 = 0; n0 < a.dk; n0 += 64) {
+        clear(p);
+        product(p, Op<T>{g, ldo, 1, len, a.dv, nullptr},
+                Op<float>{S + (long long)n0 * a.dv, a.dv, 1, a.dk - n0, a.dv, nullptr}, a.dv, s.sA, s.sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty * 8 + i;
+            const float f = a.scale * s.d.row[r];
+            float u = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + tx * 4 + j;
+                p[i][j] *= f;
+                if (r < len && n < a.dk) u = fmaf(to_f(q[r * a.ldq + n]), p[i][j], u);
+            }
+            u = sum16(u);
+            if (tx == 0) s.u[r] += u;
+        }
+        product(p, Op<float>{&s.Pd[0][0], LC + 1, 1, LC, len, nullptr},
+                Op<T>{k + n0, 1, a.ldk, a.dk - n0, len, nullptr}, len, s.sA, s.sB);
+        clear(t);
+        product(t, Op<T>{v, a.ldv, 1, len, a.dv, nullptr},
+                Op<float>{dS + (long long)n0 * a.dv, a.dv, 1, a.dk - n0, a.dv, nullptr}, a.dv, s.sA, s.sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = ty * 8 + i;
+            const float f = s.d.col[r];
+            float w = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = n0 + tx * 4 + j;
+                t[i][j] *= f;
+                if (r < len && n < a.dk) w = fmaf(to_f(k[r * a.ldk + n]), t[i][j], w);
+            }
+            w = sum16(w);
+            if (tx == 0) s.w[r] += w;
+        }
+        product(t, Op<float>{&s.Pd[0][0], 1, LC + 1, LC, len, nullptr},
+                Op<T>{q + n0, 1, a.ldq, a.dk - n0, len, nullptr}, len, s.sA, s.sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                if (r >= len || n >= a.dk) continue;
+                if (part_q) {
+                    const long long at = ((ck.row + r) * a.H + h) * a.dk + n;
+                    part_q[at] = p[i][j];
+                    part_k[at] = t[i][j];
+                } else {
+                    const long long at = ((ck.row + r) * a.Hqk + hq) * a.dk + n;
+                    put(static_cast<T *>(a.dq) + at, p[i][j]);
+                    put(static_cast<T *>(a.dk_) + at, t[i][j]);
+                }
+            }
+    }
+    for (int n0 = 0; n0 < a.dv; n0 += 64) {
+        clear(t);
+        product(t, Op<T>{k, a.ldk, 1, len, a.dk, nullptr}, Op<float>{dS + n0, 1, a.dv, a.dv - n0, a.dk, nullptr}, a.dk,
+                s.sA, s.sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = s.d.col[ty * 8 + i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[i][j] *= f;
+        }
+        product(t, Op<float>{&s.P[0][0], 1, LC + 1, LC, len, nullptr},
+                Op<T>{g + n0, 1, ldo, a.dv - n0, len, nullptr}, len, s.sA, s.sB);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                if (r < len && n < a.dv)
+                    put(static_cast<T *>(a.dv_) + (ck.row + r) * ldo + (long long)h * a.dv + n, t[i][j]);
+            }
+    }
+    if (a.dg == nullptr) return;
+    // <S_n, dS_{n+1}>, then dg by one warp
+    float dot = 0.0f;
+    for (int i = threadIdx.x; i < a.dk * a.dv; i += NT) dot = fmaf(S[i], dS[i], dot);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    const int lane = threadIdx.x;
+    dot = (s.red[0] + s.red[1] + s.red[2] + s.red[3]) * s.d.tot;
+    // two rows a lane; sums of up to 64 terms, in 64 bits: they cancel
+    double x[2], w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = lane * 2 + i;
+        double col = 0.0;
+        for (int y = 0; y < 8; ++y) col += s.cs[y][r];
+        x[i] = (double)s.r[r] + s.u[r] - col;
+        w[i] = s.w[r];
+    }
+    double xs = x[0] + x[1], ws = w[0] + w[1];
+    const double xl = xs, wl = ws;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double xu = __shfl_down_sync(0xffffffffu, xs, o), wu = __shfl_up_sync(0xffffffffu, ws, o);
+        if (lane + o < 32) xs += xu;
+        if (lane >= o) ws += wu;
+    }
+    const double xa = xs - xl, wb = ws - wl;   // rows behind, rows before this lane's
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = lane * 2 + i;
+        float dgv = (float)(xa + (i == 0 ? x[0] + x[1] : x[1]) + wb + (i == 0 ? 0.0 : w[0]) + (double)dot);
+        if (r >= len || s.d.first[r] == r) dgv = 0.0f;   // nothing passes a row that clears the state
+        if (r < len && !a.per_head) a.dg[(ck.row + r) * a.H + h] = dgv;
+        sum += dgv;
+    }
+    if (a.per_head) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) dgc[(long long)c * a.H + h] = sum;
+    }
+}
+
+// One thread for each element of dq or dk.
+template <typename T>
+__global__ void __launch_bounds__(256) la_share_kernel(const float *__restrict__ part, T *out, LaChunks ch,
+                                                       long long rows, int Hqk, int rep, int dk)
+{
+    // packed: the rows of the sequences only
+    const long long w = (long long)Hqk * dk, i0 = ch.pos ? ch.pos[0] * w : 0;
+    const long long n = ch.pos ? ch.pos[ch.n_seq] * w : rows * w;
+    for (long long i = i0 + (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+        const int d = (int)(i % dk);
+        const long long rh = i / dk;   // row * Hqk + hq
+        float s = 0.0f;
+        for (int r = 0; r < rep; ++r) s += part[(rh * rep + r) * dk + d];
+        put(out + i, s);
+    }
+}
+
+__global__ void __launch_bounds__(256) la_head_sum_kernel(const float *__restrict__ part, float *dg, LaChunks ch,
+                                                          int H)
+{
+    __shared__ double red[8];
+    const int h = blockIdx.x;
+    const int n = ch.pos ? ch.coff[ch.n_seq] : ch.total;
+    double s = 0.0;
+    for (int c = threadIdx.x; c < n; c += 256) s += part[(long long)c * H + h];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) s += red[w];
+        dg[h] = (float)s;
+    }
+}
+
+// The table of packed sequences: offsets clamped into [0, T] and raised to the
+// largest before them, and the chunks before each sequence.  One block, 1024
+// offsets at a time.
+__global__ void __launch_bounds__(1024) la_table_kernel(const int *__restrict__ cu, int n_seq, int T, int C, int *pos,
+                                                        int *coff)
+{
+    __shared__ int wm[32], ws[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int top = 0, sum = 0;   // the largest offset, and the chunks, of the tiles before
+    for (int k0 = 0; k0 <= n_seq; k0 += 1024) {
+        const int k = k0 + threadIdx.x;
+        int m = k <= n_seq ? min(max(cu[k], 0), T) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, m, o);
+            if (lane >= o) m = max(m, u);
+        }
+        if (lane == 31) wm[warp] = m;
+        __syncthreads();
+        int before = top;
+        for (int w = 0; w < warp; ++w) before = max(before, wm[w]);
+        m = max(m, before);
+        int prev = __shfl_up_sync(0xffffffffu, m, 1);
+        if (lane == 0) prev = before;
+        for (int w = 0; w < 32; ++w) top = max(top, wm[w]);
+        // chunks of sequence k - 1, which ends at offset k
+        int n = k >= 1 && k <= n_seq ? (m - prev + C - 1) / C : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, n, o);
+            if (lane >= o) n += u;
+        }
+        if (lane == 31) ws[warp] = n;
+        __syncthreads();
+        int off = sum;
+        for (int w = 0; w < warp; ++w) off += ws[w];
+        if (k <= n_seq) {
+            pos[k] = m;
+            coff[k] = off + n;
+        }
+        for (int w = 0; w < 32; ++w) sum += ws[w];
+        __syncthreads();
+    }
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t la_table_bytes(const LaArgs &a) { return a.cu ? 2 * up256(4 * ((size_t)a.B + 1)) : 0; }
+
+int la_chunk_bound(const LaArgs &a, int C)
+{
+    return a.cu ? a.T / C + a.B : a.B * ((a.T + C - 1) / C);
+}
+
+cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st)
+{
+    *out = LaChunks{a.B, a.T, C, (a.T + C - 1) / C, la_chunk_bound(a, C), nullptr, nullptr};
+    if (a.cu == nullptr) return cudaSuccess;
+    int *pos = static_cast<int *>(mem);
+    int *coff = reinterpret_cast<int *>(static_cast<char *>(mem) + up256(4 * ((size_t)a.B + 1)));
+    la_table_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.T, C, pos, coff);
+    out->pos = pos;
+    out->coff = coff;
+    return cudaGetLastError();
+}
+
+cudaError_t la_share_sum(const float *part, void *out, int dtype, const LaChunks &ch, const LaArgs &a, cudaStream_t st)
+{
+    const long long rows = a.cu ? a.T : (long long)a.B * a.T;
+    const long long n = rows * a.Hqk * a.dk;
+    const int blocks = (int)min((n + 255) / 256, (long long)148 * 32);
+    if (dtype == SLSTM_F32)
+        la_share_kernel<<<blocks, 256, 0, st>>>(part, static_cast<float *>(out), ch, rows, a.Hqk, a.H / a.Hqk, a.dk);
+    else
+        la_share_kernel<<<blocks, 256, 0, st>>>(part, static_cast<__nv_bfloat16 *>(out), ch, rows, a.Hqk,
+                                                a.H / a.Hqk, a.dk);
+    return cudaGetLastError();
+}
+
+cudaError_t la_head_sum(const float *part, float *dg, const LaChunks &ch, int H, cudaStream_t st)
+{
+    la_head_sum_kernel<<<H, 256, 0, st>>>(part, dg, ch, H);
+    return cudaGetLastError();
+}
+
+namespace {
+
+struct SimtWs {
+    char *table;
+    float *S, *totS, *dS, *totD, *pq, *pk, *dgc;
+    size_t bytes;
+};
+
+SimtWs simt_layout(const LaArgs &a, bool backward, void *ws)
+{
+    SimtWs w{};
+    char *p = static_cast<char *>(ws);
+    const size_t nc = (size_t)la_chunk_bound(a, LC), E = (size_t)a.dk * a.dv;
+    const size_t rows = a.cu ? (size_t)a.T : (size_t)a.B * a.T;
+    auto take = [&](size_t bytes) {
+        char *r = p;
+        p += up256(bytes);
+        return r;
+    };
+    w.table = take(la_table_bytes(a));
+    w.S = reinterpret_cast<float *>(take(4 * nc * a.H * E));
+    w.totS = reinterpret_cast<float *>(take(4 * nc * a.H));
+    if (backward) {
+        w.dS = reinterpret_cast<float *>(take(4 * nc * a.H * E));
+        w.totD = reinterpret_cast<float *>(take(4 * nc * a.H));
+        w.dgc = reinterpret_cast<float *>(take(4 * nc * a.H));
+        if (a.H != a.Hqk) {
+            w.pq = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
+            w.pk = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
+        }
+    }
+    w.bytes = (size_t)(p - static_cast<char *>(ws));
+    return w;
+}
+
+template <typename T>
+cudaError_t states(const LaArgs &a, const LaChunks &ch, bool back, float *buf, float *tot, cudaStream_t st)
+{
+    const int E = a.dk * a.dv;
+    const dim3 grid((unsigned)ch.total * a.H, (a.dk + 63) / 64, (a.dv + 63) / 64);
+    la_delta_kernel<T><<<grid, NT, 0, st>>>(a, ch, back, buf, tot);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    la_scan_kernel<<<dim3((unsigned)a.B * a.H, (E + 255) / 256), 256, 0, st>>>(ch, a.H, E, back, buf, tot,
+                                                                             back ? a.dsT : a.s0, back ? a.ds0 : a.sT);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t forward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    const SimtWs w = simt_layout(a, false, ws);
+    LaChunks ch;
+    cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
+    if (e == cudaSuccess) e = states<T>(a, ch, false, w.S, w.totS, st);
+    if (e != cudaSuccess) return e;
+    la_out_kernel<T><<<(unsigned)ch.total * a.H, NT, 0, st>>>(a, ch, w.S);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t backward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    const SimtWs w = simt_layout(a, true, ws);
+    LaChunks ch;
+    cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
+    if (e == cudaSuccess) e = states<T>(a, ch, false, w.S, w.totS, st);
+    if (e == cudaSuccess) e = states<T>(a, ch, true, w.dS, w.totD, st);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(la_back_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)sizeof(BackShared));
+    if (e != cudaSuccess) return e;
+    la_back_kernel<T><<<(unsigned)ch.total * a.H, NT, sizeof(BackShared), st>>>(a, ch, w.S, w.dS, w.pq, w.pk, w.dgc);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, a.dq, a.dtype, ch, a, st);
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pk, a.dk_, a.dtype, ch, a, st);
+    if (e == cudaSuccess && a.dg && a.per_head) e = la_head_sum(w.dgc, a.dg, ch, a.H, st);
+    return e;
+}
+
+}  // namespace
+
+size_t la_simt_workspace(const LaArgs &a, bool backward)
+{
+    return simt_layout(a, backward, reinterpret_cast<void *>((uintptr_t)256)).bytes;
+}
+
+cudaError_t la_simt_forward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    return a.dtype == SLSTM_F32 ? forward<float>(a, ws, st) : forward<__nv_bfloat16>(a, ws, st);
+}
+
+cudaError_t la_simt_backward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    return a.dtype == SLSTM_F32 ? backward<float>(a, ws, st) : backward<__nv_bfloat16>(a, ws, st);
+}
+
+// ---------------------------------------------------------------------------
+// the step of single tokens
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int STEP_WARPS = 8;
+
+// A block takes COLS columns of one state: LPR lanes hold a row of them (VEC
+// columns each), the warps walk the rows, and the partial products with q meet
+// in shared memory.  The state is read once and written once, in 16-byte
+// pieces; s_next may be s_prev, as each element is read and written by one
+// thread.  Bound by those bytes.
+template <typename T, int COLS, int VEC>
+__global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, const float *s_prev, float *s_next)
+{
+    constexpr int LPR = COLS / VEC;                     // lanes of a row
+    constexpr int RPW = 32 / LPR;                       // rows a warp takes at once
+    constexpr int ROWS = STEP_WARPS * RPW;
+    __shared__ float red[ROWS][COLS];
+    const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, hq = h / (a.H / a.Hqk);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.y * COLS + (lane % LPR) * VEC;
+    const int slot = warp * RPW + lane / LPR;
+    const T *q = static_cast<const T *>(a.q) + b * a.ldq + (long long)hq * a.dk;
+    const T *k = static_cast<const T *>(a.k) + b * a.ldk + (long long)hq * a.dk;
+    const T *v = static_cast<const T *>(a.v) + b * a.ldv + (long long)h * a.dv;
+    const float decay = expf(a.g[a.per_head ? h : (long long)b * a.H + h]);
+    const long long base = ((long long)b * a.H + h) * a.dk * a.dv;
+    float o[VEC], vv[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        o[i] = 0.0f;
+        vv[i] = col + i < a.dv ? to_f(v[col + i]) : 0.0f;
+    }
+    if (col < a.dv) {
+#pragma unroll 8
+        for (int r = slot; r < a.dk; r += ROWS) {
+            const float kr = to_f(k[r]), qr = to_f(q[r]);
+            const long long at = base + (long long)r * a.dv + col;
+            float s[VEC];
+            if (VEC == 4) {
+                const float4 f = s_prev ? *reinterpret_cast<const float4 *>(s_prev + at) : make_float4(0, 0, 0, 0);
+                s[0] = f.x;
+                s[VEC > 1 ? 1 : 0] = f.y;
+                s[VEC > 2 ? 2 : 0] = f.z;
+                s[VEC > 3 ? 3 : 0] = f.w;
+            } else {
+                s[0] = s_prev ? s_prev[at] : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s[i] = fmaf(decay, s[i], kr * vv[i]);
+                o[i] = fmaf(qr, s[i], o[i]);
+            }
+            if (VEC == 4)
+                *reinterpret_cast<float4 *>(s_next + at) =
+                    make_float4(s[0], s[VEC > 1 ? 1 : 0], s[VEC > 2 ? 2 : 0], s[VEC > 3 ? 3 : 0]);
+            else
+                s_next[at] = s[0];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) red[slot][(lane % LPR) * VEC + i] = o[i];
+    __syncthreads();
+    const int n = blockIdx.y * COLS + threadIdx.x;
+    if (threadIdx.x < COLS && n < a.dv) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) sum += red[r][threadIdx.x];
+        put(static_cast<T *>(a.o) + ((long long)b * a.H + h) * a.dv + n, sum * a.scale);
+    }
+}
+
+template <typename T>
+cudaError_t step(const LaArgs &a, float *s_next, cudaStream_t st)
+{
+    const unsigned n = (unsigned)a.B * a.H;
+    // whole rows of up to 128 columns a block while that fills the GPU; 32
+    // columns, four times the blocks, for few sequences
+    if (a.dv % 4 != 0)
+        la_step_kernel<T, 32, 1><<<dim3(n, (a.dv + 31) / 32), STEP_WARPS * 32, 0, st>>>(a, a.s0, s_next);
+    else if (a.dv > 32 && (long long)n * ((a.dv + 127) / 128) >= 148)
+        la_step_kernel<T, 128, 4><<<dim3(n, (a.dv + 127) / 128), STEP_WARPS * 32, 0, st>>>(a, a.s0, s_next);
+    else
+        la_step_kernel<T, 32, 4><<<dim3(n, (a.dv + 31) / 32), STEP_WARPS * 32, 0, st>>>(a, a.s0, s_next);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t la_step_launch(const LaArgs &a, float *s_next, cudaStream_t st)
+{
+    return a.dtype == SLSTM_F32 ? step<float>(a, s_next, st) : step<__nv_bfloat16>(a, s_next, st);
+}
+
+}  // namespace slstm

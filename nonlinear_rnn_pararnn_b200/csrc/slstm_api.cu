@@ -5,6 +5,7 @@
 
 #include "block.h"
 #include "checked.cuh"
+#include "la.h"
 #include "launchers.h"
 
 using namespace slstm;
@@ -77,6 +78,95 @@ bool block_sizes_ok(int B, int T, int D, int F)
 // B*T rows 256 at a time on the grid's y axis (at most 65535 chunks).
 constexpr long long kBlockBwdMaxRows = 65535LL * 256;
 
+// The linear attention.  Rows (tokens), chunk x head grids and table entries
+// stay inside 32 bits; element offsets are 64-bit.
+bool la_sizes_ok(const slstm_linear_attention_config *c, int B, int T, bool packed)
+{
+    if (c == nullptr || B < 1 || T < 1) return false;
+    if (c->H < 1 || c->H_qk < 1 || c->H % c->H_qk != 0 || c->H > 65535) return false;
+    if (c->d_k < 1 || c->d_v < 1 || c->d_k > SLSTM_LA_MAX_DIM || c->d_v > SLSTM_LA_MAX_DIM) return false;
+    if (c->dtype != SLSTM_F32 && c->dtype != SLSTM_BF16) return false;
+    if (c->decay != SLSTM_DECAY_TOKEN && c->decay != SLSTM_DECAY_HEAD) return false;
+    const long long wqk = (long long)c->H_qk * c->d_k, wv = (long long)c->H * c->d_v;
+    if (c->ld_q < wqk || c->ld_k < wqk || c->ld_v < wv) return false;
+    if (c->ld_q > kIndexLimit || c->ld_k > kIndexLimit || c->ld_v > kIndexLimit) return false;
+    const long long rows = packed ? (long long)T : (long long)B * T;
+    const long long chunks = packed ? (long long)T / 64 + B : (long long)B * ((T + 63LL) / 64);
+    return rows <= kIndexLimit && chunks * c->H <= kIndexLimit && (long long)B * c->H <= kIndexLimit;
+}
+
+bool la_elem_aligned(const void *p, int dtype)
+{
+    return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (dtype == SLSTM_BF16 ? 1u : 3u)) == 0;
+}
+
+LaArgs la_args(const void *q, const void *k, const void *v, const float *g, const float *s0,
+               const slstm_linear_attention_config &c, int B, int T, const int *cu)
+{
+    LaArgs a{};
+    a.B = B;
+    a.T = T;
+    a.H = c.H;
+    a.Hqk = c.H_qk;
+    a.dk = c.d_k;
+    a.dv = c.d_v;
+    a.ldq = c.ld_q;
+    a.ldk = c.ld_k;
+    a.ldv = c.ld_v;
+    a.dtype = c.dtype;
+    a.per_head = c.decay == SLSTM_DECAY_HEAD;
+    a.scale = c.scale;
+    a.cu = cu;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.s0 = s0;
+    return a;
+}
+
+size_t la_workspace(const LaArgs &a, bool backward) { return la_simt_workspace(a, backward); }
+
+bool la_inputs_ok(const LaArgs &a)
+{
+    return la_elem_aligned(a.q, a.dtype) && la_elem_aligned(a.k, a.dtype) && la_elem_aligned(a.v, a.dtype) &&
+           la_elem_aligned(a.g, SLSTM_F32) && aligned16_or_null(a.s0);
+}
+
+int la_forward(LaArgs a, void *o, float *sT, void *ws, size_t ws_bytes, slstm_stream_t stream)
+{
+    a.o = o;
+    a.sT = sT;
+    if (!la_inputs_ok(a) || !la_elem_aligned(o, a.dtype) || !aligned16_or_null(sT)) return SLSTM_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, la_workspace(a, false))) return SLSTM_ERR_INVALID_ARG;
+    return cuda_status(la_simt_forward(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+int la_backward(LaArgs a, const void *dO, const float *dsT, void *dq, void *dk, void *dv, float *dg, float *ds0,
+                void *ws, size_t ws_bytes, slstm_stream_t stream)
+{
+    a.dO = dO;
+    a.dsT = dsT;
+    a.dq = dq;
+    a.dk_ = dk;
+    a.dv_ = dv;
+    a.dg = dg;
+    a.ds0 = ds0;
+    if (!la_inputs_ok(a) || !la_elem_aligned(dO, a.dtype) || !aligned16_or_null(dsT) || !aligned16_or_null(ds0))
+        return SLSTM_ERR_INVALID_ARG;
+    if (!la_elem_aligned(dq, a.dtype) || !la_elem_aligned(dk, a.dtype) || !la_elem_aligned(dv, a.dtype))
+        return SLSTM_ERR_INVALID_ARG;
+    if (dg != nullptr && !la_elem_aligned(dg, SLSTM_F32)) return SLSTM_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, la_workspace(a, true))) return SLSTM_ERR_INVALID_ARG;
+    return cuda_status(la_simt_backward(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+bool ln_sizes_ok(long long rows, int groups, int d)
+{
+    if (rows < 1 || groups < 1 || groups > 65535 || d < 1 || d > SLSTM_LN_MAX_DIM) return false;
+    return rows <= kIndexLimit && rows * groups <= kIndexLimit && (long long)groups * d <= kIndexLimit / 2;
+}
+
 }  // namespace
 
 namespace slstm {
@@ -139,7 +229,7 @@ const char *slstm_check_site_file(int file_id)
 {
     static const char *const names[] = {nullptr,         "newton.cu", "backward.cu", "scan.cu",  "sequential.cu",
                                         "varlen.cu",     "decode.cu", "head.cu",     "block.cu", "gemm_simt.cu",
-                                        "scan_noalloc.cu"};
+                                        "scan_noalloc.cu", "linear_attention.cu", "layer_norm.cu"};
     if (file_id < 1 || file_id >= (int)(sizeof(names) / sizeof(names[0]))) return nullptr;
     return names[file_id];
 }
@@ -456,6 +546,102 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
     return cuda_status(block_backward_launch(x, norm1_w, Wx, bias, R, norm2_w, W_gu, W_down, S, dY, dx, dnorm1_w, dWx,
                                              dbias, dR, dnorm2_w, dW_gu, dW_down, forget, B, T, d_model, d_ff, eps, ws,
                                              static_cast<cudaStream_t>(stream)));
+}
+
+size_t slstm_linear_attention_workspace_size(const slstm_linear_attention_config *cfg, int B, int T, int packed,
+                                             int backward)
+{
+    if (!la_sizes_ok(cfg, B, T, packed != 0)) return 0;
+    static const int any = 0;   // a packed call's workspace depends on there being offsets, not on them
+    return la_workspace(la_args(nullptr, nullptr, nullptr, nullptr, nullptr, *cfg, B, T, packed ? &any : nullptr),
+                        backward != 0);
+}
+
+int slstm_linear_attention_forward(const void *q, const void *k, const void *v, const float *g, const float *s0,
+                                   void *o, float *sT, const slstm_linear_attention_config *cfg, int B, int T,
+                                   void *ws, size_t ws_bytes, slstm_stream_t stream)
+{
+    if (!la_sizes_ok(cfg, B, T, false)) return SLSTM_ERR_INVALID_ARG;
+    return la_forward(la_args(q, k, v, g, s0, *cfg, B, T, nullptr), o, sT, ws, ws_bytes, stream);
+}
+
+int slstm_linear_attention_backward(const void *q, const void *k, const void *v, const float *g, const float *s0,
+                                    const void *dO, const float *dsT, void *dq, void *dk, void *dv, float *dg,
+                                    float *ds0, const slstm_linear_attention_config *cfg, int B, int T, void *ws,
+                                    size_t ws_bytes, slstm_stream_t stream)
+{
+    if (!la_sizes_ok(cfg, B, T, false)) return SLSTM_ERR_INVALID_ARG;
+    return la_backward(la_args(q, k, v, g, s0, *cfg, B, T, nullptr), dO, dsT, dq, dk, dv, dg, ds0, ws, ws_bytes,
+                       stream);
+}
+
+int slstm_linear_attention_forward_varlen(const void *q, const void *k, const void *v, const float *g,
+                                          const float *s0, const int *cu_seqlens, int n_seq, void *o, float *sT,
+                                          const slstm_linear_attention_config *cfg, int total_T, void *ws,
+                                          size_t ws_bytes, slstm_stream_t stream)
+{
+    if (!la_sizes_ok(cfg, n_seq, total_T, true) || !la_elem_aligned(cu_seqlens, SLSTM_F32))
+        return SLSTM_ERR_INVALID_ARG;
+    return la_forward(la_args(q, k, v, g, s0, *cfg, n_seq, total_T, cu_seqlens), o, sT, ws, ws_bytes, stream);
+}
+
+int slstm_linear_attention_backward_varlen(const void *q, const void *k, const void *v, const float *g,
+                                           const float *s0, const int *cu_seqlens, int n_seq, const void *dO,
+                                           const float *dsT, void *dq, void *dk, void *dv, float *dg, float *ds0,
+                                           const slstm_linear_attention_config *cfg, int total_T, void *ws,
+                                           size_t ws_bytes, slstm_stream_t stream)
+{
+    if (!la_sizes_ok(cfg, n_seq, total_T, true) || !la_elem_aligned(cu_seqlens, SLSTM_F32))
+        return SLSTM_ERR_INVALID_ARG;
+    return la_backward(la_args(q, k, v, g, s0, *cfg, n_seq, total_T, cu_seqlens), dO, dsT, dq, dk, dv, dg, ds0, ws,
+                       ws_bytes, stream);
+}
+
+int slstm_linear_attention_step(const void *q, const void *k, const void *v, const float *g, const float *s_prev,
+                                float *s_next, void *o, const slstm_linear_attention_config *cfg, int B,
+                                slstm_stream_t stream)
+{
+    if (!la_sizes_ok(cfg, B, 1, false)) return SLSTM_ERR_INVALID_ARG;
+    LaArgs a = la_args(q, k, v, g, s_prev, *cfg, B, 1, nullptr);
+    a.o = o;
+    if (!la_inputs_ok(a) || !aligned16(s_next) || !la_elem_aligned(o, a.dtype)) return SLSTM_ERR_INVALID_ARG;
+    return cuda_status(la_step_launch(a, s_next, static_cast<cudaStream_t>(stream)));
+}
+
+int slstm_layer_norm_forward(const void *x, int x_dtype, const float *w, const float *b, void *y, int y_dtype,
+                             float *mean, float *rstd, long long rows, int groups, int d, float eps,
+                             slstm_stream_t stream)
+{
+    if (x_dtype != SLSTM_F32 && x_dtype != SLSTM_BF16) return SLSTM_ERR_INVALID_ARG;
+    if (y_dtype != SLSTM_F32 && y_dtype != SLSTM_BF16) return SLSTM_ERR_INVALID_ARG;
+    if (!ln_sizes_ok(rows, groups, d) || !(eps >= 0.0f)) return SLSTM_ERR_INVALID_ARG;
+    if (!la_elem_aligned(x, x_dtype) || !la_elem_aligned(y, y_dtype) || !la_elem_aligned(w, SLSTM_F32) ||
+        (b != nullptr && !la_elem_aligned(b, SLSTM_F32)) || !la_elem_aligned(mean, SLSTM_F32) ||
+        !la_elem_aligned(rstd, SLSTM_F32))
+        return SLSTM_ERR_INVALID_ARG;
+    return cuda_status(layer_norm_forward(x, x_dtype, w, b, y, y_dtype, mean, rstd, rows, groups, d, eps,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t slstm_layer_norm_workspace_size(long long rows, int groups, int d)
+{
+    return ln_sizes_ok(rows, groups, d) ? layer_norm_workspace_bytes(rows, groups, d) : 0;
+}
+
+int slstm_layer_norm_backward(const void *x, int x_dtype, const float *w, const void *dy, int y_dtype,
+                              const float *mean, const float *rstd, void *dx, float *dw, float *db, long long rows,
+                              int groups, int d, void *ws, size_t ws_bytes, slstm_stream_t stream)
+{
+    if (x_dtype != SLSTM_F32 && x_dtype != SLSTM_BF16) return SLSTM_ERR_INVALID_ARG;
+    if (y_dtype != SLSTM_F32 && y_dtype != SLSTM_BF16) return SLSTM_ERR_INVALID_ARG;
+    if (!ln_sizes_ok(rows, groups, d)) return SLSTM_ERR_INVALID_ARG;
+    if (!la_elem_aligned(x, x_dtype) || !la_elem_aligned(dx, x_dtype) || !la_elem_aligned(dy, y_dtype) ||
+        !la_elem_aligned(w, SLSTM_F32) || !la_elem_aligned(mean, SLSTM_F32) || !la_elem_aligned(rstd, SLSTM_F32) ||
+        !la_elem_aligned(dw, SLSTM_F32) || !la_elem_aligned(db, SLSTM_F32))
+        return SLSTM_ERR_INVALID_ARG;
+    if (!ws_ok(ws, ws_bytes, layer_norm_workspace_bytes(rows, groups, d))) return SLSTM_ERR_INVALID_ARG;
+    return cuda_status(layer_norm_backward(x, x_dtype, w, dy, y_dtype, mean, rstd, dx, dw, db, rows, groups, d, ws,
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
