@@ -53,6 +53,19 @@ int la_chunk_bound(const LaArgs &a, int C);
 // Fill the table (packed) at `mem` on `st`.
 cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st);
 
+// The states over the chunks (or segments) of each sequence, elementwise: the
+// E-element deltas in buf[chunk][h], with the decays tot[chunk][h], give way to
+// the state that enters each (back: the gradient of the one that leaves it),
+// starting from first[sequence][h] (null: zero); the last one to `last` (or
+// null).
+cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,
+                    float *last, cudaStream_t st);
+
+// bf16 on the tensor cores.
+bool la_tc_takes(const LaArgs &a);
+size_t la_tc_forward_workspace(const LaArgs &a);
+cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st);
+
 // Sums of the fp32 per-head partial gradients over the heads that share a
 // query and key head: out[row][hq][d] = sum over r of part[row][hq * rep + r][d].
 cudaError_t la_share_sum(const float *part, void *out, int dtype, const LaChunks &ch, const LaArgs &a, cudaStream_t st);

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(1024) la_table_kernel(const int *__restrict__ 
         if (lane == 0) prev = before;
         for (int w = 0; w < 32; ++w) top = max(top, wm[w]);
         // chunks of sequence k - 1, which ends at offset k
-        int n = k >= 1 && k <= n_seq ? (m - prev + C - 1) / C : 0;
+        int n = k >= 1 && k <= n_seq && m > prev ? (m - prev - 1) / C + 1 : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, n, o);
@@ -539,18 +539,26 @@ size_t la_table_bytes(const LaArgs &a) { return a.cu ? 2 * up256(4 * ((size_t)a.
 
 int la_chunk_bound(const LaArgs &a, int C)
 {
-    return a.cu ? a.T / C + a.B : a.B * ((a.T + C - 1) / C);
+    return a.cu ? a.T / C + a.B : a.B * ((a.T - 1) / C + 1);
 }
 
 cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st)
 {
-    *out = LaChunks{a.B, a.T, C, (a.T + C - 1) / C, la_chunk_bound(a, C), nullptr, nullptr};
+    *out = LaChunks{a.B, a.T, C, (a.T - 1) / C + 1, la_chunk_bound(a, C), nullptr, nullptr};
     if (a.cu == nullptr) return cudaSuccess;
     int *pos = static_cast<int *>(mem);
     int *coff = reinterpret_cast<int *>(static_cast<char *>(mem) + up256(4 * ((size_t)a.B + 1)));
     la_table_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.T, C, pos, coff);
     out->pos = pos;
     out->coff = coff;
+    return cudaGetLastError();
+}
+
+cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,
+                    float *last, cudaStream_t st)
+{
+    la_scan_kernel<<<dim3((unsigned)ch.n_seq * H, (E + 255) / 256), 256, 0, st>>>(ch, H, E, back, buf, tot, first,
+                                                                                last);
     return cudaGetLastError();
 }
 
@@ -616,9 +624,7 @@ cudaError_t states(const LaArgs &a, const LaChunks &ch, bool back, float *buf, f
     la_delta_kernel<T><<<grid, NT, 0, st>>>(a, ch, back, buf, tot);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    la_scan_kernel<<<dim3((unsigned)a.B * a.H, (E + 255) / 256), 256, 0, st>>>(ch, a.H, E, back, buf, tot,
-                                                                             back ? a.dsT : a.s0, back ? a.ds0 : a.sT);
-    return cudaGetLastError();
+    return la_scan(ch, a.H, E, back, buf, tot, back ? a.dsT : a.s0, back ? a.ds0 : a.sT, st);
 }
 
 template <typename T>

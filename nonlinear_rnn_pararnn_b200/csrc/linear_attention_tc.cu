@@ -1,0 +1,897 @@
+// Linear attention with a decay for each head, bf16 on the sm_100a tensor
+// cores (tcgen05 + TMEM, fed by TMA); the formulas are at linear_attention.cu.
+// d_k and d_v up to 128, multiples of 8; chunks of 128 rows, so that a chunk's
+// products are 128 x 128 x d tiles.
+//
+// What needs how many bits: products of q, k, v and dO with one another are
+// exact in the fp32 accumulators.  The weights D (q k) are rounded to bf16
+// where they enter the product with v, as the outputs are.  The state is held
+// in fp32 registers; what is added to it, a row of v times its decay, is split
+// into two bf16 terms (2^-17 of it left), since the final state is an fp32
+// output.  Where the state enters a product for a bf16 output its upper term
+// does; for the gradient of the decay, an fp32 output, both do.
+//
+// Every mbarrier wait is bounded in time; on expiry the block marks itself,
+// waits (bounded) for its own loads and MMAs, writes NaN over its outputs,
+// frees its tensor memory and returns.
+#include <cuda_bf16.h>
+
+#define SLSTM_FILE_ID 13
+#include "checked.cuh"
+#include "la.cuh"
+#include "launchers.h"
+#include "tc.cuh"
+
+namespace slstm {
+namespace {
+
+constexpr int TCC = 128;                     // rows of a chunk
+constexpr uint32_t BOX = TCC * 128;          // bytes of 128 rows of 64 bf16
+constexpr uint64_t TC_WAIT_NS = 1000000000ull;
+
+// Blocks of one pass: a segment (a run of chunks of one sequence) of one head
+// and 64 columns of the state.
+struct TcArgs {
+    LaArgs a;
+    LaChunks seg;             // the segments
+    LaChunks ch;              // the chunks (packed: the table's second view)
+    int tiles;                // 64-column tiles of d_v
+    // states: where a segment starts and what it leaves
+    const float *init;        // entry states [segment][h], or null: first
+    const float *first;       // entry states [sequence][h] (null: zero)
+    float *fin;               // final states [segment][h], or null: last
+    float *fin_tot;           // [segment][h] decay of a segment
+    float *last;              // final states [sequence][h], or null
+    __nv_bfloat16 *hi, *lo;   // states that enter each chunk, [chunk][h] (dk x dv), or null
+    bool back;                // from the end: (q, dO) in place of (k, v)
+};
+
+struct TcDecays {
+    double cum[TCC];
+    double blk[4];        // cum of the first row of each 32
+    float loc[TCC];       // cum - blk of its 32
+    int first[TCC];
+    float row[TCC], col[TCC];
+    float tot;
+    int pad;
+};
+
+SLSTM_DEVINL float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+SLSTM_DEVINL uint32_t pack2(float a, float b)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+SLSTM_DEVINL float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+SLSTM_DEVINL float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Byte offset of 16-byte piece p of a row in a 128-byte-swizzled box.
+SLSTM_DEVINL uint32_t swz(int row, int p) { return (uint32_t)row * 128u + (uint32_t)((p ^ (row & 7)) << 4); }
+
+// One wait of a whole warp: every lane the same answer; false once this block
+// has given up.
+SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+{
+    const bool ok = !*(volatile int *)s_abort && mbar_wait(bar, parity, TC_WAIT_NS);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    *(volatile int *)s_abort = 1;
+    return false;
+}
+SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+{
+    if (!*(volatile int *)s_abort && mbar_wait(bar, parity, TC_WAIT_NS)) return true;
+    *(volatile int *)s_abort = 1;
+    return false;
+}
+
+// The warp's shared-memory writes (and its reads of tensor memory) before the
+// arrival on `bar`.
+SLSTM_DEVINL void warp_arrive(uint64_t *bar)
+{
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// The decays of a chunk by one warp into `d`.
+SLSTM_DEVINL void tc_decays(TcDecays &d, const LaArgs &a, long long row, int len, int h, int lane)
+{
+    la_decays<4>(a.g, a.per_head ? h : row * a.H + h, a.per_head ? 0 : a.H, len, lane, d.cum, d.first, d.row, d.col,
+                 &d.tot);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = lane * 4 + i;
+        d.loc[t] = (float)(d.cum[t] - d.cum[t & ~31]);
+    }
+    if (lane < 4) d.blk[lane] = d.cum[lane * 32];
+}
+
+// Row t of a 64-column box of v (or dO) times w as two bf16 terms into the
+// boxes at hi and lo; zero where !on.
+SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, float w, bool on)
+{
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+        const uint32_t o = swz(t, p);
+        uint4 h = make_uint4(0, 0, 0, 0), l = h;
+        if (on) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(src + o);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t y[4], z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
+                y[i] = pack2(a, b);
+                z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
+            }
+            h = make_uint4(y[0], y[1], y[2], y[3]);
+            l = make_uint4(z[0], z[1], z[2], z[3]);
+        }
+        *reinterpret_cast<uint4 *>(hi + o) = h;
+        *reinterpret_cast<uint4 *>(lo + o) = l;
+    }
+}
+
+SLSTM_DEVINL void zero_row(uint8_t *box, int t)
+{
+#pragma unroll
+    for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4 *>(box + t * 128 + p * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// Where a segment lies.
+struct Seg {
+    int seq, nch, len;        // sequence, chunks, rows
+    long long row;            // first row
+    int t, b;                 // TMA coordinates of the first row
+    long long c0;             // index of its first chunk
+};
+
+SLSTM_DEVINL bool seg_of(const TcArgs &g, int i, Seg *s)
+{
+    const LaChunk c = la_chunk(g.seg, i);
+    if (c.len <= 0) return false;
+    s->seq = c.seq;
+    s->len = c.len;
+    s->nch = (c.len + TCC - 1) / TCC;
+    s->row = c.row;
+    const bool packed = g.seg.pos != nullptr;
+    s->t = packed ? (int)c.row : c.n * g.seg.C;
+    s->b = packed ? 0 : c.seq;
+    s->c0 = (packed ? (long long)g.ch.coff[c.seq] : (long long)c.seq * g.ch.nc) + (long long)c.n * (g.seg.C / TCC);
+    return true;
+}
+
+// The thread's share of a state tile of DK rows and 64 columns in registers:
+// with DK = 128 a row of 64; with DK = 64 the accumulator's lanes 64..127
+// repeat lanes 0..63 (the MMA is given its 64 rows twice), and a thread holds
+// 32 columns.
+template <int DK>
+struct Share {
+    static constexpr int N = DK == 128 ? 64 : 32;
+    SLSTM_DEVINL static int row(int warp, int lane) { return (DK == 128 ? warp : (warp & 1)) * 32 + lane; }
+    SLSTM_DEVINL static int col(int warp) { return DK == 128 ? 0 : 32 * (warp >> 1); }
+};
+
+template <int N>
+SLSTM_DEVINL void state_load(float (&S)[N], const float *src, int dk, int dv, int r, int col)
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        float4 f = make_float4(0, 0, 0, 0);
+        if (src && r < dk && col + i < dv) f = *reinterpret_cast<const float4 *>(src + (long long)r * dv + col + i);
+        S[i] = f.x;
+        S[i + 1] = f.y;
+        S[i + 2] = f.z;
+        S[i + 3] = f.w;
+    }
+}
+
+template <int N>
+SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, int r, int col)
+{
+    if (r >= dk) return;
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+        if (col + i < dv)
+            *reinterpret_cast<float4 *>(dst + (long long)r * dv + col + i) =
+                make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+}
+
+// ---------------------------------------------------------------------------
+// The states of a segment: one block walks its chunks and keeps the state of
+// its 64 columns in registers,
+//   S <- e^{c_C} S + X^T (w Y):  X = k, Y = v, w = e^{c_C - c_j} (forward)
+//                                X = q, Y = dO, w = scale e^{c_i} (from the end)
+// and writes the state that each chunk starts from (two bf16 terms, for the
+// backward kernel) and / or the final one.  Warps 0-3 scale Y and hold the
+// state (lane = row of d_k), warp 4 loads (a ring of NST chunks), warp 5 issues
+// the MMAs, warp 6 computes the decays.  Bound: the bytes of X and Y and of the
+// states written.
+// ---------------------------------------------------------------------------
+template <int DK>
+struct StateShared {
+    static constexpr int NST = DK == 128 ? 3 : 4;
+    static constexpr int NB = DK / 64;
+    static constexpr uint32_t STAGE = (NB + 1) * BOX;
+    static constexpr uint32_t Y = NST * STAGE;          // two buffers of hi, lo
+    static constexpr uint32_t DEC = Y + 4 * BOX;
+    static constexpr uint32_t BYTES = DEC + 3 * sizeof(TcDecays) + 1024;
+};
+
+template <int DK>
+__global__ void __launch_bounds__(224, 1)
+    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                    const __grid_constant__ CUtensorMap mx2, const __grid_constant__ CUtensorMap my2, TcArgs g0,
+                    TcArgs g1)
+{
+    typedef StateShared<DK> SM;
+    constexpr int NST = SM::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
+    __shared__ uint64_t full[NST], empty[NST], dfull[3], dempty[3], yready[2], delta[2], fin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_loaded;
+    // blockIdx.y picks the direction where both run in one launch
+    const TcArgs &g = blockIdx.y ? g1 : g0;
+    const CUtensorMap *tx = blockIdx.y ? &mx2 : &mx, *ty = blockIdx.y ? &my2 : &my;
+    const LaArgs &a = g.a;
+    const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
+    Seg sg;
+    if (!seg_of(g, item, &sg)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool back = g.back, packed = g.seg.pos != nullptr;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&yready[i], 4);
+            mbar_init(&delta[i], 1);
+        }
+        mbar_init(&fin, 1);
+        mbar_init_fence();
+        s_abort = 0;
+        s_loaded = 0;
+    }
+    if (warp == 0) tmem_alloc<128>(&s_tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int nch = sg.nch;
+    // the n-th chunk walked, and its rows
+    auto chunk = [&](int n) { return back ? nch - 1 - n : n; };
+    auto rows = [&](int n) { return min(TCC, sg.len - chunk(n) * TCC); };
+
+    if (warp == 4) {
+        if (lane == 0) {
+            const int hq = h / (a.H / a.Hqk);
+            int n = 0;
+            for (; n < nch; ++n) {
+                const int s = n % NST;
+                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) break;
+                uint8_t *st = smem + s * SM::STAGE;
+                mbar_expect_tx(&full[s], SM::STAGE);
+                const int t = sg.t + chunk(n) * TCC;
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, tx, &full[s], 64 * i, hq, t, sg.b);
+                tma_load_4d(st + SM::NB * BOX, ty, &full[s], 64 * tile, h, t, sg.b);
+            }
+            s_loaded = n;
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16(128, 64, true, true);
+            for (int n = 0; n < nch; ++n) {
+                const int s = n % NST;
+                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+                if (!lane_wait(&yready[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
+                tc_fence_after();
+                // the 64 rows of a narrow d_k twice: no step from one 64 to the next
+                const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
+                const uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint64_t bd = smem_desc_mn_sw128(smem_u32(y + z * BOX), BOX);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_bf16(tmem + (n & 1) * 64, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, idesc,
+                                  (z > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&delta[n & 1]);
+                umma_commit(&empty[s]);
+            }
+            umma_commit(&fin);
+        }
+    } else if (warp == 6) {
+        for (int n = 0; n < nch; ++n) {
+            if (!warp_wait(&dempty[n % 3], ((uint32_t)(n / 3) & 1u) ^ 1u, &s_abort)) break;
+            tc_decays(dec[n % 3], a, sg.row + (long long)chunk(n) * TCC, rows(n), h, lane);
+            warp_arrive(&dfull[n % 3]);
+        }
+    } else {
+        typedef Share<DK> SH;
+        const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
+        const long long E = (long long)a.dk * a.dv;
+        const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
+                                  : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
+        float S[SH::N];
+        state_load(S, src, a.dk, a.dv, r, col);
+        float run = 1.0f;
+        auto scale = [&](int n) -> bool {
+            const int s = n % NST;
+            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
+            if (!warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort)) return false;
+            uint8_t *st = smem + s * SM::STAGE;
+            const TcDecays &d = dec[n % 3];
+            const int t = threadIdx.x, len = rows(n);
+            uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
+            scale_row(st + SM::NB * BOX, y, y + BOX, t, back ? a.scale * d.row[t] : d.col[t], t < len);
+            // rows behind a packed sequence belong to another one
+            if (packed && t >= len)
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) zero_row(st + i * BOX, t);
+            tma_store_fence();
+            warp_arrive(&yready[n & 1]);
+            return true;
+        };
+        bool ok = scale(0);
+        for (int n = 0; n < nch && ok; ++n) {
+            if (n + 1 < nch) ok = scale(n + 1);
+            if (!ok) break;
+            if (g.hi && r < a.dk) {
+                const long long at = ((sg.c0 + chunk(n)) * a.H + h) * E + (long long)r * a.dv + col;
+#pragma unroll
+                for (int i = 0; i < SH::N; i += 8) {
+                    if (col + i >= a.dv) break;
+                    uint32_t y[4], z[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float u = S[i + 2 * j], v = S[i + 2 * j + 1];
+                        y[j] = pack2(u, v);
+                        z[j] = pack2(u - lo_of(y[j]), v - hi_of(y[j]));
+                    }
+                    *reinterpret_cast<uint4 *>(g.hi + at + i) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(g.lo + at + i) = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+            }
+            if (!warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float tot = dec[n % 3].tot;
+            run *= tot;
+#pragma unroll
+            for (int i = 0; i < SH::N; i += 32) {
+                float v[32];
+                tmem_ld32(tmem + (n & 1) * 64 + c0 + i + ((uint32_t)(warp * 32) << 16), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[i + j] = fmaf(tot, S[i + j], v[j]);
+            }
+            tc_fence_before();
+            warp_arrive(&dempty[n % 3]);
+        }
+        if (!ok) {
+#pragma unroll
+            for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
+            if (g.hi && r < a.dk)
+                for (int n = 0; n < nch; ++n)
+                    for (int i = 0; i < SH::N && col + i < a.dv; ++i)
+                        g.hi[((sg.c0 + n) * a.H + h) * E + (long long)r * a.dv + col + i] = __float2bfloat16(S[0]);
+        }
+        float *dst = g.fin ? g.fin + ((long long)item * a.H + h) * E
+                           : (g.last ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
+        if (dst) state_store(S, dst, a.dk, a.dv, r, col);
+        if (g.fin && tile == 0 && threadIdx.x == 0) g.fin_tot[(long long)item * a.H + h] = run;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (s_abort)
+            for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
+                (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
+        (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free<128>(tmem);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The forward pass of a segment: one block walks the chunks of one head and 64
+// columns of v and does all of it while q, k and v are in shared memory, the
+// state in registers:
+//   warps 0-3   v times its decays (two bf16 terms), the state (lane = row of
+//               d_k), the state's upper term into shared memory
+//   warps 4-7   the weights D (q k) from tensor memory and back as bf16
+//               (lane = query row), then the outputs
+//   warp 8      loads, a ring of NST chunks;  warp 9 issues the MMAs
+//   warp 10     the decays, up to three chunks ahead
+// A chunk's products: q k^T (128 x 128), then into one 64-column accumulator
+// each q S, D(q k) v (A from tensor memory) and k^T (w v).  The first of the
+// next chunk is issued before the last of this one, so that the tensor cores
+// work while the weights are computed.
+// ---------------------------------------------------------------------------
+template <int DK>
+struct FwdShared {
+    static constexpr int NST = DK == 128 ? 2 : 3;
+    static constexpr int NB = DK / 64;
+    static constexpr uint32_t STAGE = (2 * NB + 1) * BOX;   // q, k, v
+    static constexpr uint32_t Y = NST * STAGE;              // hi, lo
+    static constexpr uint32_t S = Y + 2 * BOX;
+    static constexpr uint32_t DEC = S + DK * 128;
+    static constexpr uint32_t BYTES = DEC + 3 * sizeof(TcDecays) + 1024;
+};
+static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
+
+constexpr int FWD_THREADS = 352;
+
+template <int DK>
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+    la_forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                      const __grid_constant__ CUtensorMap mv, TcArgs g)
+{
+    typedef FwdShared<DK> SM;
+    constexpr int NST = SM::NST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
+    __shared__ uint64_t full[NST], empty[NST], dfull[3], dempty[3], scfull[2];
+    __shared__ uint64_t yready, delta, sready, sfree, pready, ofull, oempty, tready, fin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_loaded;
+    const LaArgs &a = g.a;
+    const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
+    Seg sg;
+    if (!seg_of(g, item, &sg)) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool packed = g.seg.pos != nullptr;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
+        mbar_init(&yready, 4);
+        mbar_init(&delta, 1);
+        mbar_init(&sready, 4);
+        mbar_init(&sfree, 1);
+        mbar_init(&pready, 4);
+        mbar_init(&ofull, 1);
+        mbar_init(&oempty, 4);
+        mbar_init(&tready, 4);
+        mbar_init(&fin, 1);
+        mbar_init_fence();
+        s_abort = 0;
+        s_loaded = 0;
+    }
+    if (warp == 0) tmem_alloc<512>(&s_tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t t_o1 = tmem + 256, t_o2 = tmem + 320, t_delta = tmem + 384;   // scores: 0 and 128
+    const int nch = sg.nch;
+    // the last chunk of a packed sequence holds rows of the next one
+    const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            const int hq = h / (a.H / a.Hqk);
+            int n = 0;
+            for (; n < nch; ++n) {
+                const int s = n % NST;
+                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) break;
+                uint8_t *st = smem + s * SM::STAGE;
+                mbar_expect_tx(&full[s], SM::STAGE);
+                const int t = sg.t + n * TCC;
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) {
+                    tma_load_4d(st + i * BOX, &mq, &full[s], 64 * i, hq, t, sg.b);
+                    tma_load_4d(st + (SM::NB + i) * BOX, &mk, &full[s], 64 * i, hq, t, sg.b);
+                }
+                tma_load_4d(st + 2 * SM::NB * BOX, &mv, &full[s], 64 * tile, h, t, sg.b);
+            }
+            s_loaded = n;
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            constexpr uint32_t id_qk = idesc_bf16(128, 128, false, false);
+            constexpr uint32_t id_kv = idesc_bf16(128, 64, true, true);
+            constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
+            auto scores = [&](int n) -> bool {
+                const int s = n % NST;
+                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
+                if (n == ragged && !lane_wait(&tready, 0u, &s_abort)) return false;
+                tc_fence_after();
+                const uint8_t *st = smem + s * SM::STAGE;
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) {
+                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
+                    const uint64_t kd = smem_desc_k_sw128(smem_u32(st + (SM::NB + i) * BOX));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(tmem + (n & 1) * 128, qd + 2 * k, kd + 2 * k, id_qk, (i > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&scfull[n & 1]);
+                return true;
+            };
+            bool ok = scores(0);
+            for (int n = 0; n < nch && ok; ++n) {
+                const int s = n % NST;
+                const uint32_t ph = (uint32_t)n & 1u;
+                const uint8_t *st = smem + s * SM::STAGE;
+                ok = lane_wait(&yready, ph, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t kt = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), DK == 128 ? BOX : 0u);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y + z * BOX), BOX);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv,
+                                  (z > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&delta);
+                if (n + 1 < nch) ok = scores(n + 1);
+                if (!ok) break;
+                ok = lane_wait(&sready, ph, &s_abort) && lane_wait(&oempty, ph ^ 1u, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) {
+                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(t_o1, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&sfree);
+                ok = lane_wait(&pready, ph, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 8 * k, vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
+                umma_commit(&ofull);
+                umma_commit(&empty[s]);
+            }
+            umma_commit(&fin);
+        }
+    } else if (warp == 10) {
+        for (int n = 0; n < nch; ++n) {
+            if (!warp_wait(&dempty[n % 3], ((uint32_t)(n / 3) & 1u) ^ 1u, &s_abort)) break;
+            tc_decays(dec[n % 3], a, sg.row + (long long)n * TCC, min(TCC, sg.len - n * TCC), h, lane);
+            warp_arrive(&dfull[n % 3]);
+        }
+    } else if (warp < 4) {
+        typedef Share<DK> SH;
+        const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0, t = threadIdx.x;
+        const long long E = (long long)a.dk * a.dv;
+        const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
+                                  : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
+        float S[SH::N];
+        state_load(S, src, a.dk, a.dv, r, col);
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST;
+            const uint32_t ph = (uint32_t)n & 1u;
+            const int len = min(TCC, sg.len - n * TCC);
+            uint8_t *st = smem + s * SM::STAGE;
+            if (n == ragged) {
+                // before anything that waits for this block's products: the
+                // first of this chunk is issued ahead of them
+                ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort);
+                if (!ok) break;
+                if (t >= len)
+#pragma unroll
+                    for (int i = 0; i < 2 * SM::NB + 1; ++i) zero_row(st + i * BOX, t);
+                tma_store_fence();
+                warp_arrive(&tready);
+            }
+            if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_abort);
+            if (!ok) break;
+            // the state's upper term, row r: the B operand of q S
+#pragma unroll
+            for (int i = 0; i < SH::N / 8; ++i)
+                *reinterpret_cast<uint4 *>(smem + SM::S + swz(r, c0 / 8 + i)) =
+                    make_uint4(pack2(S[8 * i], S[8 * i + 1]), pack2(S[8 * i + 2], S[8 * i + 3]),
+                               pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
+            tma_store_fence();
+            warp_arrive(&sready);
+            ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
+                 warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort);
+            if (!ok) break;
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, dec[n % 3].col[t], t < len);
+            tma_store_fence();
+            warp_arrive(&yready);
+            ok = warp_wait(&delta, ph, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const float tot = dec[n % 3].tot;
+#pragma unroll
+            for (int i = 0; i < SH::N; i += 32) {
+                float v[32];
+                tmem_ld32(t_delta + c0 + i + ((uint32_t)(warp * 32) << 16), v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[i + j] = fmaf(tot, S[i + j], v[j]);
+            }
+            tc_fence_before();
+            warp_arrive(&dempty[n % 3]);
+        }
+        if (!ok)
+#pragma unroll
+            for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
+        if (g.last) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
+    } else {
+        const int q = warp & 3;
+        const int i = q * 32 + lane;   // query row
+        const uint32_t la = (uint32_t)(q * 32) << 16;
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
+                           (long long)h * a.dv + tile * 64;
+        const int cols = min(64, a.dv - tile * 64);
+        bool ok = true;
+        int n = 0;
+        for (; n < nch; ++n) {
+            const uint32_t ph = (uint32_t)n & 1u;
+            ok = warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort) &&
+                 warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const TcDecays &d = dec[n % 3];
+            const uint32_t sc = tmem + (n & 1) * 128 + la;
+            const double ci = d.cum[i];
+            const int f = max(d.first[i], 0);
+            const uint32_t span = (uint32_t)(i - f);
+            const float rowc = d.row[i] * a.scale;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16];
+                if (b <= q) {
+                    float v[32];
+                    tmem_ld32(sc + 32 * b, v);
+                    const float rb = (float)(ci - d.blk[b]);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 l = *reinterpret_cast<const float2 *>(&d.loc[32 * b + j]);
+                        const float e0 = ex2(rb - l.x), e1 = ex2(rb - l.y);
+                        const float p0 = (uint32_t)(32 * b + j - f) <= span ? v[j] * e0 : 0.0f;
+                        const float p1 = (uint32_t)(32 * b + j + 1 - f) <= span ? v[j + 1] * e1 : 0.0f;
+                        p[j / 2] = pack2(p0, p1);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[j] = 0u;
+                }
+                // over the scores already read: column 16 b .. of 32 (b + 1)
+                tmem_st16(sc + 16 * b, p);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&pready);
+            ok = warp_wait(&ofull, ph, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const bool on = n * TCC + i < sg.len;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                float u[32], w[32];
+                tmem_ld32(t_o1 + la + c, u);
+                tmem_ld32(t_o2 + la + c, w);
+                if (c == 32) {
+                    tc_fence_before();
+                    warp_arrive(&oempty);
+                    warp_arrive(&dempty[n % 3]);
+                }
+                if (on) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        if (c + j >= cols) break;
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = pack2(fmaf(rowc, u[j + 2 * k], a.scale * w[j + 2 * k]),
+                                         fmaf(rowc, u[j + 2 * k + 1], a.scale * w[j + 2 * k + 1]));
+                        *reinterpret_cast<uint4 *>(o + (long long)n * TCC * a.H * a.dv + c + j) =
+                            make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+        }
+        if (!ok)
+            for (; n * TCC + i < sg.len; ++n)
+                if (n < nch)
+                    for (int j = 0; j < cols; ++j)
+                        o[(long long)n * TCC * a.H * a.dv + j] = __float2bfloat16(__int_as_float(0x7fc00000));
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (s_abort)
+            for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
+                (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
+        (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free<512>(tmem);
+    }
+}
+
+// Packed sequences without a row: their final state is their first.
+__global__ void __launch_bounds__(256) la_empty_kernel(LaChunks ch, long long HE, const float *first, float *last)
+{
+    const int seq = blockIdx.x;
+    if (ch.coff[seq + 1] != ch.coff[seq]) return;
+    for (long long i = (long long)blockIdx.y * 256 + threadIdx.x; i < HE; i += (long long)gridDim.y * 256)
+        last[seq * HE + i] = first ? first[seq * HE + i] : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// (features, heads, rows of a sequence, sequences) of a token tensor with rows
+// ld elements apart, in boxes of 64 features of one head and 128 rows.
+bool token_map(CUtensorMap *m, const void *p, int d, int heads, long long ld, const LaArgs &a)
+{
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const uint64_t T = (uint64_t)a.T, B = a.cu ? 1u : (uint64_t)a.B;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)heads, T, B};
+    cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * T};
+    cuuint32_t box[4] = {64u, 1u, (cuuint32_t)TCC, 1u};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Chunks of a segment: whole sequences where their blocks fill the GPU, else
+// as many equal segments as make the fewest idle SMs of whole waves (one block
+// an SM), of four chunks at least, since a segment's first state costs a pass
+// over its k and v.
+int seg_chunks(const LaArgs &a, int per_item)
+{
+    const int nc = (a.T - 1) / TCC + 1;
+    if (a.cu) return nc > 16 ? 16 : nc;
+    const long long base = (long long)a.B * per_item;
+    if (base >= 120 || nc < 8) return nc;
+    int best = nc;
+    double best_t = 1e300;
+    for (int n = 1; n <= nc / 4 && n <= 64; ++n) {
+        const int len = (nc + n - 1) / n;
+        const long long waves = (base * n + 147) / 148;
+        // the pass for the first states costs about two thirds of a segment
+        const double t = (double)waves * len * (n > 1 ? 1.67 : 1.0);
+        if (t < best_t) {
+            best_t = t;
+            best = len;
+        }
+    }
+    return best;
+}
+
+struct FwdWs {
+    char *table, *seg_table;
+    float *states, *tot;
+    size_t bytes;
+};
+
+FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
+{
+    FwdWs w{};
+    char *p = static_cast<char *>(ws);
+    auto take = [&](size_t n) {
+        char *r = p;
+        p += up256(n);
+        return r;
+    };
+    w.table = take(la_table_bytes(a));
+    w.seg_table = take(la_table_bytes(a));
+    if (L < (a.T - 1) / TCC + 1) {
+        const size_t items = (size_t)la_chunk_bound(a, L * TCC);
+        w.states = reinterpret_cast<float *>(take(4 * items * a.H * a.dk * a.dv));
+        w.tot = reinterpret_cast<float *>(take(4 * items * a.H));
+    }
+    w.bytes = (size_t)(p - static_cast<char *>(ws));
+    return w;
+}
+
+template <int DK>
+cudaError_t launch_state(const CUtensorMap *m, const TcArgs &g0, const TcArgs &g1, int dirs, cudaStream_t st)
+{
+    const int bytes = StateShared<DK>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, dirs);
+    la_state_kernel<DK><<<grid, 224, bytes, st>>>(m[0], m[1], m[2], m[3], g0, g1);
+    return cudaGetLastError();
+}
+
+template <int DK>
+cudaError_t launch_forward(const CUtensorMap *m, const TcArgs &g, cudaStream_t st)
+{
+    const int bytes = FwdShared<DK>::BYTES;
+    cudaError_t e = cudaFuncSetAttribute(la_forward_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    la_forward_kernel<DK>
+        <<<(unsigned)g.seg.total * g.a.H * g.tiles, FWD_THREADS, bytes, st>>>(m[0], m[1], m[2], g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool la_tc_takes(const LaArgs &a)
+{
+    return a.dtype == SLSTM_BF16 && a.dk <= 128 && a.dv <= 128 && a.dk % 8 == 0 && a.dv % 8 == 0 && a.ldq % 8 == 0 &&
+           a.ldk % 8 == 0 && a.ldv % 8 == 0;
+}
+
+size_t la_tc_forward_workspace(const LaArgs &a)
+{
+    return fwd_layout(a, seg_chunks(a, a.H * ((a.dv + 63) / 64)), reinterpret_cast<void *>((uintptr_t)256)).bytes;
+}
+
+cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    TcArgs g{};
+    g.a = a;
+    g.tiles = (a.dv + 63) / 64;
+    const int L = seg_chunks(a, a.H * g.tiles);
+    const FwdWs w = fwd_layout(a, L, ws);
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
+    if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    if (e != cudaSuccess) return e;
+    CUtensorMap m[4];
+    if (!token_map(&m[0], a.q, a.dk, a.Hqk, a.ldq, a) || !token_map(&m[1], a.k, a.dk, a.Hqk, a.ldk, a) ||
+        !token_map(&m[2], a.v, a.dv, a.H, a.ldv, a))
+        return cudaErrorInvalidValue;
+    g.first = a.s0;
+    g.last = a.sT;
+    if (w.states) {
+        TcArgs s = g;
+        s.first = nullptr;
+        s.last = nullptr;
+        s.fin = w.states;
+        s.fin_tot = w.tot;
+        const CUtensorMap ms[4] = {m[1], m[2], m[1], m[2]};
+        e = a.dk <= 64 ? launch_state<64>(ms, s, s, 1, st) : launch_state<128>(ms, s, s, 1, st);
+        if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st);
+        if (e != cudaSuccess) return e;
+        g.init = w.states;
+        g.last = nullptr;
+    } else if (a.cu && a.sT) {
+        const long long HE = (long long)a.H * a.dk * a.dv;
+        la_empty_kernel<<<dim3(a.B, (unsigned)min((HE + 1023) / 1024, 64LL)), 256, 0, st>>>(g.seg, HE, a.s0, a.sT);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return a.dk <= 64 ? launch_forward<64>(m, g, st) : launch_forward<128>(m, g, st);
+}
+
+}  // namespace slstm

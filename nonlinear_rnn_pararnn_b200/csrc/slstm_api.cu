@@ -92,7 +92,7 @@ bool la_sizes_ok(const slstm_linear_attention_config *c, int B, int T, bool pack
     if (c->ld_q > kIndexLimit || c->ld_k > kIndexLimit || c->ld_v > kIndexLimit) return false;
     const long long rows = packed ? (long long)T : (long long)B * T;
     const long long chunks = packed ? (long long)T / 64 + B : (long long)B * ((T + 63LL) / 64);
-    return rows <= kIndexLimit && chunks * c->H <= kIndexLimit && (long long)B * c->H <= kIndexLimit;
+    return rows <= kIndexLimit - 256 && chunks * c->H * 4 <= kIndexLimit;
 }
 
 bool la_elem_aligned(const void *p, int dtype)
@@ -125,7 +125,12 @@ LaArgs la_args(const void *q, const void *k, const void *v, const float *g, cons
     return a;
 }
 
-size_t la_workspace(const LaArgs &a, bool backward) { return la_simt_workspace(a, backward); }
+// The tensor cores take a call by its sizes and strides alone; what they then
+// need of the pointers is refused, not worked around.
+size_t la_workspace(const LaArgs &a, bool backward)
+{
+    return la_tc_takes(a) && !backward ? la_tc_forward_workspace(a) : la_simt_workspace(a, backward);
+}
 
 bool la_inputs_ok(const LaArgs &a)
 {
@@ -139,6 +144,10 @@ int la_forward(LaArgs a, void *o, float *sT, void *ws, size_t ws_bytes, slstm_st
     a.sT = sT;
     if (!la_inputs_ok(a) || !la_elem_aligned(o, a.dtype) || !aligned16_or_null(sT)) return SLSTM_ERR_INVALID_ARG;
     if (!ws_ok(ws, ws_bytes, la_workspace(a, false))) return SLSTM_ERR_INVALID_ARG;
+    if (la_tc_takes(a)) {
+        if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(o)) return SLSTM_ERR_INVALID_ARG;
+        return cuda_status(la_tc_forward(a, ws, static_cast<cudaStream_t>(stream)));
+    }
     return cuda_status(la_simt_forward(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
@@ -229,7 +238,8 @@ const char *slstm_check_site_file(int file_id)
 {
     static const char *const names[] = {nullptr,         "newton.cu", "backward.cu", "scan.cu",  "sequential.cu",
                                         "varlen.cu",     "decode.cu", "head.cu",     "block.cu", "gemm_simt.cu",
-                                        "scan_noalloc.cu", "linear_attention.cu", "layer_norm.cu"};
+                                        "scan_noalloc.cu", "linear_attention.cu", "layer_norm.cu",
+                                        "linear_attention_tc.cu"};
     if (file_id < 1 || file_id >= (int)(sizeof(names) / sizeof(names[0]))) return nullptr;
     return names[file_id];
 }
@@ -553,8 +563,9 @@ size_t slstm_linear_attention_workspace_size(const slstm_linear_attention_config
 {
     if (!la_sizes_ok(cfg, B, T, packed != 0)) return 0;
     static const int any = 0;   // a packed call's workspace depends on there being offsets, not on them
-    return la_workspace(la_args(nullptr, nullptr, nullptr, nullptr, nullptr, *cfg, B, T, packed ? &any : nullptr),
-                        backward != 0);
+    const size_t n = la_workspace(
+        la_args(nullptr, nullptr, nullptr, nullptr, nullptr, *cfg, B, T, packed ? &any : nullptr), backward != 0);
+    return n < 256 ? 256 : n;
 }
 
 int slstm_linear_attention_forward(const void *q, const void *k, const void *v, const float *g, const float *s0,
