@@ -28,6 +28,7 @@ namespace {
 constexpr int TCC = 128;                     // rows of a chunk
 constexpr uint32_t BOX = TCC * 128;          // bytes of 128 rows of 64 bf16
 constexpr uint64_t TC_WAIT_NS = 1000000000ull;
+constexpr int ND = 4;                        // chunks whose decays are held
 
 // Blocks of one pass: a segment (a run of chunks of one sequence) of one head
 // and 64 columns of the state.
@@ -46,15 +47,20 @@ struct TcArgs {
     bool back;                // from the end: (q, dO) in place of (k, v)
 };
 
-struct TcDecays {
-    double cum[TCC];
-    double blk[4];        // cum of the first row of each 32
-    float loc[TCC];       // cum - blk of its 32
+// The decays of a chunk.  D_ij = e^{c_i - c_j} of rows i in 32-row block q and
+// j in an earlier one is rq[i] cq[q - 1][j], by way of the block's first row
+// (both factors are at most 1 where nothing grows): one exponential a row and
+// three a column in place of one an element.  Inside a block it is the
+// exponential of loc[i] - loc[j].
+struct alignas(16) TcDecays {
+    float loc[TCC];       // c_i less that of the first row of its 32
     int first[TCC];
     float row[TCC], col[TCC];
+    float rq[TCC];        // e^{loc}, 0 behind a row of the block that clears
+    float cq[3][96];      // [q - 1][j], j < 32 q; 0 where the state is cleared after j, up to row 32 q
     float tot;
-    int pad;
 };
+static_assert(sizeof(TcDecays) % 16 == 0, "an array of them in shared memory, read 16 bytes at a time");
 
 SLSTM_DEVINL float ex2(float x)
 {
@@ -75,20 +81,39 @@ SLSTM_DEVINL float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); 
 // Byte offset of 16-byte piece p of a row in a 128-byte-swizzled box.
 SLSTM_DEVINL uint32_t swz(int row, int p) { return (uint32_t)row * 128u + (uint32_t)((p ^ (row & 7)) << 4); }
 
-// One wait of a whole warp: every lane the same answer; false once this block
-// has given up.
-SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+// The first 1024-byte boundary in dynamic shared memory, by an offset: a pointer
+// that goes through an integer is no longer known to be shared memory, and every
+// access through it becomes a generic one (564 us where this takes 170 us).
+SLSTM_DEVINL uint8_t *aligned_smem(uint8_t *raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
+
+// Wait for a phase of an mbarrier: the hardware suspends the thread in each try
+// (for up to about the hinted time), and the tries are counted, which costs the
+// waiting warps' neighbours less than reading a clock.  False after the last, or
+// once this block has given up.
+SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
 {
-    const bool ok = !*(volatile int *)s_abort && mbar_wait(bar, parity, TC_WAIT_NS);
-    if (__all_sync(0xffffffffu, ok)) return true;
+    const uint32_t addr = smem_u32(bar);
+    for (int i = 0; i < (1 << 20); ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n"
+            " .reg .pred p;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (*(volatile int *)s_abort) return false;
+    }
     *(volatile int *)s_abort = 1;
     return false;
 }
-SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+// One wait of a whole warp: every lane the same answer.
+SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, int *s_abort)
 {
-    if (!*(volatile int *)s_abort && mbar_wait(bar, parity, TC_WAIT_NS)) return true;
-    *(volatile int *)s_abort = 1;
-    return false;
+    return __all_sync(0xffffffffu, lane_wait(bar, parity, s_abort));
 }
 
 // The warp's shared-memory writes (and its reads of tensor memory) before the
@@ -99,43 +124,121 @@ SLSTM_DEVINL void warp_arrive(uint64_t *bar)
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The decays of a chunk by one warp into `d`.
-SLSTM_DEVINL void tc_decays(TcDecays &d, const LaArgs &a, long long row, int len, int h, int lane)
+// The log decays of a lane's four rows 4 l .. of a chunk; 0 behind `len`.
+SLSTM_DEVINL void load_decays(float (&gv)[4], const LaArgs &a, long long row, int len, int h, int lane)
 {
-    la_decays<4>(a.g, a.per_head ? h : row * a.H + h, a.per_head ? 0 : a.H, len, lane, d.cum, d.first, d.row, d.col,
-                 &d.tot);
-    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = lane * 4 + i;
-        d.loc[t] = (float)(d.cum[t] - d.cum[t & ~31]);
+        gv[i] = t < len ? __ldg(a.g + (a.per_head ? h : (row + t) * a.H + h)) : 0.0f;
     }
-    if (lane < 4) d.blk[lane] = d.cum[lane * 32];
 }
 
-// Row t of a 64-column box of v (or dO) times w as two bf16 terms into the
-// boxes at hi and lo; zero where !on.
-SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, float w, bool on)
+// The decays of a chunk by one warp into `d` (la_decays for the fields there).
+// The sums run in 64 bits; what is left of them once the 32-row block's first
+// row is taken off is fp32.
+SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
 {
+    constexpr uint32_t ALL = 0xffffffffu;
+    double c[4], run = 0.0;
+    int f[4], last = -1;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        const uint32_t o = swz(t, p);
-        uint4 h = make_uint4(0, 0, 0, 0), l = h;
-        if (on) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src + o);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            uint32_t y[4], z[4];
+    for (int i = 0; i < 4; ++i) {
+        if (la_clears(gv[i])) last = lane * 4 + i;
+        else run += (double)gv[i] * 1.4426950408889634074;
+        c[i] = run;
+        f[i] = last;
+    }
+    double pre = run;
+    int pf = last;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
-                y[i] = pack2(a, b);
-                z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
-            }
-            h = make_uint4(y[0], y[1], y[2], y[3]);
-            l = make_uint4(z[0], z[1], z[2], z[3]);
+    for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(ALL, pre, o);
+        const int w = __shfl_up_sync(ALL, pf, o);
+        if (lane >= o) {
+            pre += u;
+            pf = max(pf, w);
         }
-        *reinterpret_cast<uint4 *>(hi + o) = h;
-        *reinterpret_cast<uint4 *>(lo + o) = l;
+    }
+    const double all = __shfl_sync(ALL, pre, 31);
+    const int allf = __shfl_sync(ALL, pf, 31);
+    double before = __shfl_up_sync(ALL, pre, 1);
+    int bf = __shfl_up_sync(ALL, pf, 1);
+    if (lane == 0) {
+        before = 0.0;
+        bf = -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] += before;
+        f[i] = max(bf, f[i]);
+    }
+    const double base = __shfl_sync(ALL, c[0], lane & 24);   // of the block's first row
+    const int b = 32 * (lane >> 3);
+    const float to_base = (float)base, to_end = (float)(all - base);
+    float to_q[3];
+    int fq[3];
+#pragma unroll
+    for (int q = 1; q < 4; ++q) {
+        to_q[q - 1] = (float)(__shfl_sync(ALL, c[0], 8 * q) - base);
+        fq[q - 1] = __shfl_sync(ALL, f[0], 8 * q);
+    }
+    float loc[4], row[4], col[4], rq[4];
+    int4 fi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = lane * 4 + i;
+        loc[i] = (float)(c[i] - base);
+        row[i] = f[i] >= 0 ? 0.0f : ex2(to_base + loc[i]);
+        col[i] = allf > t ? 0.0f : ex2(to_end - loc[i]);
+        rq[i] = f[i] > b ? 0.0f : ex2(loc[i]);
+    }
+    fi = make_int4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4 *>(d.loc + lane * 4) = make_float4(loc[0], loc[1], loc[2], loc[3]);
+    *reinterpret_cast<float4 *>(d.row + lane * 4) = make_float4(row[0], row[1], row[2], row[3]);
+    *reinterpret_cast<float4 *>(d.col + lane * 4) = make_float4(col[0], col[1], col[2], col[3]);
+    *reinterpret_cast<float4 *>(d.rq + lane * 4) = make_float4(rq[0], rq[1], rq[2], rq[3]);
+    *reinterpret_cast<int4 *>(d.first + lane * 4) = fi;
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+        if (b < 32 * q) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = fq[q - 1] > lane * 4 + i ? 0.0f : ex2(to_q[q - 1] - loc[i]);
+            *reinterpret_cast<float4 *>(&d.cq[q - 1][lane * 4]) = make_float4(e[0], e[1], e[2], e[3]);
+        }
+    if (lane == 0) d.tot = allf >= 0 ? 0.0f : ex2((float)all);
+}
+
+// Half of row t of a 64-column box of v (or dO) times w as two bf16 terms into
+// the boxes at hi and lo; zero where !on.
+SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int half, float w, bool on)
+{
+    uint4 v[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        v[p] = *reinterpret_cast<const uint4 *>(src + swz(t, 4 * half + p));
+        if (!on) v[p] = make_uint4(0, 0, 0, 0);
+    }
+    uint4 h[4], l[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
+        uint32_t y[4], z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
+            y[i] = pack2(a, b);
+            z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
+        }
+        h[p] = make_uint4(y[0], y[1], y[2], y[3]);
+        l[p] = make_uint4(z[0], z[1], z[2], z[3]);
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t o = swz(t, 4 * half + p);
+        *reinterpret_cast<uint4 *>(hi + o) = h[p];
+        *reinterpret_cast<uint4 *>(lo + o) = l[p];
     }
 }
 
@@ -168,16 +271,32 @@ SLSTM_DEVINL bool seg_of(const TcArgs &g, int i, Seg *s)
     return true;
 }
 
-// The thread's share of a state tile of DK rows and 64 columns in registers:
-// with DK = 128 a row of 64; with DK = 64 the accumulator's lanes 64..127
-// repeat lanes 0..63 (the MMA is given its 64 rows twice), and a thread holds
-// 32 columns.
+// The share of a thread of eight warps (two on each quarter of the
+// accumulator's lanes) in a state tile of DK rows and 64 columns: with DK = 128
+// half a row; with DK = 64 lanes 64..127 repeat lanes 0..63 (the MMA is given
+// its 64 rows twice), and a thread holds a quarter.
 template <int DK>
 struct Share {
-    static constexpr int N = DK == 128 ? 64 : 32;
-    SLSTM_DEVINL static int row(int warp, int lane) { return (DK == 128 ? warp : (warp & 1)) * 32 + lane; }
-    SLSTM_DEVINL static int col(int warp) { return DK == 128 ? 0 : 32 * (warp >> 1); }
+    static constexpr int N = DK == 128 ? 32 : 16;
+    SLSTM_DEVINL static int row(int warp, int lane) { return (DK == 128 ? warp & 3 : warp & 1) * 32 + lane; }
+    SLSTM_DEVINL static int col(int warp) { return 32 * (warp >> 2) + (DK == 128 ? 0 : 16 * ((warp >> 1) & 1)); }
 };
+
+// S <- tot S + the sum of the two accumulators at `at` and 64 columns on.
+SLSTM_DEVINL void state_add(float (&S)[32], float tot, uint32_t at)
+{
+    float v[32], w[32];
+    tmem_ld32x2(at, at + 64, v, w);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) S[i] = fmaf(tot, S[i], v[i] + w[i]);
+}
+SLSTM_DEVINL void state_add(float (&S)[16], float tot, uint32_t at)
+{
+    float v[16], w[16];
+    tmem_ld16x2(at, at + 64, v, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) S[i] = fmaf(tot, S[i], v[i] + w[i]);
+}
 
 template <int N>
 SLSTM_DEVINL void state_load(float (&S)[N], const float *src, int dk, int dv, int r, int col)
@@ -210,9 +329,9 @@ SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, i
 //   S <- e^{c_C} S + X^T (w Y):  X = k, Y = v, w = e^{c_C - c_j} (forward)
 //                                X = q, Y = dO, w = scale e^{c_i} (from the end)
 // and writes the state that each chunk starts from (two bf16 terms, for the
-// backward kernel) and / or the final one.  Warps 0-3 scale Y and hold the
-// state (lane = row of d_k), warp 4 loads (a ring of NST chunks), warp 5 issues
-// the MMAs, warp 6 computes the decays.  Bound: the bytes of X and Y and of the
+// backward kernel) and / or the final one.  Warps 0-7 scale Y and hold the
+// state (lane = row of d_k), warp 8 loads (a ring of NST chunks), warp 9 issues
+// the MMAs, warps 10 and 11 compute the decays of every other chunk each.  Bound: the bytes of X and Y and of the
 // states written.
 // ---------------------------------------------------------------------------
 template <int DK>
@@ -222,11 +341,11 @@ struct StateShared {
     static constexpr uint32_t STAGE = (NB + 1) * BOX;
     static constexpr uint32_t Y = NST * STAGE;          // two buffers of hi, lo
     static constexpr uint32_t DEC = Y + 4 * BOX;
-    static constexpr uint32_t BYTES = DEC + 3 * sizeof(TcDecays) + 1024;
+    static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 
 template <int DK>
-__global__ void __launch_bounds__(224, 1)
+__global__ void __launch_bounds__(384, 1)
     la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
                     const __grid_constant__ CUtensorMap mx2, const __grid_constant__ CUtensorMap my2, TcArgs g0,
                     TcArgs g1)
@@ -234,9 +353,9 @@ __global__ void __launch_bounds__(224, 1)
     typedef StateShared<DK> SM;
     constexpr int NST = SM::NST;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
-    __shared__ uint64_t full[NST], empty[NST], dfull[3], dempty[3], yready[2], delta[2], fin;
+    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
     // blockIdx.y picks the direction where both run in one launch
@@ -253,12 +372,12 @@ __global__ void __launch_bounds__(224, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 4);
+            mbar_init(&dempty[i], 8);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&yready[i], 4);
+            mbar_init(&yready[i], 8);
             mbar_init(&delta[i], 1);
         }
         mbar_init(&fin, 1);
@@ -266,7 +385,7 @@ __global__ void __launch_bounds__(224, 1)
         s_abort = 0;
         s_loaded = 0;
     }
-    if (warp == 0) tmem_alloc<128>(&s_tmem);
+    if (warp == 0) tmem_alloc<256>(&s_tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -276,7 +395,7 @@ __global__ void __launch_bounds__(224, 1)
     auto chunk = [&](int n) { return back ? nch - 1 - n : n; };
     auto rows = [&](int n) { return min(TCC, sg.len - chunk(n) * TCC); };
 
-    if (warp == 4) {
+    if (warp == 8) {
         if (lane == 0) {
             const int hq = h / (a.H / a.Hqk);
             int n = 0;
@@ -292,9 +411,9 @@ __global__ void __launch_bounds__(224, 1)
             }
             s_loaded = n;
         }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16(128, 64, true, true);
+            constexpr uint32_t idesc = idesc_bf16(128, 128, true, true);
             for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
                 if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
@@ -302,25 +421,27 @@ __global__ void __launch_bounds__(224, 1)
                 tc_fence_after();
                 // the 64 rows of a narrow d_k twice: no step from one 64 to the next
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
-                const uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
+                // both terms of w Y side by side: X is read once for them
+                const uint64_t bd = smem_desc_mn_sw128(smem_u32(smem + SM::Y + (n & 1) * 2 * BOX), BOX);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint64_t bd = smem_desc_mn_sw128(smem_u32(y + z * BOX), BOX);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_bf16(tmem + (n & 1) * 64, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, idesc,
-                                  (z > 0 || k > 0) ? 1u : 0u);
-                }
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16(tmem + (n & 1) * 128, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, idesc,
+                              k > 0 ? 1u : 0u);
                 umma_commit(&delta[n & 1]);
                 umma_commit(&empty[s]);
             }
             umma_commit(&fin);
         }
-    } else if (warp == 6) {
-        for (int n = 0; n < nch; ++n) {
-            if (!warp_wait(&dempty[n % 3], ((uint32_t)(n / 3) & 1u) ^ 1u, &s_abort)) break;
-            tc_decays(dec[n % 3], a, sg.row + (long long)chunk(n) * TCC, rows(n), h, lane);
-            warp_arrive(&dfull[n % 3]);
+    } else if (warp >= 10) {
+        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (warp - 10 < nch) load_decays(gn, a, sg.row + (long long)chunk(warp - 10) * TCC, rows(warp - 10), h, lane);
+        for (int n = warp - 10; n < nch; n += 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
+            if (n + 2 < nch) load_decays(gn, a, sg.row + (long long)chunk(n + 2) * TCC, rows(n + 2), h, lane);
+            if (!warp_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
+            tc_decays(dec[n % ND], gv, lane);
+            warp_arrive(&dfull[n % ND]);
         }
     } else {
         typedef Share<DK> SH;
@@ -334,16 +455,15 @@ __global__ void __launch_bounds__(224, 1)
         auto scale = [&](int n) -> bool {
             const int s = n % NST;
             if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
-            if (!warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort)) return false;
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) return false;
             uint8_t *st = smem + s * SM::STAGE;
-            const TcDecays &d = dec[n % 3];
-            const int t = threadIdx.x, len = rows(n);
+            const TcDecays &d = dec[n % ND];
+            const int t = (warp & 3) * 32 + lane, half = warp >> 2, len = rows(n);
             uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
-            scale_row(st + SM::NB * BOX, y, y + BOX, t, back ? a.scale * d.row[t] : d.col[t], t < len);
+            scale_row(st + SM::NB * BOX, y, y + BOX, t, half, back ? a.scale * d.row[t] : d.col[t], t < len);
             // rows behind a packed sequence belong to another one
             if (packed && t >= len)
-#pragma unroll
-                for (int i = 0; i < SM::NB; ++i) zero_row(st + i * BOX, t);
+                for (int i = half; i < SM::NB; i += 2) zero_row(st + i * BOX, t);
             tma_store_fence();
             warp_arrive(&yready[n & 1]);
             return true;
@@ -373,17 +493,11 @@ __global__ void __launch_bounds__(224, 1)
                 break;
             }
             tc_fence_after();
-            const float tot = dec[n % 3].tot;
+            const float tot = dec[n % ND].tot;
             run *= tot;
-#pragma unroll
-            for (int i = 0; i < SH::N; i += 32) {
-                float v[32];
-                tmem_ld32(tmem + (n & 1) * 64 + c0 + i + ((uint32_t)(warp * 32) << 16), v);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) S[i + j] = fmaf(tot, S[i + j], v[j]);
-            }
+            state_add(S, tot, tmem + (n & 1) * 128 + c0 + ((uint32_t)((warp & 3) * 32) << 16));
             tc_fence_before();
-            warp_arrive(&dempty[n % 3]);
+            warp_arrive(&dempty[n % ND]);
         }
         if (!ok) {
 #pragma unroll
@@ -409,7 +523,7 @@ __global__ void __launch_bounds__(224, 1)
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_free<128>(tmem);
+        tmem_free<256>(tmem);
     }
 }
 
@@ -417,12 +531,12 @@ __global__ void __launch_bounds__(224, 1)
 // The forward pass of a segment: one block walks the chunks of one head and 64
 // columns of v and does all of it while q, k and v are in shared memory, the
 // state in registers:
-//   warps 0-3   v times its decays (two bf16 terms), the state (lane = row of
+//   warps 0-7   v times its decays (two bf16 terms), the state (lane = row of
 //               d_k), the state's upper term into shared memory
-//   warps 4-7   the weights D (q k) from tensor memory and back as bf16
-//               (lane = query row), then the outputs
-//   warp 8      loads, a ring of NST chunks;  warp 9 issues the MMAs
-//   warp 10     the decays, up to three chunks ahead
+//   warps 8-15  the weights D (q k) from tensor memory and back as bf16
+//               (lane = query row, half of the keys each), then the outputs
+//   warp 16     loads, a ring of NST chunks;  warp 17 issues the MMAs
+//   warps 18-19 the decays of every other chunk each, up to three chunks ahead
 // A chunk's products: q k^T (128 x 128), then into one 64-column accumulator
 // each q S, D(q k) v (A from tensor memory) and k^T (w v).  The first of the
 // next chunk is issued before the last of this one, so that the tensor cores
@@ -436,11 +550,11 @@ struct FwdShared {
     static constexpr uint32_t Y = NST * STAGE;              // hi, lo
     static constexpr uint32_t S = Y + 2 * BOX;
     static constexpr uint32_t DEC = S + DK * 128;
-    static constexpr uint32_t BYTES = DEC + 3 * sizeof(TcDecays) + 1024;
+    static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
-constexpr int FWD_THREADS = 352;
+constexpr int FWD_THREADS = 640;
 
 template <int DK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -450,9 +564,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     typedef FwdShared<DK> SM;
     constexpr int NST = SM::NST;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
-    __shared__ uint64_t full[NST], empty[NST], dfull[3], dempty[3], scfull[2];
+    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], scfull[2];
     __shared__ uint64_t yready, delta, sready, sfree, pready, ofull, oempty, tready, fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
@@ -467,19 +581,19 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 8);
+            mbar_init(&dempty[i], 16);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
-        mbar_init(&yready, 4);
+        mbar_init(&yready, 8);
         mbar_init(&delta, 1);
-        mbar_init(&sready, 4);
+        mbar_init(&sready, 8);
         mbar_init(&sfree, 1);
-        mbar_init(&pready, 4);
+        mbar_init(&pready, 8);
         mbar_init(&ofull, 1);
-        mbar_init(&oempty, 4);
-        mbar_init(&tready, 4);
+        mbar_init(&oempty, 8);
+        mbar_init(&tready, 8);
         mbar_init(&fin, 1);
         mbar_init_fence();
         s_abort = 0;
@@ -495,7 +609,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     // the last chunk of a packed sequence holds rows of the next one
     const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             const int hq = h / (a.H / a.Hqk);
             int n = 0;
@@ -514,15 +628,21 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             s_loaded = n;
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         if (lane == 0) {
             constexpr uint32_t id_qk = idesc_bf16(128, 128, false, false);
-            constexpr uint32_t id_kv = idesc_bf16(128, 64, true, true);
+            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
-            auto scores = [&](int n) -> bool {
+            // q k^T of chunk n; unless `must`, only if its rows are there
+            int scored = 0;
+            auto scores = [&](int n, bool must) -> bool {
                 const int s = n % NST;
+                if (!must && (!mbar_try_wait(&full[s], (uint32_t)(n / NST) & 1u) ||
+                              (n == ragged && !mbar_try_wait(&tready, 0u))))
+                    return true;
                 if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
                 if (n == ragged && !lane_wait(&tready, 0u, &s_abort)) return false;
+                scored = n + 1;
                 tc_fence_after();
                 const uint8_t *st = smem + s * SM::STAGE;
 #pragma unroll
@@ -536,26 +656,21 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 umma_commit(&scfull[n & 1]);
                 return true;
             };
-            bool ok = scores(0);
+            bool ok = true;
             for (int n = 0; n < nch && ok; ++n) {
                 const int s = n % NST;
                 const uint32_t ph = (uint32_t)n & 1u;
                 const uint8_t *st = smem + s * SM::STAGE;
-                ok = lane_wait(&yready, ph, &s_abort);
+                ok = (scored > n || scores(n, true)) && lane_wait(&yready, ph, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t kt = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), DK == 128 ? BOX : 0u);
+                // both terms of w v side by side: k is read once for them
+                const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y + z * BOX), BOX);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv,
-                                  (z > 0 || k > 0) ? 1u : 0u);
-                }
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
                 umma_commit(&delta);
-                if (n + 1 < nch) ok = scores(n + 1);
-                if (!ok) break;
                 ok = lane_wait(&sready, ph, &s_abort) && lane_wait(&oempty, ph ^ 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
@@ -568,27 +683,41 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         umma_bf16(t_o1, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&sfree);
+                // the next chunk's scores go ahead of this one's last product
+                // when its rows have come, and never make it wait
+                if (n + 1 < nch) {
+                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !mbar_try_wait(&pready, ph); ++i) scores(n + 1, false);
+                }
                 ok = lane_wait(&pready, ph, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 8 * k, vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
+                    umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
                 umma_commit(&ofull);
                 umma_commit(&empty[s]);
             }
             umma_commit(&fin);
         }
-    } else if (warp == 10) {
-        for (int n = 0; n < nch; ++n) {
-            if (!warp_wait(&dempty[n % 3], ((uint32_t)(n / 3) & 1u) ^ 1u, &s_abort)) break;
-            tc_decays(dec[n % 3], a, sg.row + (long long)n * TCC, min(TCC, sg.len - n * TCC), h, lane);
-            warp_arrive(&dfull[n % 3]);
+    } else if (warp >= 18) {
+        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto load = [&](int n) {
+            if (n < nch) load_decays(gn, a, sg.row + (long long)n * TCC, min(TCC, sg.len - n * TCC), h, lane);
+        };
+        load(warp - 18);
+        for (int n = warp - 18; n < nch; n += 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
+            load(n + 2);
+            if (!warp_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
+            tc_decays(dec[n % ND], gv, lane);
+            warp_arrive(&dfull[n % ND]);
         }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         typedef Share<DK> SH;
-        const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0, t = threadIdx.x;
+        const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
+        const int t = (warp & 3) * 32 + lane, half = warp >> 2;
         const long long E = (long long)a.dk * a.dv;
         const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
                                   : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
@@ -606,8 +735,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort);
                 if (!ok) break;
                 if (t >= len)
-#pragma unroll
-                    for (int i = 0; i < 2 * SM::NB + 1; ++i) zero_row(st + i * BOX, t);
+                    for (int i = half; i < 2 * SM::NB + 1; i += 2) zero_row(st + i * BOX, t);
                 tma_store_fence();
                 warp_arrive(&tready);
             }
@@ -622,71 +750,80 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             tma_store_fence();
             warp_arrive(&sready);
             ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
-                 warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort);
+                 warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
             if (!ok) break;
-            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, dec[n % 3].col[t], t < len);
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, half, dec[n % ND].col[t], t < len);
             tma_store_fence();
             warp_arrive(&yready);
             ok = warp_wait(&delta, ph, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            const float tot = dec[n % 3].tot;
-#pragma unroll
-            for (int i = 0; i < SH::N; i += 32) {
-                float v[32];
-                tmem_ld32(t_delta + c0 + i + ((uint32_t)(warp * 32) << 16), v);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) S[i + j] = fmaf(tot, S[i + j], v[j]);
-            }
+            const float tot = dec[n % ND].tot;
+            state_add(S, tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
             tc_fence_before();
-            warp_arrive(&dempty[n % 3]);
+            warp_arrive(&dempty[n % ND]);
         }
         if (!ok)
 #pragma unroll
             for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
         if (g.last) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
     } else {
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp >> 2) & 1;
         const int i = q * 32 + lane;   // query row
         const uint32_t la = (uint32_t)(q * 32) << 16;
+        const int col = tile * 64 + 32 * half, cols = min(32, a.dv - col);
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
-                           (long long)h * a.dv + tile * 64;
-        const int cols = min(64, a.dv - tile * 64);
+                           (long long)h * a.dv + col;
+        // the keys of 32-row block b, this thread's query: weights of v in place of w
+        auto weigh = [&](const TcDecays &d, int b, const float (&v)[32], uint32_t (&p)[16]) {
+            if (b < q) {
+                const float ri = d.rq[i];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 e = *reinterpret_cast<const float4 *>(&d.cq[q - 1][32 * b + j]);
+                    p[j / 2] = pack2(v[j] * (ri * e.x), v[j + 1] * (ri * e.y));
+                    p[j / 2 + 1] = pack2(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w));
+                }
+            } else {
+                const float li = d.loc[i];
+                const int f = max(d.first[i] - 32 * q, 0);
+                const uint32_t span = (uint32_t)(lane - f);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 l = *reinterpret_cast<const float4 *>(&d.loc[32 * b + j]);
+                    const float e[4] = {ex2(li - l.x), ex2(li - l.y), ex2(li - l.z), ex2(li - l.w)};
+                    float x[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) x[z] = (uint32_t)(j + z - f) <= span ? v[j + z] * e[z] : 0.0f;
+                    p[j / 2] = pack2(x[0], x[1]);
+                    p[j / 2 + 1] = pack2(x[2], x[3]);
+                }
+            }
+        };
         bool ok = true;
         int n = 0;
         for (; n < nch; ++n) {
             const uint32_t ph = (uint32_t)n & 1u;
-            ok = warp_wait(&dfull[n % 3], (uint32_t)(n / 3) & 1u, &s_abort) &&
+            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) &&
                  warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            const TcDecays &d = dec[n % 3];
-            const uint32_t sc = tmem + (n & 1) * 128 + la;
-            const double ci = d.cum[i];
-            const int f = max(d.first[i], 0);
-            const uint32_t span = (uint32_t)(i - f);
+            const TcDecays &d = dec[n % ND];
             const float rowc = d.row[i] * a.scale;
+            // 64 keys of this warp; their bf16 weights over the first half of their scores
+            const uint32_t sc = tmem + (n & 1) * 128 + 64 * half + la;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int z = 0; z < 2; ++z) {
                 uint32_t p[16];
-                if (b <= q) {
+                if (2 * half + z <= q) {
                     float v[32];
-                    tmem_ld32(sc + 32 * b, v);
-                    const float rb = (float)(ci - d.blk[b]);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 l = *reinterpret_cast<const float2 *>(&d.loc[32 * b + j]);
-                        const float e0 = ex2(rb - l.x), e1 = ex2(rb - l.y);
-                        const float p0 = (uint32_t)(32 * b + j - f) <= span ? v[j] * e0 : 0.0f;
-                        const float p1 = (uint32_t)(32 * b + j + 1 - f) <= span ? v[j + 1] * e1 : 0.0f;
-                        p[j / 2] = pack2(p0, p1);
-                    }
+                    tmem_ld32(sc + 32 * z, v);
+                    weigh(d, 2 * half + z, v, p);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) p[j] = 0u;
                 }
-                // over the scores already read: column 16 b .. of 32 (b + 1)
-                tmem_st16(sc + 16 * b, p);
+                tmem_st16(sc + 16 * z, p);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -694,37 +831,29 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             ok = warp_wait(&ofull, ph, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            const bool on = n * TCC + i < sg.len;
+            float u[32], w[32];
+            tmem_ld32x2(t_o1 + la + 32 * half, t_o2 + la + 32 * half, u, w);
+            tc_fence_before();
+            warp_arrive(&oempty);
+            warp_arrive(&dempty[n % ND]);
+            if (n * TCC + i < sg.len) {
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                float u[32], w[32];
-                tmem_ld32(t_o1 + la + c, u);
-                tmem_ld32(t_o2 + la + c, w);
-                if (c == 32) {
-                    tc_fence_before();
-                    warp_arrive(&oempty);
-                    warp_arrive(&dempty[n % 3]);
-                }
-                if (on) {
+                for (int j = 0; j < 32; j += 8) {
+                    if (j >= cols) break;
+                    uint32_t y[4];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        if (c + j >= cols) break;
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            y[k] = pack2(fmaf(rowc, u[j + 2 * k], a.scale * w[j + 2 * k]),
-                                         fmaf(rowc, u[j + 2 * k + 1], a.scale * w[j + 2 * k + 1]));
-                        *reinterpret_cast<uint4 *>(o + (long long)n * TCC * a.H * a.dv + c + j) =
-                            make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        y[k] = pack2(fmaf(rowc, u[j + 2 * k], a.scale * w[j + 2 * k]),
+                                     fmaf(rowc, u[j + 2 * k + 1], a.scale * w[j + 2 * k + 1]));
+                    *reinterpret_cast<uint4 *>(o + (long long)n * TCC * a.H * a.dv + j) =
+                        make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
         }
         if (!ok)
-            for (; n * TCC + i < sg.len; ++n)
-                if (n < nch)
-                    for (int j = 0; j < cols; ++j)
-                        o[(long long)n * TCC * a.H * a.dv + j] = __float2bfloat16(__int_as_float(0x7fc00000));
+            for (; n < nch && n * TCC + i < sg.len; ++n)
+                for (int j = 0; j < cols; ++j)
+                    o[(long long)n * TCC * a.H * a.dv + j] = __float2bfloat16(__int_as_float(0x7fc00000));
     }
     tc_fence_before();
     __syncthreads();
@@ -778,7 +907,7 @@ bool token_map(CUtensorMap *m, const void *p, int d, int heads, long long ld, co
 int seg_chunks(const LaArgs &a, int per_item)
 {
     const int nc = (a.T - 1) / TCC + 1;
-    if (a.cu) return nc > 16 ? 16 : nc;
+    if (a.cu) return nc > 4 ? 4 : nc;
     const long long base = (long long)a.B * per_item;
     if (base >= 120 || nc < 8) return nc;
     int best = nc;
@@ -829,7 +958,7 @@ cudaError_t launch_state(const CUtensorMap *m, const TcArgs &g0, const TcArgs &g
     cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, dirs);
-    la_state_kernel<DK><<<grid, 224, bytes, st>>>(m[0], m[1], m[2], m[3], g0, g1);
+    la_state_kernel<DK><<<grid, 384, bytes, st>>>(m[0], m[1], m[2], m[3], g0, g1);
     return cudaGetLastError();
 }
 
