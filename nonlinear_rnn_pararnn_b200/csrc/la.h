@@ -65,6 +65,8 @@ cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, con
 bool la_tc_takes(const LaArgs &a);
 size_t la_tc_forward_workspace(const LaArgs &a);
 cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st);
+size_t la_tc_backward_workspace(const LaArgs &a);
+cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st);
 
 // Sums of the fp32 per-head partial gradients over the heads that share a
 // query and key head: out[row][hq][d] = sum over r of part[row][hq * rep + r][d].

@@ -43,7 +43,9 @@ struct TcArgs {
     float *fin;               // final states [segment][h], or null: last
     float *fin_tot;           // [segment][h] decay of a segment
     float *last;              // final states [sequence][h], or null
-    __nv_bfloat16 *hi, *lo;   // states that enter each chunk, [chunk][h] (dk x dv), or null
+    __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
+    const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
+    float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
     bool back;                // from the end: (q, dO) in place of (k, v)
 };
 
@@ -57,6 +59,7 @@ struct alignas(16) TcDecays {
     int first[TCC];
     float row[TCC], col[TCC];
     float rq[TCC];        // e^{loc}, 0 behind a row of the block that clears
+    uint32_t mask[TCC];   // rows of the row's 32 that it reaches: itself and those behind it, up to a clear
     float cq[3][96];      // [q - 1][j], j < 32 q; 0 where the state is cleared after j, up to row 32 q
     float tot;
 };
@@ -193,6 +196,20 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
         col[i] = allf > t ? 0.0f : ex2(to_end - loc[i]);
         rq[i] = f[i] > b ? 0.0f : ex2(loc[i]);
     }
+    // the block's rows that clear, then for each row the run up to the next of them
+    uint32_t clears = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) clears |= (f[i] == lane * 4 + i ? 1u : 0u) << ((lane * 4 + i) & 31);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) clears |= __shfl_xor_sync(ALL, clears, o);
+    uint32_t mk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t from = ~0u << ((lane * 4 + i) & 31);
+        const uint32_t next = clears & (from << 1);
+        mk[i] = from & (next ? (next & (0u - next)) - 1u : ~0u);
+    }
+    *reinterpret_cast<uint4 *>(d.mask + lane * 4) = make_uint4(mk[0], mk[1], mk[2], mk[3]);
     fi = make_int4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4 *>(d.loc + lane * 4) = make_float4(loc[0], loc[1], loc[2], loc[3]);
     *reinterpret_cast<float4 *>(d.row + lane * 4) = make_float4(row[0], row[1], row[2], row[3]);
@@ -346,9 +363,7 @@ struct StateShared {
 
 template <int DK>
 __global__ void __launch_bounds__(384, 1)
-    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
-                    const __grid_constant__ CUtensorMap mx2, const __grid_constant__ CUtensorMap my2, TcArgs g0,
-                    TcArgs g1)
+    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my, TcArgs g)
 {
     typedef StateShared<DK> SM;
     constexpr int NST = SM::NST;
@@ -358,9 +373,6 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
-    // blockIdx.y picks the direction where both run in one launch
-    const TcArgs &g = blockIdx.y ? g1 : g0;
-    const CUtensorMap *tx = blockIdx.y ? &mx2 : &mx, *ty = blockIdx.y ? &my2 : &my;
     const LaArgs &a = g.a;
     const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
     Seg sg;
@@ -406,8 +418,8 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_expect_tx(&full[s], SM::STAGE);
                 const int t = sg.t + chunk(n) * TCC;
 #pragma unroll
-                for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, tx, &full[s], 64 * i, hq, t, sg.b);
-                tma_load_4d(st + SM::NB * BOX, ty, &full[s], 64 * tile, h, t, sg.b);
+                for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, &mx, &full[s], 64 * i, hq, t, sg.b);
+                tma_load_4d(st + SM::NB * BOX, &my, &full[s], 64 * tile, h, t, sg.b);
             }
             s_loaded = n;
         }
@@ -487,6 +499,27 @@ __global__ void __launch_bounds__(384, 1)
                     *reinterpret_cast<uint4 *>(g.hi + at + i) = make_uint4(y[0], y[1], y[2], y[3]);
                     *reinterpret_cast<uint4 *>(g.lo + at + i) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
+            }
+            if (g.dot) {
+                float s = 0.0f;
+                if (r < a.dk) {
+                    const long long at = ((sg.c0 + chunk(n)) * a.H + h) * E + (long long)r * a.dv + col;
+#pragma unroll
+                    for (int i = 0; i < SH::N; i += 8) {
+                        if (col + i >= a.dv) break;
+                        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(g.phi + at + i));
+                        const uint4 z = __ldg(reinterpret_cast<const uint4 *>(g.plo + at + i));
+                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w}, zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            s = fmaf(S[i + 2 * j], lo_of(yy[j]) + lo_of(zz[j]), s);
+                            s = fmaf(S[i + 2 * j + 1], hi_of(yy[j]) + hi_of(zz[j]), s);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) g.dot[(((sg.c0 + chunk(n)) * a.H + h) * 2 + tile) * 8 + warp] = s;
             }
             if (!warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) {
                 ok = false;
@@ -870,6 +903,532 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     }
 }
 
+// ---------------------------------------------------------------------------
+// The gradients of a chunk and head, given the state that enters it and the
+// gradient of the state that leaves it (two bf16 terms each).  Persistent
+// blocks; item = chunk * H + head.  Everything with a key's row per lane:
+//   q k^T and dO v^T transposed (lane = key j, column = query i), from which
+//   come P_ij = scale D_ij (q_i . k_j), Pd_ij = scale D_ij (dO_i . v_j) and the
+//   row and column sums of W = P (dO v) for dg;  then
+//   dq = Pd k + scale e^{c_i} dO S^T,   dk = Pd^T q + e^{c_C - c_j} v dS^T,
+//   dv = P^T dO + e^{c_C - c_j} k dS
+// with P^T and Pd^T in shared memory (Pd^T read both ways round).  The products
+// with the states come first; their rows are scaled in tensor memory, where the
+// other products are then added (dv's stay apart).  u_i and w_j of dg are the
+// dot products of q_i and k_j with those rows.
+//   warps 0-15  lane quarter q = warp & 3, columns 32 b .. of b = warp >> 2
+//   warp 16     loads;  warp 17 MMAs;  warp 18 decays;  warp 19 dg
+// Tensor memory: [0, 128) q k^T, then k dS; [128, 256) dO v^T, then P^T dO;
+// [256, 384) dq; [384, 512) dk.  Shared memory holds q, k, v, dO and two 32 KB
+// buffers that take S, then dS, then P^T and Pd^T.  Bound: the bytes of q, k,
+// v, dO, the two states and the gradients.
+// ---------------------------------------------------------------------------
+struct BackArgs {
+    LaArgs a;
+    LaChunks ch;
+    int total;             // items where the sequences are dense
+    float *part_q, *part_k;
+    float *dgc;            // [chunk][h]
+    const float *dot;
+    int tiles;
+};
+
+template <int DK, int DV>
+struct BackShared {
+    static constexpr int NK = DK / 64, NV = DV / 64;
+    static constexpr uint32_t Q = 0, K = NK * BOX, V = 2 * NK * BOX, G = V + NV * BOX, X = G + NV * BOX;
+    static constexpr uint32_t DEC = X + 4 * BOX;
+    static constexpr uint32_t SUMS = DEC + 2 * sizeof(TcDecays);
+    // the parts of r, u, w of each column block and of c of each lane quarter's columns
+    static constexpr uint32_t BYTES = SUMS + 16 * TCC * 4 + 1024;
+};
+static_assert(BackShared<128, 128>::BYTES + 1024 <= 227 * 1024, "backward shared memory");
+
+constexpr int BACK_THREADS = 640;
+
+// A thread's 32 columns of a row in bf16 from a swizzled box pair.
+SLSTM_DEVINL float dot_row(const uint8_t *tile, int row, int b, const float (&v)[32])
+{
+    const uint8_t *box = tile + (b >> 1) * BOX;
+    float s = 0.0f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(box + swz(row, 4 * (b & 1) + p));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s = fmaf(lo_of(w[j]), v[8 * p + 2 * j], s);
+            s = fmaf(hi_of(w[j]), v[8 * p + 2 * j + 1], s);
+        }
+    }
+    return s;
+}
+
+// 32 columns of a row to bf16, `cols` of them.
+SLSTM_DEVINL void put_row(__nv_bfloat16 *p, const float (&v)[32], int cols)
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+        if (j >= cols) break;
+        *reinterpret_cast<uint4 *>(p + j) = make_uint4(pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]),
+                                                       pack2(v[j + 4], v[j + 5]), pack2(v[j + 6], v[j + 7]));
+    }
+}
+SLSTM_DEVINL void put_row(float *p, const float (&v)[32], int cols)
+{
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        if (j >= cols) break;
+        *reinterpret_cast<float4 *>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    }
+}
+
+template <int DK, int DV>
+__global__ void __launch_bounds__(BACK_THREADS, 1)
+    la_backward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
+                       const __grid_constant__ CUtensorMap msh, const __grid_constant__ CUtensorMap msl,
+                       const __grid_constant__ CUtensorMap mdh, const __grid_constant__ CUtensorMap mdl, BackArgs g)
+{
+    typedef BackShared<DK, DV> SM;
+    constexpr int NK = SM::NK, NV = SM::NV;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = aligned_smem(smem_raw);
+    TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
+    float(*sums)[TCC] = reinterpret_cast<float(*)[TCC]>(smem + SM::SUMS);   // r: 0-3, c: 4-7, u: 8-11, w: 12-15
+    uint8_t *x0 = smem + SM::X, *x1 = x0 + 2 * BOX;
+    __shared__ uint64_t full1, full2, fullS, fullD, dfull[2], dempty[2], bsc, bdqi, bdki, bx, scfree, pready, bout,
+        tfree, tready, sumfree, fin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_loaded;
+    const LaArgs &a = g.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool packed = g.ch.pos != nullptr;
+    const int items = packed ? g.ch.coff[g.ch.n_seq] * a.H : g.total;
+    if ((int)blockIdx.x >= items) return;
+    if (threadIdx.x == 0) {
+        mbar_init(&full1, 1);
+        mbar_init(&full2, 1);
+        mbar_init(&fullS, 1);
+        mbar_init(&fullD, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], 17);
+        }
+        mbar_init(&bsc, 1);
+        mbar_init(&bdqi, 1);
+        mbar_init(&bdki, 1);
+        mbar_init(&bx, 1);
+        mbar_init(&scfree, 16);
+        mbar_init(&pready, 16);
+        mbar_init(&bout, 1);
+        mbar_init(&tfree, 16);
+        mbar_init(&tready, 16);
+        mbar_init(&sumfree, 1);
+        mbar_init(&fin, 1);
+        mbar_init_fence();
+        s_abort = 0;
+        s_loaded = 0;
+    }
+    if (warp == 0) tmem_alloc<512>(&s_tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const uint32_t R0 = tmem, R1 = tmem + 128, R2 = tmem + 256, R3 = tmem + 384;
+    const int rep = a.H / a.Hqk;
+
+    if (warp == 16) {
+        if (lane == 0) {
+            constexpr uint32_t SB = DK * 128;   // bytes of a box of a state: DK rows, 64 columns
+            int it = 0;
+            for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+                const int h = item % a.H, c = item / a.H, hq = h / rep;
+                const LaChunk ck = la_chunk(g.ch, c);
+                const int t = packed ? (int)ck.row : ck.n * TCC, b = packed ? 0 : ck.seq;
+                const uint32_t ph = (uint32_t)it & 1u;
+                if (it > 0 && !lane_wait(&bout, ph ^ 1u, &s_abort)) break;
+                mbar_expect_tx(&full1, 2 * NK * BOX);
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    tma_load_4d(smem + SM::Q + i * BOX, &mq, &full1, 64 * i, hq, t, b);
+                    tma_load_4d(smem + SM::K + i * BOX, &mk, &full1, 64 * i, hq, t, b);
+                }
+                mbar_expect_tx(&full2, 2 * NV * BOX);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    tma_load_4d(smem + SM::V + i * BOX, &mv, &full2, 64 * i, h, t, b);
+                    tma_load_4d(smem + SM::G + i * BOX, &mg, &full2, 64 * i, h, t, b);
+                }
+                mbar_expect_tx(&fullS, 2 * NV * SB);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    tma_load_3d(x0 + i * SB, &msh, &fullS, 64 * i, 0, item);
+                    tma_load_3d(x1 + i * SB, &msl, &fullS, 64 * i, 0, item);
+                }
+                s_loaded = 2 * it + 1;
+                if (!lane_wait(&bdqi, ph, &s_abort)) break;
+                mbar_expect_tx(&fullD, 2 * NV * SB);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    tma_load_3d(x0 + i * SB, &mdh, &fullD, 64 * i, 0, item);
+                    tma_load_3d(x1 + i * SB, &mdl, &fullD, 64 * i, 0, item);
+                }
+                s_loaded = 2 * it + 2;
+            }
+        }
+    } else if (warp == 17) {
+        if (lane == 0) {
+            constexpr uint32_t id_ss = idesc_bf16(128, 128, false, false);   // q k^T, dO v^T
+            constexpr uint32_t id_si = idesc_bf16(128, DK, false, false);    // dO S^T, v dS^T
+            constexpr uint32_t id_kd = idesc_bf16(128, DV, false, true);     // k dS, P^T dO
+            constexpr uint32_t id_dk = idesc_bf16(128, DK, false, true);     // Pd^T q
+            constexpr uint32_t id_dq = idesc_bf16(128, DK, true, true);      // Pd k
+            constexpr uint32_t SB = DK * 128;
+            // A (128 rows) by B over 64 NB deep K-major tiles
+            auto inner = [&](uint32_t d, uint32_t at, uint32_t bt, uint32_t bstride, int nb, uint32_t id, bool add) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i >= nb) break;
+                    const uint64_t ad = smem_desc_k_sw128(at + i * BOX), bd = smem_desc_k_sw128(bt + i * bstride);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(d, ad + 2 * k, bd + 2 * k, id, (add || i > 0 || k > 0) ? 1u : 0u);
+                }
+            };
+            const uint32_t sm = smem_u32(smem), sx0 = smem_u32(x0), sx1 = smem_u32(x1);
+            int it = 0;
+            for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+                const uint32_t ph = (uint32_t)it & 1u;
+                if (!lane_wait(&full1, ph, &s_abort)) break;
+                if (packed) {
+                    // rows behind a ragged chunk are cleared before they are read
+                    if (!lane_wait(&tready, ph, &s_abort)) break;
+                }
+                if (it > 0 && !lane_wait(&tfree, ph ^ 1u, &s_abort)) break;
+                tc_fence_after();
+                inner(R0, sm + SM::K, sm + SM::Q, BOX, NK, id_ss, false);
+                if (!lane_wait(&full2, ph, &s_abort)) break;
+                tc_fence_after();
+                inner(R1, sm + SM::V, sm + SM::G, BOX, NV, id_ss, false);
+                umma_commit(&bsc);
+                if (!lane_wait(&fullS, ph, &s_abort)) break;
+                tc_fence_after();
+                inner(R2, sm + SM::G, sx0, SB, NV, id_si, false);
+                inner(R2, sm + SM::G, sx1, SB, NV, id_si, true);
+                umma_commit(&bdqi);
+                if (!lane_wait(&fullD, ph, &s_abort)) break;
+                tc_fence_after();
+                inner(R3, sm + SM::V, sx0, SB, NV, id_si, false);
+                inner(R3, sm + SM::V, sx1, SB, NV, id_si, true);
+                umma_commit(&bdki);
+                if (!lane_wait(&scfree, ph, &s_abort)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < NK; ++i) {
+                    const uint64_t ad = smem_desc_k_sw128(sm + SM::K + i * BOX);
+                    const uint64_t bd = smem_desc_mn_sw128(sx0 + i * 64 * 128, SB);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(R0, ad + 2 * k, bd + (2048u >> 4) * k, id_kd, (i > 0 || k > 0) ? 1u : 0u);
+                }
+                umma_commit(&bx);
+                if (!lane_wait(&pready, ph, &s_abort)) break;
+                tc_fence_after();
+                const uint64_t gd = smem_desc_mn_sw128(sm + SM::G, BOX), qd = smem_desc_mn_sw128(sm + SM::Q, BOX),
+                               kd = smem_desc_mn_sw128(sm + SM::K, BOX), pdt = smem_desc_mn_sw128(sx1, BOX);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t pt = smem_desc_k_sw128(sx0 + (k >> 2) * BOX) + 2 * (k & 3);
+                    umma_bf16(R1, pt, gd + (2048u >> 4) * k, id_kd, k > 0 ? 1u : 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t pt = smem_desc_k_sw128(sx1 + (k >> 2) * BOX) + 2 * (k & 3);
+                    umma_bf16(R3, pt, qd + (2048u >> 4) * k, id_dk, 1u);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16(R2, pdt + (2048u >> 4) * k, kd + (2048u >> 4) * k, id_dq, 1u);
+                umma_commit(&bout);
+            }
+            umma_commit(&fin);
+        }
+    } else if (warp == 18) {
+        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto load = [&](int item) {
+            if (item < items) {
+                const LaChunk ck = la_chunk(g.ch, item / a.H);
+                load_decays(gn, a, ck.row, ck.len, item % a.H, lane);
+            }
+        };
+        load(blockIdx.x);
+        int it = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
+            load(item + gridDim.x);
+            if (!warp_wait(&dempty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s_abort)) break;
+            tc_decays(dec[it & 1], gv, lane);
+            warp_arrive(&dfull[it & 1]);
+        }
+    } else if (warp == 19) {
+        // dg of four rows a lane from the parts of r, c, u, w, in 64 bits: the
+        // sums over the chunk cancel
+        int it = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+            const int h = item % a.H, c = item / a.H;
+            const uint32_t ph = (uint32_t)it & 1u;
+            if (!warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_abort)) break;
+            if (!warp_wait(&pready, ph, &s_abort)) break;
+            if (a.dg) {
+                const TcDecays &d = dec[it & 1];
+                const LaChunk ck = la_chunk(g.ch, c);
+                double x[4], w[4], xs = 0.0, ws = 0.0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = lane * 4 + i;
+                    double v = 0.0, y = 0.0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k <= (t >> 5)) v += sums[k][t];          // r: parts of the keys' blocks up to its own
+                        if (k >= (t >> 5)) v -= sums[4 + k][t];      // c: of the queries' blocks from its own
+                        if (k < DK / 32) {
+                            v += sums[8 + k][t];
+                            y += sums[12 + k][t];
+                        }
+                    }
+                    x[i] = v;
+                    w[i] = y;
+                    xs += v;
+                    ws += y;
+                }
+                const double xl = xs, wl = ws;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double xu = __shfl_down_sync(0xffffffffu, xs, o), wu = __shfl_up_sync(0xffffffffu, ws, o);
+                    if (lane + o < 32) xs += xu;
+                    if (lane >= o) ws += wu;
+                }
+                double dot = 0.0;
+                if (lane < 16 && lane / 8 < g.tiles) dot = g.dot[((long long)c * a.H + h) * 16 + lane];
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                dot = __shfl_sync(0xffffffffu, dot, 0) * (double)d.tot;
+                double back = xs - xl, front = ws - wl;   // rows behind this lane's, rows before
+                float out[4], sum = 0.0f;
+#pragma unroll
+                for (int i = 3; i >= 0; --i) {
+                    back += x[i];
+                    out[i] = (float)back;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = lane * 4 + i;
+                    float v = (float)((double)out[i] + front + dot);
+                    front += w[i];
+                    if (t >= ck.len || d.first[t] == t) v = 0.0f;   // nothing passes a row that clears the state
+                    if (t < ck.len && !a.per_head) a.dg[(ck.row + t) * a.H + h] = v;
+                    sum += v;
+                }
+                if (a.per_head) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) g.dgc[(long long)c * a.H + h] = sum;
+                }
+            }
+            warp_arrive(&sumfree);
+            warp_arrive(&dempty[it & 1]);
+        }
+    } else {
+        const int q = warp & 3, b = warp >> 2;
+        const int r = q * 32 + lane;                  // row: key or query
+        const uint32_t at = ((uint32_t)(q * 32) << 16) + 32 * b;
+        int it = 0;
+        bool ok = true;
+        LaChunk ck;
+        int h = 0;
+        for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+            const uint32_t ph = (uint32_t)it & 1u;
+            h = item % a.H;
+            ck = la_chunk(g.ch, item / a.H);
+            if (packed) {
+                ok = warp_wait(&full1, ph, &s_abort) && warp_wait(&full2, ph, &s_abort);
+                if (!ok) break;
+                if (r >= ck.len)
+                    for (int i = b; i < 2 * (NK + NV); i += 4) zero_row(smem + i * BOX, r);
+                tma_store_fence();
+                warp_arrive(&tready);
+            }
+            ok = warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_abort) && warp_wait(&bsc, ph, &s_abort);
+            if (ok && it > 0) ok = warp_wait(&sumfree, ph ^ 1u, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const TcDecays &d = dec[it & 1];
+            uint32_t p[16], pd[16];
+            if (b >= q) {
+                float csum = 0.0f;
+                // e^{c_i - c_j}: column i, this thread's j
+                const float cj = b > q ? d.cq[b > q ? b - 1 : 0][r] * a.scale : 0.0f, lj = d.loc[r];
+                const uint32_t mask = d.mask[r];
+#pragma unroll
+                for (int z = 0; z < 32; z += 16) {
+                    float s[16], t[16];
+                    tmem_ld16x2(R0 + at + z, R1 + at + z, s, t);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        float w[4];
+                        if (b > q) {
+                            const float4 e = *reinterpret_cast<const float4 *>(&d.rq[32 * b + z + j]);
+                            w[0] = cj * e.x;
+                            w[1] = cj * e.y;
+                            w[2] = cj * e.z;
+                            w[3] = cj * e.w;
+                        } else {
+                            const float4 l = *reinterpret_cast<const float4 *>(&d.loc[32 * b + z + j]);
+                            w[0] = ex2(l.x - lj) * a.scale;
+                            w[1] = ex2(l.y - lj) * a.scale;
+                            w[2] = ex2(l.z - lj) * a.scale;
+                            w[3] = ex2(l.w - lj) * a.scale;
+                        }
+                        float pp[4], pq[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool on = b > q || ((mask >> (z + j + k)) & 1u);
+                            pp[k] = on ? w[k] * s[j + k] : 0.0f;
+                            pq[k] = on ? w[k] * t[j + k] : 0.0f;
+                            // W, without the diagonal; s keeps it for the sums over this warp's keys
+                            const bool off = b > q || (on && z + j + k != lane);
+                            s[j + k] = off ? pp[k] * t[j + k] : 0.0f;
+                            csum += s[j + k];
+                        }
+                        p[(z + j) / 2] = pack2(pp[0], pp[1]);
+                        p[(z + j) / 2 + 1] = pack2(pp[2], pp[3]);
+                        pd[(z + j) / 2] = pack2(pq[0], pq[1]);
+                        pd[(z + j) / 2 + 1] = pack2(pq[2], pq[3]);
+                    }
+                    // 16 columns summed over the lanes: each step halves the columns a lane holds
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) {
+                        const bool up = lane & o;
+#pragma unroll
+                        for (int k = 0; k < o; ++k) {
+                            const float send = up ? s[k] : s[k + o], keep = up ? s[k + o] : s[k];
+                            s[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                        }
+                    }
+                    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 16);
+                    if (lane < 16) sums[q][32 * b + z + lane] = s[0];
+                }
+                sums[4 + b][r] = csum;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) p[j] = pd[j] = 0u;
+            }
+            tc_fence_before();
+            warp_arrive(&scfree);
+            // the states' part of dq and dk: scaled in place, dotted with q and k
+            ok = warp_wait(&bdqi, ph, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            if (b < DK / 32) {
+                float v[32];
+                tmem_ld32(R2 + at, v);
+                const float f = a.scale * d.row[r];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= f;
+                tmem_st32(R2 + at, v);
+                sums[8 + b][r] = dot_row(smem + SM::Q, r, b, v);
+            }
+            ok = warp_wait(&bdki, ph, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const float colr = d.col[r];
+            if (b < DK / 32) {
+                float v[32];
+                tmem_ld32(R3 + at, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= colr;
+                tmem_st32(R3 + at, v);
+                sums[12 + b][r] = dot_row(smem + SM::K, r, b, v);
+            }
+            tmem_wait_st();
+            ok = warp_wait(&bx, ph, &s_abort);
+            if (!ok) break;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t o = (b >> 1) * BOX + swz(r, 4 * (b & 1) + k);
+                *reinterpret_cast<uint4 *>(x0 + o) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
+                *reinterpret_cast<uint4 *>(x1 + o) = make_uint4(pd[4 * k], pd[4 * k + 1], pd[4 * k + 2], pd[4 * k + 3]);
+            }
+            tma_store_fence();
+            tc_fence_before();
+            warp_arrive(&pready);
+            warp_arrive(&dempty[it & 1]);
+            ok = warp_wait(&bout, ph, &s_abort);
+            if (!ok) break;
+            tc_fence_after();
+            const bool on = r < ck.len;
+            const long long row = ck.row + r;
+            if (b < DV / 32) {
+                float v[32];
+                {
+                    float s[16], t[16];
+#pragma unroll
+                    for (int z = 0; z < 32; z += 16) {
+                        tmem_ld16x2(R0 + at + z, R1 + at + z, s, t);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[z + j] = fmaf(colr, s[j], t[j]);
+                    }
+                }
+                if (on) put_row(static_cast<__nv_bfloat16 *>(a.dv_) + (row * a.H + h) * a.dv + 32 * b, v, a.dv - 32 * b);
+            }
+            if (b < DK / 32) {
+                const int cols = a.dk - 32 * b;
+                float v[32];
+                tmem_ld32(R2 + at, v);
+                if (on) {
+                    if (g.part_q) put_row(g.part_q + (row * a.H + h) * a.dk + 32 * b, v, cols);
+                    else put_row(static_cast<__nv_bfloat16 *>(a.dq) + (row * a.Hqk + h) * a.dk + 32 * b, v, cols);
+                }
+                tmem_ld32(R3 + at, v);
+                if (on) {
+                    if (g.part_q) put_row(g.part_k + (row * a.H + h) * a.dk + 32 * b, v, cols);
+                    else put_row(static_cast<__nv_bfloat16 *>(a.dk_) + (row * a.Hqk + h) * a.dk + 32 * b, v, cols);
+                }
+            }
+            tc_fence_before();
+            warp_arrive(&tfree);
+        }
+        if (!ok)
+            for (int item = blockIdx.x + it * gridDim.x; item < items; item += gridDim.x) {
+                ck = la_chunk(g.ch, item / a.H);
+                h = item % a.H;
+                if (r < ck.len)
+                    for (int j = 32 * b; j < min(a.dv, 32 * b + 32); ++j)
+                        static_cast<__nv_bfloat16 *>(a.dv_)[((ck.row + r) * a.H + h) * a.dv + j] =
+                            __float2bfloat16(__int_as_float(0x7fc00000));
+            }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        if (s_abort && s_loaded > 0) {
+            const uint32_t ph = (uint32_t)((s_loaded - 1) / 2) & 1u;
+            (void)mbar_wait(&full1, ph, TC_WAIT_NS);
+            (void)mbar_wait(&full2, ph, TC_WAIT_NS);
+            (void)mbar_wait(&fullS, ph, TC_WAIT_NS);
+            if (s_loaded % 2 == 0) (void)mbar_wait(&fullD, ph, TC_WAIT_NS);
+        }
+        (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_free<512>(tmem);
+    }
+}
+
 // Packed sequences without a row: their final state is their first.
 __global__ void __launch_bounds__(256) la_empty_kernel(LaChunks ch, long long HE, const float *first, float *last)
 {
@@ -952,13 +1511,12 @@ FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
 }
 
 template <int DK>
-cudaError_t launch_state(const CUtensorMap *m, const TcArgs &g0, const TcArgs &g1, int dirs, cudaStream_t st)
+cudaError_t launch_state(const CUtensorMap &x, const CUtensorMap &y, const TcArgs &g, cudaStream_t st)
 {
     const int bytes = StateShared<DK>::BYTES;
     cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, dirs);
-    la_state_kernel<DK><<<grid, 384, bytes, st>>>(m[0], m[1], m[2], m[3], g0, g1);
+    la_state_kernel<DK><<<(unsigned)g.seg.total * g.a.H * g.tiles, 384, bytes, st>>>(x, y, g);
     return cudaGetLastError();
 }
 
@@ -970,6 +1528,73 @@ cudaError_t launch_forward(const CUtensorMap *m, const TcArgs &g, cudaStream_t s
     if (e != cudaSuccess) return e;
     la_forward_kernel<DK>
         <<<(unsigned)g.seg.total * g.a.H * g.tiles, FWD_THREADS, bytes, st>>>(m[0], m[1], m[2], g);
+    return cudaGetLastError();
+}
+
+// The state planes of the chunks: (d_v, d_k, chunk * H + h), boxes of 64
+// columns and DK rows.
+bool state_map(CUtensorMap *m, const void *p, const LaArgs &a, long long n, int DK)
+{
+    auto fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)a.dv, (cuuint64_t)a.dk, (cuuint64_t)n};
+    cuuint64_t strides[2] = {(cuuint64_t)a.dv * 2, (cuuint64_t)a.dv * a.dk * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)DK, 1u};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct BackWs {
+    char *table, *seg_table;
+    float *seg[2], *tot[2];            // a segment's first states, forward and from the end
+    __nv_bfloat16 *hi[2], *lo[2];      // the chunks' states
+    float *dot, *dgc, *pq, *pk;
+    size_t bytes;
+};
+
+BackWs back_layout(const LaArgs &a, int L, void *ws)
+{
+    BackWs w{};
+    char *p = static_cast<char *>(ws);
+    auto take = [&](size_t n) {
+        char *r = p;
+        p += up256(n);
+        return r;
+    };
+    const size_t E = (size_t)a.dk * a.dv, n = (size_t)la_chunk_bound(a, TCC) * a.H;
+    const size_t rows = a.cu ? (size_t)a.T : (size_t)a.B * a.T;
+    w.table = take(la_table_bytes(a));
+    w.seg_table = take(la_table_bytes(a));
+    for (int i = 0; i < 2; ++i) {
+        if (L < (a.T - 1) / TCC + 1) {
+            const size_t items = (size_t)la_chunk_bound(a, L * TCC) * a.H;
+            w.seg[i] = reinterpret_cast<float *>(take(4 * items * E));
+            w.tot[i] = reinterpret_cast<float *>(take(4 * items));
+        }
+        w.hi[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
+        w.lo[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
+    }
+    w.dot = reinterpret_cast<float *>(take(4 * n * 16));
+    w.dgc = reinterpret_cast<float *>(take(4 * n));
+    if (a.H != a.Hqk) {
+        w.pq = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
+        w.pk = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
+    }
+    w.bytes = (size_t)(p - static_cast<char *>(ws));
+    return w;
+}
+
+template <int DK, int DV>
+cudaError_t launch_back(const CUtensorMap *m, const BackArgs &g, int items, cudaStream_t st)
+{
+    const int bytes = BackShared<DK, DV>::BYTES;
+    cudaError_t e =
+        cudaFuncSetAttribute(la_backward_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    la_backward_kernel<DK, DV><<<min(items, 148), BACK_THREADS, bytes, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6],
+                                                                           m[7], g);
     return cudaGetLastError();
 }
 
@@ -1008,8 +1633,7 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
         s.last = nullptr;
         s.fin = w.states;
         s.fin_tot = w.tot;
-        const CUtensorMap ms[4] = {m[1], m[2], m[1], m[2]};
-        e = a.dk <= 64 ? launch_state<64>(ms, s, s, 1, st) : launch_state<128>(ms, s, s, 1, st);
+        e = a.dk <= 64 ? launch_state<64>(m[1], m[2], s, st) : launch_state<128>(m[1], m[2], s, st);
         if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st);
         if (e != cudaSuccess) return e;
         g.init = w.states;
@@ -1021,6 +1645,85 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
         if (e != cudaSuccess) return e;
     }
     return a.dk <= 64 ? launch_forward<64>(m, g, st) : launch_forward<128>(m, g, st);
+}
+
+size_t la_tc_backward_workspace(const LaArgs &a)
+{
+    return back_layout(a, seg_chunks(a, a.H * ((a.dv + 63) / 64)), reinterpret_cast<void *>((uintptr_t)256)).bytes;
+}
+
+cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
+{
+    TcArgs g{};
+    g.a = a;
+    g.tiles = (a.dv + 63) / 64;
+    const int L = seg_chunks(a, a.H * g.tiles);
+    const BackWs w = back_layout(a, L, ws);
+    const int DK = a.dk <= 64 ? 64 : 128, DV = a.dv <= 64 ? 64 : 128;
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
+    if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    if (e != cudaSuccess) return e;
+    const long long n = (long long)g.ch.total * a.H;
+    CUtensorMap m[8];
+    bool ok = token_map(&m[0], a.q, a.dk, a.Hqk, a.ldq, a) && token_map(&m[1], a.k, a.dk, a.Hqk, a.ldk, a) &&
+              token_map(&m[2], a.v, a.dv, a.H, a.ldv, a) &&
+              token_map(&m[3], a.dO, a.dv, a.H, (long long)a.H * a.dv, a);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && state_map(&m[4 + 2 * i], w.hi[i], a, n, DK) && state_map(&m[5 + 2 * i], w.lo[i], a, n, DK);
+    if (!ok) return cudaErrorInvalidValue;
+    // the states: forward, then from the end (which meets the forward ones for dg)
+    for (int i = 0; i < 2; ++i) {
+        TcArgs s = g;
+        s.back = i == 1;
+        const CUtensorMap &x = s.back ? m[0] : m[1], &y = s.back ? m[3] : m[2];
+        const float *first = s.back ? a.dsT : a.s0;
+        float *last = s.back ? a.ds0 : nullptr;
+        if (w.seg[i]) {
+            s.fin = w.seg[i];
+            s.fin_tot = w.tot[i];
+            e = DK == 64 ? launch_state<64>(x, y, s, st) : launch_state<128>(x, y, s, st);
+            if (e == cudaSuccess)
+                e = la_scan(g.seg, a.H, a.dk * a.dv, s.back, w.seg[i], w.tot[i], first, last, st);
+            if (e != cudaSuccess) return e;
+            s.fin = nullptr;
+            s.fin_tot = nullptr;
+            s.init = w.seg[i];
+        } else {
+            if (a.cu && last) {
+                const long long HE = (long long)a.H * a.dk * a.dv;
+                la_empty_kernel<<<dim3(a.B, (unsigned)min((HE + 1023) / 1024, 64LL)), 256, 0, st>>>(g.seg, HE, first,
+                                                                                                  last);
+                e = cudaGetLastError();
+                if (e != cudaSuccess) return e;
+            }
+            s.first = first;
+            s.last = last;
+        }
+        s.hi = w.hi[i];
+        s.lo = w.lo[i];
+        if (s.back && a.dg) {
+            s.phi = w.hi[0];
+            s.plo = w.lo[0];
+            s.dot = w.dot;
+        }
+        e = DK == 64 ? launch_state<64>(x, y, s, st) : launch_state<128>(x, y, s, st);
+        if (e != cudaSuccess) return e;
+    }
+    BackArgs b{};
+    b.a = a;
+    b.ch = g.ch;
+    b.total = (int)n;
+    b.part_q = w.pq;
+    b.part_k = w.pk;
+    b.dgc = w.dgc;
+    b.dot = w.dot;
+    b.tiles = g.tiles;
+    if (DK == 64) e = DV == 64 ? launch_back<64, 64>(m, b, (int)n, st) : launch_back<64, 128>(m, b, (int)n, st);
+    else e = DV == 64 ? launch_back<128, 64>(m, b, (int)n, st) : launch_back<128, 128>(m, b, (int)n, st);
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, a.dq, a.dtype, g.ch, a, st);
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pk, a.dk_, a.dtype, g.ch, a, st);
+    if (e == cudaSuccess && a.dg && a.per_head) e = la_head_sum(w.dgc, a.dg, g.ch, a.H, st);
+    return e;
 }
 
 }  // namespace slstm

@@ -129,7 +129,8 @@ LaArgs la_args(const void *q, const void *k, const void *v, const float *g, cons
 // need of the pointers is refused, not worked around.
 size_t la_workspace(const LaArgs &a, bool backward)
 {
-    return la_tc_takes(a) && !backward ? la_tc_forward_workspace(a) : la_simt_workspace(a, backward);
+    if (!la_tc_takes(a)) return la_simt_workspace(a, backward);
+    return backward ? la_tc_backward_workspace(a) : la_tc_forward_workspace(a);
 }
 
 bool la_inputs_ok(const LaArgs &a)
@@ -167,6 +168,11 @@ int la_backward(LaArgs a, const void *dO, const float *dsT, void *dq, void *dk, 
         return SLSTM_ERR_INVALID_ARG;
     if (dg != nullptr && !la_elem_aligned(dg, SLSTM_F32)) return SLSTM_ERR_INVALID_ARG;
     if (!ws_ok(ws, ws_bytes, la_workspace(a, true))) return SLSTM_ERR_INVALID_ARG;
+    if (la_tc_takes(a)) {
+        for (const void *p : {a.q, a.k, a.v, dO, (const void *)dq, (const void *)dk, (const void *)dv})
+            if (!aligned16(p)) return SLSTM_ERR_INVALID_ARG;
+        return cuda_status(la_tc_backward(a, ws, static_cast<cudaStream_t>(stream)));
+    }
     return cuda_status(la_simt_backward(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
