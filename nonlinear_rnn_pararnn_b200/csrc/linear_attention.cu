@@ -188,21 +188,20 @@ __global__ void __launch_bounds__(256) la_scan_kernel(LaChunks ch, int H, int E,
     float s = first ? first[at] : 0.0f;
     for (int i0 = 0; i0 < n; i0 += 8) {
         float dl[8], tt[8];
-        const int m = min(8, n - i0);
+        const long long c1 = back ? c0 + n - 1 - i0 : c0 + i0, d1 = back ? -1 : 1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (i >= m) break;
-            const long long c = back ? c0 + n - 1 - (i0 + i) : c0 + i0 + i;
+            const bool on = i0 + i < n;
+            const long long c = on ? c1 + i * d1 : c1;
             dl[i] = buf[(c * H + h) * E + e];
             tt[i] = tot[c * H + h];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (i >= m) break;
-            const long long c = back ? c0 + n - 1 - (i0 + i) : c0 + i0 + i;
-            buf[(c * H + h) * E + e] = s;
-            s = fmaf(tt[i], s, dl[i]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < n) {
+                buf[((c1 + i * d1) * H + h) * E + e] = s;
+                s = fmaf(tt[i], s, dl[i]);
+            }
     }
     if (last) last[at] = s;
 }

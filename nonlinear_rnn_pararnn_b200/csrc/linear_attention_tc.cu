@@ -45,7 +45,7 @@ struct TcArgs {
     float *last;              // final states [sequence][h], or null
     __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
     const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
-    float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
+    float *dot;               // [chunk][h][2][4]: a warp's share of <S_n, dS_{n+1}>, or null
     bool back;                // from the end: (q, dO) in place of (k, v)
 };
 
@@ -300,19 +300,16 @@ struct Share {
 };
 
 // S <- tot S + the sum of the two accumulators at `at` and 64 columns on.
-SLSTM_DEVINL void state_add(float (&S)[32], float tot, uint32_t at)
+template <int N>
+SLSTM_DEVINL void state_add(float (&S)[N], float tot, uint32_t at)
 {
-    float v[32], w[32];
-    tmem_ld32x2(at, at + 64, v, w);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) S[i] = fmaf(tot, S[i], v[i] + w[i]);
-}
-SLSTM_DEVINL void state_add(float (&S)[16], float tot, uint32_t at)
-{
-    float v[16], w[16];
-    tmem_ld16x2(at, at + 64, v, w);
+    for (int z = 0; z < N; z += 16) {
+        float v[16], w[16];
+        tmem_ld16x2(at + z, at + 64 + z, v, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) S[i] = fmaf(tot, S[i], v[i] + w[i]);
+        for (int i = 0; i < 16; ++i) S[z + i] = fmaf(tot, S[z + i], v[i] + w[i]);
+    }
 }
 
 template <int N>
@@ -346,31 +343,39 @@ SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, i
 //   S <- e^{c_C} S + X^T (w Y):  X = k, Y = v, w = e^{c_C - c_j} (forward)
 //                                X = q, Y = dO, w = scale e^{c_i} (from the end)
 // and writes the state that each chunk starts from (two bf16 terms, for the
-// backward kernel) and / or the final one.  Warps 0-7 scale Y and hold the
-// state (lane = row of d_k), warp 8 loads (a ring of NST chunks), warp 9 issues
-// the MMAs, warps 10 and 11 compute the decays of every other chunk each.  Bound: the bytes of X and Y and of the
-// states written.
+// backward kernel) and / or the final one.  The work of a chunk is split over
+// warps that run a chunk apart, since each part of it is a chain of latencies:
+// warps 0-7 hold the state (lane = row of d_k), warps 8-15 scale Y, warp 16
+// loads (a ring of NST chunks), warp 17 issues the MMAs, warps 18 and 19
+// compute the decays of every other chunk each.  Bound: the bytes of X and Y
+// and of the states written.  Those go out through shared memory by TMA (warps
+// 20-23): a lane holds a row of them, and stores from the registers, a line for
+// each lane, took 5500 cycles a chunk where the rest takes 2000.
 // ---------------------------------------------------------------------------
 template <int DK>
 struct StateShared {
-    static constexpr int NST = DK == 128 ? 3 : 4;
+    static constexpr int NST = DK == 128 ? 2 : 3;
     static constexpr int NB = DK / 64;
     static constexpr uint32_t STAGE = (NB + 1) * BOX;
     static constexpr uint32_t Y = NST * STAGE;          // two buffers of hi, lo
-    static constexpr uint32_t DEC = Y + 4 * BOX;
+    static constexpr uint32_t OUT = Y + 4 * BOX;        // DK rows of hi, of lo
+    static constexpr uint32_t DEC = OUT + 2 * DK * 128;
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 
+constexpr int STATE_THREADS = 768;
+
 template <int DK>
-__global__ void __launch_bounds__(384, 1)
-    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my, TcArgs g)
+__global__ void __launch_bounds__(STATE_THREADS, 1)
+    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                    const __grid_constant__ CUtensorMap mhi, const __grid_constant__ CUtensorMap mlo, TcArgs g)
 {
     typedef StateShared<DK> SM;
     constexpr int NST = SM::NST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
-    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], fin;
+    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], drained[2], staged, unstaged, fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
     const LaArgs &a = g.a;
@@ -386,12 +391,15 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 8);
+            mbar_init(&dempty[i], 16);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&yready[i], 8);
             mbar_init(&delta[i], 1);
+            mbar_init(&drained[i], 8);
         }
+        mbar_init(&staged, 8);
+        mbar_init(&unstaged, 4);
         mbar_init(&fin, 1);
         mbar_init_fence();
         s_abort = 0;
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(384, 1)
     auto chunk = [&](int n) { return back ? nch - 1 - n : n; };
     auto rows = [&](int n) { return min(TCC, sg.len - chunk(n) * TCC); };
 
-    if (warp == 8) {
+    if (warp == 16) {
         if (lane == 0) {
             const int hq = h / (a.H / a.Hqk);
             int n = 0;
@@ -423,13 +431,14 @@ __global__ void __launch_bounds__(384, 1)
             }
             s_loaded = n;
         }
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_bf16(128, 128, true, true);
             for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
                 if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
                 if (!lane_wait(&yready[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
+                if (!lane_wait(&drained[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort)) break;
                 tc_fence_after();
                 // the 64 rows of a narrow d_k twice: no step from one 64 to the next
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
@@ -444,16 +453,84 @@ __global__ void __launch_bounds__(384, 1)
             }
             umma_commit(&fin);
         }
-    } else if (warp >= 10) {
+    } else if (warp >= 20) {
+        // the state in shared memory: stored, and met with the forward one for dg
+        for (int n = 0; n < nch && g.hi; ++n) {
+            const long long ci = (sg.c0 + chunk(n)) * a.H + h;
+            float s = 0.0f;
+            constexpr int NP = DK / 16;   // 16-byte pieces of a thread
+            uint4 y[NP], z[NP];
+            if (g.dot) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int idx = (warp - 20) * 32 + lane + 128 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
+                    y[i] = z[i] = make_uint4(0, 0, 0, 0);
+                    if (r < a.dk && c < a.dv) {
+                        const long long at = ci * a.dk * a.dv + (long long)r * a.dv + c;
+                        y[i] = __ldg(reinterpret_cast<const uint4 *>(g.phi + at));
+                        z[i] = __ldg(reinterpret_cast<const uint4 *>(g.plo + at));
+                    }
+                }
+            }
+            if (!warp_wait(&staged, (uint32_t)n & 1u, &s_abort)) break;
+            if (warp == 20 && lane == 0) {
+                tma_store_3d(&mhi, smem + SM::OUT, 64 * tile, 0, (int)ci);
+                tma_store_3d(&mlo, smem + SM::OUT + DK * 128, 64 * tile, 0, (int)ci);
+                bulk_commit();
+            }
+            if (g.dot) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int idx = (warp - 20) * 32 + lane + 128 * i;
+                    const uint8_t *at = smem + SM::OUT + swz(idx >> 3, idx & 7);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(at);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(at + DK * 128);
+                    const uint32_t yy[4] = {y[i].x, y[i].y, y[i].z, y[i].w}, zz[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s = fmaf(lo_of(uu[j]) + lo_of(ww[j]), lo_of(yy[j]) + lo_of(zz[j]), s);
+                        s = fmaf(hi_of(uu[j]) + hi_of(ww[j]), hi_of(yy[j]) + hi_of(zz[j]), s);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane == 0) g.dot[(ci * 2 + tile) * 4 + warp - 20] = s;
+            }
+            if (warp == 20 && lane == 0) bulk_wait_read_all();
+            warp_arrive(&unstaged);
+        }
+        if (warp == 20 && lane == 0) bulk_wait_all();
+    } else if (warp >= 18) {
         float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (warp - 10 < nch) load_decays(gn, a, sg.row + (long long)chunk(warp - 10) * TCC, rows(warp - 10), h, lane);
-        for (int n = warp - 10; n < nch; n += 2) {
+        if (warp - 18 < nch) load_decays(gn, a, sg.row + (long long)chunk(warp - 18) * TCC, rows(warp - 18), h, lane);
+        for (int n = warp - 18; n < nch; n += 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) gv[i] = gn[i];
             if (n + 2 < nch) load_decays(gn, a, sg.row + (long long)chunk(n + 2) * TCC, rows(n + 2), h, lane);
             if (!warp_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
             tc_decays(dec[n % ND], gv, lane);
             warp_arrive(&dfull[n % ND]);
+        }
+    } else if (warp >= 8) {
+        const int t = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST;
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
+            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+            // the product that read this buffer two chunks ago
+            if (n > 1 && !warp_wait(&delta[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort)) break;
+            uint8_t *st = smem + s * SM::STAGE;
+            const TcDecays &d = dec[n % ND];
+            const int len = rows(n);
+            uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
+            scale_row(st + SM::NB * BOX, y, y + BOX, t, half, back ? a.scale * d.row[t] : d.col[t], t < len);
+            // rows behind a packed sequence belong to another one
+            if (packed && t >= len)
+                for (int i = half; i < SM::NB; i += 2) zero_row(st + i * BOX, t);
+            tma_store_fence();
+            warp_arrive(&yready[n & 1]);
+            warp_arrive(&dempty[n % ND]);
         }
     } else {
         typedef Share<DK> SH;
@@ -464,31 +541,15 @@ __global__ void __launch_bounds__(384, 1)
         float S[SH::N];
         state_load(S, src, a.dk, a.dv, r, col);
         float run = 1.0f;
-        auto scale = [&](int n) -> bool {
-            const int s = n % NST;
-            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
-            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) return false;
-            uint8_t *st = smem + s * SM::STAGE;
-            const TcDecays &d = dec[n % ND];
-            const int t = (warp & 3) * 32 + lane, half = warp >> 2, len = rows(n);
-            uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
-            scale_row(st + SM::NB * BOX, y, y + BOX, t, half, back ? a.scale * d.row[t] : d.col[t], t < len);
-            // rows behind a packed sequence belong to another one
-            if (packed && t >= len)
-                for (int i = half; i < SM::NB; i += 2) zero_row(st + i * BOX, t);
-            tma_store_fence();
-            warp_arrive(&yready[n & 1]);
-            return true;
-        };
-        bool ok = scale(0);
-        for (int n = 0; n < nch && ok; ++n) {
-            if (n + 1 < nch) ok = scale(n + 1);
-            if (!ok) break;
-            if (g.hi && r < a.dk) {
-                const long long at = ((sg.c0 + chunk(n)) * a.H + h) * E + (long long)r * a.dv + col;
+        bool ok = true;
+        for (int n = 0; n < nch; ++n) {
+            if (g.hi) {
+                if (n > 0 && !warp_wait(&unstaged, (uint32_t)(n - 1) & 1u, &s_abort)) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
                 for (int i = 0; i < SH::N; i += 8) {
-                    if (col + i >= a.dv) break;
                     uint32_t y[4], z[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -496,32 +557,15 @@ __global__ void __launch_bounds__(384, 1)
                         y[j] = pack2(u, v);
                         z[j] = pack2(u - lo_of(y[j]), v - hi_of(y[j]));
                     }
-                    *reinterpret_cast<uint4 *>(g.hi + at + i) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4 *>(g.lo + at + i) = make_uint4(z[0], z[1], z[2], z[3]);
+                    uint8_t *at = smem + SM::OUT + swz(r, (c0 + i) / 8);
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(at + DK * 128) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
+                tma_store_fence();
+                warp_arrive(&staged);
             }
-            if (g.dot) {
-                float s = 0.0f;
-                if (r < a.dk) {
-                    const long long at = ((sg.c0 + chunk(n)) * a.H + h) * E + (long long)r * a.dv + col;
-#pragma unroll
-                    for (int i = 0; i < SH::N; i += 8) {
-                        if (col + i >= a.dv) break;
-                        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(g.phi + at + i));
-                        const uint4 z = __ldg(reinterpret_cast<const uint4 *>(g.plo + at + i));
-                        const uint32_t yy[4] = {y.x, y.y, y.z, y.w}, zz[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            s = fmaf(S[i + 2 * j], lo_of(yy[j]) + lo_of(zz[j]), s);
-                            s = fmaf(S[i + 2 * j + 1], hi_of(yy[j]) + hi_of(zz[j]), s);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) g.dot[(((sg.c0 + chunk(n)) * a.H + h) * 2 + tile) * 8 + warp] = s;
-            }
-            if (!warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) {
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) ||
+                !warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) {
                 ok = false;
                 break;
             }
@@ -530,6 +574,7 @@ __global__ void __launch_bounds__(384, 1)
             run *= tot;
             state_add(S, tot, tmem + (n & 1) * 128 + c0 + ((uint32_t)((warp & 3) * 32) << 16));
             tc_fence_before();
+            warp_arrive(&drained[n & 1]);
             warp_arrive(&dempty[n % ND]);
         }
         if (!ok) {
@@ -564,16 +609,20 @@ __global__ void __launch_bounds__(384, 1)
 // The forward pass of a segment: one block walks the chunks of one head and 64
 // columns of v and does all of it while q, k and v are in shared memory, the
 // state in registers:
-//   warps 0-7   v times its decays (two bf16 terms), the state (lane = row of
-//               d_k), the state's upper term into shared memory
-//   warps 8-15  the weights D (q k) from tensor memory and back as bf16
-//               (lane = query row, half of the keys each), then the outputs
-//   warp 16     loads, a ring of NST chunks;  warp 17 issues the MMAs
-//   warps 18-19 the decays of every other chunk each, up to three chunks ahead
+//   warps 0-7   the state (lane = row of d_k), its upper term into shared memory
+//   warps 8-11  v times its decays as two bf16 terms
+//   warps 12-19 the weights D (q k) from tensor memory and back as bf16
+//               (lane = query row, half of the keys each)
+//   warps 20-23 the outputs
+//   warp 24     loads (a ring of NST chunks) and the MMAs of k^T (w v)
+//   warp 25     the other MMAs
+//   warps 26-27 the decays of every other chunk each, up to three chunks ahead
+// Each of these is a chain of latencies some 1500 cycles long; apart from one
+// another they run a chunk or two ahead or behind, and a chunk takes as long as
+// the longest of them, not as all.
 // A chunk's products: q k^T (128 x 128), then into one 64-column accumulator
 // each q S, D(q k) v (A from tensor memory) and k^T (w v).  The first of the
-// next chunk is issued before the last of this one, so that the tensor cores
-// work while the weights are computed.
+// next chunk is issued before the last of this one where its rows have come.
 // ---------------------------------------------------------------------------
 template <int DK>
 struct FwdShared {
@@ -587,7 +636,7 @@ struct FwdShared {
 };
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
-constexpr int FWD_THREADS = 640;
+constexpr int FWD_THREADS = 896;
 
 template <int DK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -600,7 +649,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready, sfree, pready, ofull, oempty, tready, fin;
+    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull, oempty, tready, drained,
+        fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
     const LaArgs &a = g.a;
@@ -612,22 +662,24 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
         }
         for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 16);
+            mbar_init(&dempty[i], 24);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
-        mbar_init(&yready, 8);
+        mbar_init(&yready, 4);
         mbar_init(&delta, 1);
         mbar_init(&sready, 8);
         mbar_init(&sfree, 1);
-        mbar_init(&pready, 8);
+        mbar_init(&pready[0], 8);
+        mbar_init(&pready[1], 8);
         mbar_init(&ofull, 1);
-        mbar_init(&oempty, 8);
-        mbar_init(&tready, 8);
-        mbar_init(&fin, 1);
+        mbar_init(&oempty, 4);
+        mbar_init(&tready, 4);
+        mbar_init(&drained, 8);
+        mbar_init(&fin, 2);
         mbar_init_fence();
         s_abort = 0;
         s_loaded = 0;
@@ -642,13 +694,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     // the last chunk of a packed sequence holds rows of the next one
     const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
 
-    if (warp == 16) {
+    if (warp == 24) {
         if (lane == 0) {
+            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             const int hq = h / (a.H / a.Hqk);
-            int n = 0;
-            for (; n < nch; ++n) {
+            auto load = [&](int n) -> bool {
                 const int s = n % NST;
-                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) break;
+                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) return false;
                 uint8_t *st = smem + s * SM::STAGE;
                 mbar_expect_tx(&full[s], SM::STAGE);
                 const int t = sg.t + n * TCC;
@@ -658,13 +710,35 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     tma_load_4d(st + (SM::NB + i) * BOX, &mk, &full[s], 64 * i, hq, t, sg.b);
                 }
                 tma_load_4d(st + 2 * SM::NB * BOX, &mv, &full[s], 64 * tile, h, t, sg.b);
+                s_loaded = n + 1;
+                return true;
+            };
+            bool ok = true;
+            for (int n = 0; n < min(NST, nch) && ok; ++n) ok = load(n);
+            for (int n = 0; n < nch && ok; ++n) {
+                const int s = n % NST;
+                const uint32_t ph = (uint32_t)n & 1u;
+                ok = lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort) && lane_wait(&yready, ph, &s_abort) &&
+                     lane_wait(&drained, ph ^ 1u, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                // both terms of w v side by side: k is read once for them; the
+                // 64 rows of a narrow d_k twice (no step from one 64 to the next)
+                const uint64_t kt =
+                    smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE + SM::NB * BOX), DK == 128 ? BOX : 0u);
+                const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
+                umma_commit(&delta);
+                umma_commit(&empty[s]);
+                if (n + NST < nch) ok = load(n + NST);
             }
-            s_loaded = n;
+            umma_commit(&fin);
         }
-    } else if (warp == 17) {
+    } else if (warp == 25) {
         if (lane == 0) {
             constexpr uint32_t id_qk = idesc_bf16(128, 128, false, false);
-            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
             // q k^T of chunk n; unless `must`, only if its rows are there
             int scored = 0;
@@ -694,16 +768,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 const int s = n % NST;
                 const uint32_t ph = (uint32_t)n & 1u;
                 const uint8_t *st = smem + s * SM::STAGE;
-                ok = (scored > n || scores(n, true)) && lane_wait(&yready, ph, &s_abort);
+                ok = scored > n || scores(n, true);
                 if (!ok) break;
-                tc_fence_after();
-                const uint64_t kt = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), DK == 128 ? BOX : 0u);
-                // both terms of w v side by side: k is read once for them
-                const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
-                umma_commit(&delta);
                 ok = lane_wait(&sready, ph, &s_abort) && lane_wait(&oempty, ph ^ 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
@@ -719,9 +785,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 // the next chunk's scores go ahead of this one's last product
                 // when its rows have come, and never make it wait
                 if (n + 1 < nch) {
-                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !mbar_try_wait(&pready, ph); ++i) scores(n + 1, false);
+                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !mbar_try_wait(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
+                        scores(n + 1, false);
                 }
-                ok = lane_wait(&pready, ph, &s_abort);
+                ok = lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
@@ -733,13 +800,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             umma_commit(&fin);
         }
-    } else if (warp >= 18) {
+    } else if (warp >= 26) {
         float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         auto load = [&](int n) {
             if (n < nch) load_decays(gn, a, sg.row + (long long)n * TCC, min(TCC, sg.len - n * TCC), h, lane);
         };
-        load(warp - 18);
-        for (int n = warp - 18; n < nch; n += 2) {
+        load(warp - 26);
+        for (int n = warp - 26; n < nch; n += 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) gv[i] = gn[i];
             load(n + 2);
@@ -750,7 +817,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     } else if (warp < 8) {
         typedef Share<DK> SH;
         const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
-        const int t = (warp & 3) * 32 + lane, half = warp >> 2;
         const long long E = (long long)a.dk * a.dv;
         const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
                                   : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
@@ -758,20 +824,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         state_load(S, src, a.dk, a.dv, r, col);
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
-            const int s = n % NST;
             const uint32_t ph = (uint32_t)n & 1u;
-            const int len = min(TCC, sg.len - n * TCC);
-            uint8_t *st = smem + s * SM::STAGE;
-            if (n == ragged) {
-                // before anything that waits for this block's products: the
-                // first of this chunk is issued ahead of them
-                ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort);
-                if (!ok) break;
-                if (t >= len)
-                    for (int i = half; i < 2 * SM::NB + 1; i += 2) zero_row(st + i * BOX, t);
-                tma_store_fence();
-                warp_arrive(&tready);
-            }
             if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_abort);
             if (!ok) break;
             // the state's upper term, row r: the B operand of q S
@@ -782,31 +835,45 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
             tma_store_fence();
             warp_arrive(&sready);
-            ok = warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
-                 warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
-            if (!ok) break;
-            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, half, dec[n % ND].col[t], t < len);
-            tma_store_fence();
-            warp_arrive(&yready);
-            ok = warp_wait(&delta, ph, &s_abort);
+            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) && warp_wait(&delta, ph, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            const float tot = dec[n % ND].tot;
-            state_add(S, tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
+            state_add(S, dec[n % ND].tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
             tc_fence_before();
+            warp_arrive(&drained);
             warp_arrive(&dempty[n % ND]);
         }
         if (!ok)
 #pragma unroll
             for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
         if (g.last) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
-    } else {
-        const int q = warp & 3, half = (warp >> 2) & 1;
+    } else if (warp < 12) {
+        const int t = (warp & 3) * 32 + lane;
+        for (int n = 0; n < nch; ++n) {
+            const int s = n % NST, len = min(TCC, sg.len - n * TCC);
+            uint8_t *st = smem + s * SM::STAGE;
+            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+            if (n == ragged) {
+                if (t >= len)
+                    for (int i = 0; i < 2 * SM::NB + 1; ++i) zero_row(st + i * BOX, t);
+                tma_store_fence();
+                warp_arrive(&tready);
+            }
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
+            // the product that read the last terms
+            if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_abort)) break;
+            const float w = dec[n % ND].col[t];
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, half, w, t < len);
+            tma_store_fence();
+            warp_arrive(&yready);
+            warp_arrive(&dempty[n % ND]);
+        }
+    } else if (warp < 20) {
+        const int q = warp & 3, half = ((warp - 12) >> 2) & 1;
         const int i = q * 32 + lane;   // query row
         const uint32_t la = (uint32_t)(q * 32) << 16;
-        const int col = tile * 64 + 32 * half, cols = min(32, a.dv - col);
-        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
-                           (long long)h * a.dv + col;
         // the keys of 32-row block b, this thread's query: weights of v in place of w
         auto weigh = [&](const TcDecays &d, int b, const float (&v)[32], uint32_t (&p)[16]) {
             if (b < q) {
@@ -833,16 +900,11 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
             }
         };
-        bool ok = true;
-        int n = 0;
-        for (; n < nch; ++n) {
-            const uint32_t ph = (uint32_t)n & 1u;
-            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) &&
-                 warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
-            if (!ok) break;
+        for (int n = 0; n < nch; ++n) {
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
+            if (!warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
             tc_fence_after();
             const TcDecays &d = dec[n % ND];
-            const float rowc = d.row[i] * a.scale;
             // 64 keys of this warp; their bf16 weights over the first half of their scores
             const uint32_t sc = tmem + (n & 1) * 128 + 64 * half + la;
 #pragma unroll
@@ -860,33 +922,49 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             tmem_wait_st();
             tc_fence_before();
-            warp_arrive(&pready);
-            ok = warp_wait(&ofull, ph, &s_abort);
+            warp_arrive(&pready[n & 1]);
+            warp_arrive(&dempty[n % ND]);
+        }
+    } else {
+        const int i = (warp & 3) * 32 + lane;   // query row
+        const uint32_t la = (uint32_t)((warp & 3) * 32) << 16;
+        const int cols = min(64, a.dv - tile * 64);
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
+                           (long long)h * a.dv + tile * 64;
+        const long long step = (long long)TCC * a.H * a.dv;
+        bool ok = true;
+        int n = 0;
+        for (; n < nch; ++n) {
+            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
+            const float rowc = dec[n % ND].row[i] * a.scale;
+            warp_arrive(&dempty[n % ND]);
+            ok = ok && warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            float u[32], w[32];
-            tmem_ld32x2(t_o1 + la + 32 * half, t_o2 + la + 32 * half, u, w);
+            uint4 y[8];
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                float u[16], w[16];
+                tmem_ld16x2(t_o1 + la + c, t_o2 + la + c, u, w);
+                uint32_t p[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
+                                 fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
+                y[c / 8] = make_uint4(p[0], p[1], p[2], p[3]);
+                y[c / 8 + 1] = make_uint4(p[4], p[5], p[6], p[7]);
+            }
             tc_fence_before();
             warp_arrive(&oempty);
-            warp_arrive(&dempty[n % ND]);
             if (n * TCC + i < sg.len) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                    if (j >= cols) break;
-                    uint32_t y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = pack2(fmaf(rowc, u[j + 2 * k], a.scale * w[j + 2 * k]),
-                                     fmaf(rowc, u[j + 2 * k + 1], a.scale * w[j + 2 * k + 1]));
-                    *reinterpret_cast<uint4 *>(o + (long long)n * TCC * a.H * a.dv + j) =
-                        make_uint4(y[0], y[1], y[2], y[3]);
-                }
+                for (int j = 0; j < 8; ++j)
+                    if (8 * j < cols) *reinterpret_cast<uint4 *>(o + n * step + 8 * j) = y[j];
             }
         }
         if (!ok)
             for (; n < nch && n * TCC + i < sg.len; ++n)
-                for (int j = 0; j < cols; ++j)
-                    o[(long long)n * TCC * a.H * a.dv + j] = __float2bfloat16(__int_as_float(0x7fc00000));
+                for (int j = 0; j < cols; ++j) o[n * step + j] = __float2bfloat16(__int_as_float(0x7fc00000));
     }
     tc_fence_before();
     __syncthreads();
@@ -1211,9 +1289,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     if (lane >= o) ws += wu;
                 }
                 double dot = 0.0;
-                if (lane < 16 && lane / 8 < g.tiles) dot = g.dot[((long long)c * a.H + h) * 16 + lane];
+                if (lane < 8 && lane / 4 < g.tiles) dot = g.dot[((long long)c * a.H + h) * 8 + lane];
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
                 dot = __shfl_sync(0xffffffffu, dot, 0) * (double)d.tot;
                 double back = xs - xl, front = ws - wl;   // rows behind this lane's, rows before
                 float out[4], sum = 0.0f;
@@ -1511,12 +1589,13 @@ FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
 }
 
 template <int DK>
-cudaError_t launch_state(const CUtensorMap &x, const CUtensorMap &y, const TcArgs &g, cudaStream_t st)
+cudaError_t launch_state(const CUtensorMap &x, const CUtensorMap &y, const CUtensorMap &hi, const CUtensorMap &lo,
+                         const TcArgs &g, cudaStream_t st)
 {
     const int bytes = StateShared<DK>::BYTES;
     cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    la_state_kernel<DK><<<(unsigned)g.seg.total * g.a.H * g.tiles, 384, bytes, st>>>(x, y, g);
+    la_state_kernel<DK><<<(unsigned)g.seg.total * g.a.H * g.tiles, STATE_THREADS, bytes, st>>>(x, y, hi, lo, g);
     return cudaGetLastError();
 }
 
@@ -1576,7 +1655,7 @@ BackWs back_layout(const LaArgs &a, int L, void *ws)
         w.hi[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
         w.lo[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
     }
-    w.dot = reinterpret_cast<float *>(take(4 * n * 16));
+    w.dot = reinterpret_cast<float *>(take(4 * n * 8));
     w.dgc = reinterpret_cast<float *>(take(4 * n));
     if (a.H != a.Hqk) {
         w.pq = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
@@ -1633,7 +1712,9 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
         s.last = nullptr;
         s.fin = w.states;
         s.fin_tot = w.tot;
-        e = a.dk <= 64 ? launch_state<64>(m[1], m[2], s, st) : launch_state<128>(m[1], m[2], s, st);
+        // (it stores no chunk's state: the last two maps are not used)
+        e = a.dk <= 64 ? launch_state<64>(m[1], m[2], m[1], m[1], s, st)
+                       : launch_state<128>(m[1], m[2], m[1], m[1], s, st);
         if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st);
         if (e != cudaSuccess) return e;
         g.init = w.states;
@@ -1676,12 +1757,13 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
         TcArgs s = g;
         s.back = i == 1;
         const CUtensorMap &x = s.back ? m[0] : m[1], &y = s.back ? m[3] : m[2];
+        const CUtensorMap &hi = m[4 + 2 * i], &lo = m[5 + 2 * i];
         const float *first = s.back ? a.dsT : a.s0;
         float *last = s.back ? a.ds0 : nullptr;
         if (w.seg[i]) {
             s.fin = w.seg[i];
             s.fin_tot = w.tot[i];
-            e = DK == 64 ? launch_state<64>(x, y, s, st) : launch_state<128>(x, y, s, st);
+            e = DK == 64 ? launch_state<64>(x, y, hi, lo, s, st) : launch_state<128>(x, y, hi, lo, s, st);
             if (e == cudaSuccess)
                 e = la_scan(g.seg, a.H, a.dk * a.dv, s.back, w.seg[i], w.tot[i], first, last, st);
             if (e != cudaSuccess) return e;
@@ -1706,7 +1788,7 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
             s.plo = w.lo[0];
             s.dot = w.dot;
         }
-        e = DK == 64 ? launch_state<64>(x, y, s, st) : launch_state<128>(x, y, s, st);
+        e = DK == 64 ? launch_state<64>(x, y, hi, lo, s, st) : launch_state<128>(x, y, hi, lo, s, st);
         if (e != cudaSuccess) return e;
     }
     BackArgs b{};
