@@ -45,7 +45,7 @@ struct TcArgs {
     float *last;              // final states [sequence][h], or null
     __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
     const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
-    float *dot;               // [chunk][h][2][4]: a warp's share of <S_n, dS_{n+1}>, or null
+    float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
     bool back;                // from the end: (q, dO) in place of (k, v)
 };
 
@@ -227,35 +227,35 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
     if (lane == 0) d.tot = allf >= 0 ? 0.0f : ex2((float)all);
 }
 
-// Half of row t of a 64-column box of v (or dO) times w as two bf16 terms into
-// the boxes at hi and lo; zero where !on.
-SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int half, float w, bool on)
+// Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
+// times w as two bf16 terms into the boxes at hi and lo; zero where !on.  The
+// loops over columns in these kernels are rolled up on purpose: the warps of a
+// block run seven different codes at once, and unrolled they do not fit the
+// instruction cache.
+SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int p0, int p1, float w, bool on)
 {
-    uint4 v[4];
+#pragma unroll 1
+    for (int p = p0; p < p1; p += 2) {
+        uint4 v[2];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        v[p] = *reinterpret_cast<const uint4 *>(src + swz(t, 4 * half + p));
-        if (!on) v[p] = make_uint4(0, 0, 0, 0);
-    }
-    uint4 h[4], l[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const uint32_t x[4] = {v[p].x, v[p].y, v[p].z, v[p].w};
-        uint32_t y[4], z[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
-            y[i] = pack2(a, b);
-            z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
+        for (int k = 0; k < 2; ++k) {
+            v[k] = *reinterpret_cast<const uint4 *>(src + swz(t, p + k));
+            if (!on) v[k] = make_uint4(0, 0, 0, 0);
         }
-        h[p] = make_uint4(y[0], y[1], y[2], y[3]);
-        l[p] = make_uint4(z[0], z[1], z[2], z[3]);
-    }
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const uint32_t o = swz(t, 4 * half + p);
-        *reinterpret_cast<uint4 *>(hi + o) = h[p];
-        *reinterpret_cast<uint4 *>(lo + o) = l[p];
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            uint32_t y[4], z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
+                y[i] = pack2(a, b);
+                z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
+            }
+            const uint32_t o = swz(t, p + k);
+            *reinterpret_cast<uint4 *>(hi + o) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4 *>(lo + o) = make_uint4(z[0], z[1], z[2], z[3]);
+        }
     }
 }
 
@@ -349,7 +349,7 @@ SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, i
 // loads (a ring of NST chunks), warp 17 issues the MMAs, warps 18 and 19
 // compute the decays of every other chunk each.  Bound: the bytes of X and Y
 // and of the states written.  Those go out through shared memory by TMA (warps
-// 20-23): a lane holds a row of them, and stores from the registers, a line for
+// 20-27): a lane holds a row of them, and stores from the registers, a line for
 // each lane, took 5500 cycles a chunk where the rest takes 2000.
 // ---------------------------------------------------------------------------
 template <int DK>
@@ -363,7 +363,7 @@ struct StateShared {
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 
-constexpr int STATE_THREADS = 768;
+constexpr int STATE_THREADS = 896;
 
 template <int DK>
 __global__ void __launch_bounds__(STATE_THREADS, 1)
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             mbar_init(&drained[i], 8);
         }
         mbar_init(&staged, 8);
-        mbar_init(&unstaged, 4);
+        mbar_init(&unstaged, 8);
         mbar_init(&fin, 1);
         mbar_init_fence();
         s_abort = 0;
@@ -458,12 +458,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         for (int n = 0; n < nch && g.hi; ++n) {
             const long long ci = (sg.c0 + chunk(n)) * a.H + h;
             float s = 0.0f;
-            constexpr int NP = DK / 16;   // 16-byte pieces of a thread
+            constexpr int NP = DK / 32;   // 16-byte pieces of a thread
             uint4 y[NP], z[NP];
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const int idx = (warp - 20) * 32 + lane + 128 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
+                    const int idx = (warp - 20) * 32 + lane + 256 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
                     y[i] = z[i] = make_uint4(0, 0, 0, 0);
                     if (r < a.dk && c < a.dv) {
                         const long long at = ci * a.dk * a.dv + (long long)r * a.dv + c;
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const int idx = (warp - 20) * 32 + lane + 128 * i;
+                    const int idx = (warp - 20) * 32 + lane + 256 * i;
                     const uint8_t *at = smem + SM::OUT + swz(idx >> 3, idx & 7);
                     const uint4 u = *reinterpret_cast<const uint4 *>(at);
                     const uint4 w = *reinterpret_cast<const uint4 *>(at + DK * 128);
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) g.dot[(ci * 2 + tile) * 4 + warp - 20] = s;
+                if (lane == 0) g.dot[(ci * 2 + tile) * 8 + warp - 20] = s;
             }
             if (warp == 20 && lane == 0) bulk_wait_read_all();
             warp_arrive(&unstaged);
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             const TcDecays &d = dec[n % ND];
             const int len = rows(n);
             uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
-            scale_row(st + SM::NB * BOX, y, y + BOX, t, half, back ? a.scale * d.row[t] : d.col[t], t < len);
+            scale_row(st + SM::NB * BOX, y, y + BOX, t, 4 * half, 4 * half + 4, back ? a.scale * d.row[t] : d.col[t], t < len);
             // rows behind a packed sequence belong to another one
             if (packed && t >= len)
                 for (int i = half; i < SM::NB; i += 2) zero_row(st + i * BOX, t);
@@ -863,9 +863,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // the product that read the last terms
             if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_abort)) break;
             const float w = dec[n % ND].col[t];
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, half, w, t < len);
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 8, w, t < len);
             tma_store_fence();
             warp_arrive(&yready);
             warp_arrive(&dempty[n % ND]);
@@ -874,32 +872,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         const int q = warp & 3, half = ((warp - 12) >> 2) & 1;
         const int i = q * 32 + lane;   // query row
         const uint32_t la = (uint32_t)(q * 32) << 16;
-        // the keys of 32-row block b, this thread's query: weights of v in place of w
-        auto weigh = [&](const TcDecays &d, int b, const float (&v)[32], uint32_t (&p)[16]) {
-            if (b < q) {
-                const float ri = d.rq[i];
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 e = *reinterpret_cast<const float4 *>(&d.cq[q - 1][32 * b + j]);
-                    p[j / 2] = pack2(v[j] * (ri * e.x), v[j + 1] * (ri * e.y));
-                    p[j / 2 + 1] = pack2(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w));
-                }
-            } else {
-                const float li = d.loc[i];
-                const int f = max(d.first[i] - 32 * q, 0);
-                const uint32_t span = (uint32_t)(lane - f);
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(&d.loc[32 * b + j]);
-                    const float e[4] = {ex2(li - l.x), ex2(li - l.y), ex2(li - l.z), ex2(li - l.w)};
-                    float x[4];
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) x[z] = (uint32_t)(j + z - f) <= span ? v[j + z] * e[z] : 0.0f;
-                    p[j / 2] = pack2(x[0], x[1]);
-                    p[j / 2 + 1] = pack2(x[2], x[3]);
-                }
-            }
-        };
         for (int n = 0; n < nch; ++n) {
             if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
             if (!warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
@@ -907,18 +879,42 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             const TcDecays &d = dec[n % ND];
             // 64 keys of this warp; their bf16 weights over the first half of their scores
             const uint32_t sc = tmem + (n & 1) * 128 + 64 * half + la;
+            const float ri = d.rq[i], li = d.loc[i];
+            const int f = max(d.first[i] - 32 * q, 0);   // first key of its own 32 that reaches the query
+            const uint32_t span = (uint32_t)(lane - f);
+#pragma unroll 1
+            for (int z = 0; z < 4; ++z) {   // 16 keys at a time
+                const int b = 2 * half + (z >> 1), key = 64 * half + 16 * z;
+                uint32_t p[8];
+                if (b <= q) {
+                    float v[16];
+                    tmem_ld16(sc + 16 * z, v);
+                    if (b < q) {
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                uint32_t p[16];
-                if (2 * half + z <= q) {
-                    float v[32];
-                    tmem_ld32(sc + 32 * z, v);
-                    weigh(d, 2 * half + z, v, p);
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 e = *reinterpret_cast<const float4 *>(&d.cq[q - 1][key + j]);
+                            p[j / 2] = pack2(v[j] * (ri * e.x), v[j + 1] * (ri * e.y));
+                            p[j / 2 + 1] = pack2(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w));
+                        }
+                    } else {
+                        const int k0 = 16 * (z & 1) - f;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(&d.loc[key + j]);
+                            const float e[4] = {ex2(li - l.x), ex2(li - l.y), ex2(li - l.z), ex2(li - l.w)};
+                            float x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = (uint32_t)(k0 + j + k) <= span ? v[j + k] * e[k] : 0.0f;
+                            p[j / 2] = pack2(x[0], x[1]);
+                            p[j / 2 + 1] = pack2(x[2], x[3]);
+                        }
+                    }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) p[j] = 0u;
+                    for (int j = 0; j < 8; ++j) p[j] = 0u;
                 }
-                tmem_st16(sc + 16 * z, p);
+                tmem_st8(sc + 8 * z, p);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -941,25 +937,23 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             ok = ok && warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
-            uint4 y[8];
-#pragma unroll
+            const bool on = n * TCC + i < sg.len;
+#pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
                 float u[16], w[16];
                 tmem_ld16x2(t_o1 + la + c, t_o2 + la + c, u, w);
+                if (c == 48) {
+                    tc_fence_before();
+                    warp_arrive(&oempty);
+                }
                 uint32_t p[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
                                  fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
-                y[c / 8] = make_uint4(p[0], p[1], p[2], p[3]);
-                y[c / 8 + 1] = make_uint4(p[4], p[5], p[6], p[7]);
-            }
-            tc_fence_before();
-            warp_arrive(&oempty);
-            if (n * TCC + i < sg.len) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * j < cols) *reinterpret_cast<uint4 *>(o + n * step + 8 * j) = y[j];
+                uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
+                if (on && c < cols) dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                if (on && c + 8 < cols) dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
             }
         }
         if (!ok)
@@ -1289,9 +1283,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     if (lane >= o) ws += wu;
                 }
                 double dot = 0.0;
-                if (lane < 8 && lane / 4 < g.tiles) dot = g.dot[((long long)c * a.H + h) * 8 + lane];
+                if (lane < 16 && lane / 8 < g.tiles) dot = g.dot[((long long)c * a.H + h) * 16 + lane];
 #pragma unroll
-                for (int o = 4; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
                 dot = __shfl_sync(0xffffffffu, dot, 0) * (double)d.tot;
                 double back = xs - xl, front = ws - wl;   // rows behind this lane's, rows before
                 float out[4], sum = 0.0f;
@@ -1655,7 +1649,7 @@ BackWs back_layout(const LaArgs &a, int L, void *ws)
         w.hi[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
         w.lo[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
     }
-    w.dot = reinterpret_cast<float *>(take(4 * n * 8));
+    w.dot = reinterpret_cast<float *>(take(4 * n * 16));
     w.dgc = reinterpret_cast<float *>(take(4 * n));
     if (a.H != a.Hqk) {
         w.pq = reinterpret_cast<float *>(take(4 * rows * a.H * a.dk));
