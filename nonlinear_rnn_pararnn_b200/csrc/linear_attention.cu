@@ -171,39 +171,61 @@ __global__ void __launch_bounds__(NT) la_delta_kernel(LaArgs a, LaChunks ch, boo
         }
 }
 
-// The states over the chunks of each sequence, one thread for an element: the
-// deltas in `buf` give way to the state that enters each chunk (forward) or the
+// The states over the chunks of each sequence, V elements a thread: the deltas
+// in `buf` give way to the state that enters each chunk (forward) or the
 // gradient of the state that leaves it (back).  first: s0 or dsT (null: zero);
 // last: sT or ds0 (may be null).  Bound by the bytes of buf, read and written
-// once; eight chunks are loaded ahead of the eight that are being joined.
-__global__ void __launch_bounds__(256) la_scan_kernel(LaChunks ch, int H, int E, bool back, float *buf,
+// once; eight chunks are loaded at a time, ahead of their joining.
+template <int V>
+__global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E, bool back, float *buf,
                                                       const float *__restrict__ tot, const float *first, float *last)
 {
-    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int e = (blockIdx.y * 128 + threadIdx.x) * V;
     const int seq = blockIdx.x / H, h = blockIdx.x % H;
     if (e >= E) return;
     const int c0 = ch.pos ? ch.coff[seq] : seq * ch.nc;
     const int n = ch.pos ? ch.coff[seq + 1] - c0 : ch.nc;
     const long long at = ((long long)seq * H + h) * E + e;
-    float s = first ? first[at] : 0.0f;
-    for (int i0 = 0; i0 < n; i0 += 8) {
-        float dl[8], tt[8];
-        const long long c1 = back ? c0 + n - 1 - i0 : c0 + i0, d1 = back ? -1 : 1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const bool on = i0 + i < n;
-            const long long c = on ? c1 + i * d1 : c1;
-            dl[i] = buf[(c * H + h) * E + e];
-            tt[i] = tot[c * H + h];
+    auto load = [](const float *p, float (&v)[V]) {
+        if (V == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p);
+            v[0] = f.x;
+            v[V > 1 ? 1 : 0] = f.y;
+            v[V > 2 ? 2 : 0] = f.z;
+            v[V > 3 ? 3 : 0] = f.w;
+        } else {
+            v[0] = *p;
         }
+    };
+    auto store = [](float *p, const float (&v)[V]) {
+        if (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[V > 1 ? 1 : 0], v[V > 2 ? 2 : 0], v[V > 3 ? 3 : 0]);
+        else *p = v[0];
+    };
+    float s[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) s[k] = 0.0f;
+    if (first) load(first + at, s);
+    const long long step = (back ? -1LL : 1LL) * H * E;
+    float *p = buf + ((long long)(back ? c0 + n - 1 : c0) * H + h) * E + e;
+    const float *t = tot + (long long)(back ? c0 + n - 1 : c0) * H + h;
+    const int ts = back ? -H : H;
+    for (int i0 = 0; i0 < n; i0 += 8, p += 8 * step, t += 8 * ts) {
+        float dl[8][V], tt[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i0 + i < n) {
-                buf[((c1 + i * d1) * H + h) * E + e] = s;
-                s = fmaf(tt[i], s, dl[i]);
+                load(p + i * step, dl[i]);
+                tt[i] = t[i * ts];
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i0 + i < n) {
+                store(p + i * step, s);
+#pragma unroll
+                for (int k = 0; k < V; ++k) s[k] = fmaf(tt[i], s[k], dl[i][k]);
             }
     }
-    if (last) last[at] = s;
+    if (last) store(last + at, s);
 }
 
 // The outputs of a chunk and head.
@@ -556,8 +578,12 @@ cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStre
 cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,
                     float *last, cudaStream_t st)
 {
-    la_scan_kernel<<<dim3((unsigned)ch.n_seq * H, (E + 255) / 256), 256, 0, st>>>(ch, H, E, back, buf, tot, first,
-                                                                                last);
+    if (E % 4 == 0)
+        la_scan_kernel<4><<<dim3((unsigned)ch.n_seq * H, (E + 511) / 512), 128, 0, st>>>(ch, H, E, back, buf, tot,
+                                                                                       first, last);
+    else
+        la_scan_kernel<1><<<dim3((unsigned)ch.n_seq * H, (E + 127) / 128), 128, 0, st>>>(ch, H, E, back, buf, tot,
+                                                                                       first, last);
     return cudaGetLastError();
 }
 

@@ -30,25 +30,6 @@ constexpr uint32_t BOX = TCC * 128;          // bytes of 128 rows of 64 bf16
 constexpr uint64_t TC_WAIT_NS = 1000000000ull;
 constexpr int ND = 4;                        // chunks whose decays are held
 
-// Blocks of one pass: a segment (a run of chunks of one sequence) of one head
-// and 64 columns of the state.
-struct TcArgs {
-    LaArgs a;
-    LaChunks seg;             // the segments
-    LaChunks ch;              // the chunks (packed: the table's second view)
-    int tiles;                // 64-column tiles of d_v
-    // states: where a segment starts and what it leaves
-    const float *init;        // entry states [segment][h], or null: first
-    const float *first;       // entry states [sequence][h] (null: zero)
-    float *fin;               // final states [segment][h], or null: last
-    float *fin_tot;           // [segment][h] decay of a segment
-    float *last;              // final states [sequence][h], or null
-    __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
-    const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
-    float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
-    bool back;                // from the end: (q, dO) in place of (k, v)
-};
-
 // The decays of a chunk.  D_ij = e^{c_i - c_j} of rows i in 32-row block q and
 // j in an earlier one is rq[i] cq[q - 1][j], by way of the block's first row
 // (both factors are at most 1 where nothing grows): one exponential a row and
@@ -64,6 +45,26 @@ struct alignas(16) TcDecays {
     float tot;
 };
 static_assert(sizeof(TcDecays) % 16 == 0, "an array of them in shared memory, read 16 bytes at a time");
+
+// Blocks of one pass: a segment (a run of chunks of one sequence) of one head
+// and 64 columns of the state.
+struct TcArgs {
+    LaArgs a;
+    const TcDecays *dec;      // [chunk][h]
+    LaChunks seg;             // the segments
+    LaChunks ch;              // the chunks (packed: the table's second view)
+    int tiles;                // 64-column tiles of d_v
+    // states: where a segment starts and what it leaves
+    const float *init;        // entry states [segment][h], or null: first
+    const float *first;       // entry states [sequence][h] (null: zero)
+    float *fin;               // final states [segment][h], or null: last
+    float *fin_tot;           // [segment][h] decay of a segment
+    float *last;              // final states [sequence][h], or null
+    __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
+    const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
+    float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
+    bool back;                // from the end: (q, dO) in place of (k, v)
+};
 
 SLSTM_DEVINL float ex2(float x)
 {
@@ -227,6 +228,21 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
     if (lane == 0) d.tot = allf >= 0 ? 0.0f : ex2((float)all);
 }
 
+// The decays of every chunk and head, [chunk][h], a warp each: about 250
+// instructions one after another, which inside the kernels below took two warps
+// 2500 cycles a chunk, longer than anything else there.
+__global__ void __launch_bounds__(256) la_decay_kernel(LaArgs a, LaChunks ch, TcDecays *out)
+{
+    const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int h = (int)(i % a.H);
+    if (i / a.H >= ch.total) return;
+    const LaChunk c = la_chunk(ch, (int)(i / a.H));
+    if (c.len <= 0) return;
+    float gv[4];
+    load_decays(gv, a, c.row, c.len, h, threadIdx.x & 31);
+    tc_decays(out[i], gv, threadIdx.x & 31);
+}
+
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
 // times w as two bf16 terms into the boxes at hi and lo; zero where !on.  The
 // loops over columns in these kernels are rolled up on purpose: the warps of a
@@ -346,10 +362,9 @@ SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, i
 // backward kernel) and / or the final one.  The work of a chunk is split over
 // warps that run a chunk apart, since each part of it is a chain of latencies:
 // warps 0-7 hold the state (lane = row of d_k), warps 8-15 scale Y, warp 16
-// loads (a ring of NST chunks), warp 17 issues the MMAs, warps 18 and 19
-// compute the decays of every other chunk each.  Bound: the bytes of X and Y
-// and of the states written.  Those go out through shared memory by TMA (warps
-// 20-27): a lane holds a row of them, and stores from the registers, a line for
+// loads (a ring of NST chunks), warp 17 issues the MMAs.  Bound: the bytes of X
+// and Y and of the states written.  Those go out through shared memory by TMA (warps
+// 18-25): a lane holds a row of them, and stores from the registers, a line for
 // each lane, took 5500 cycles a chunk where the rest takes 2000.
 // ---------------------------------------------------------------------------
 template <int DK>
@@ -363,7 +378,7 @@ struct StateShared {
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 
-constexpr int STATE_THREADS = 896;
+constexpr int STATE_THREADS = 832;
 
 template <int DK>
 __global__ void __launch_bounds__(STATE_THREADS, 1)
@@ -422,7 +437,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             for (; n < nch; ++n) {
                 const int s = n % NST;
                 if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) break;
+                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
                 uint8_t *st = smem + s * SM::STAGE;
+                mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
+                bulk_load(&dec[n % ND], g.dec + (sg.c0 + chunk(n)) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
                 mbar_expect_tx(&full[s], SM::STAGE);
                 const int t = sg.t + chunk(n) * TCC;
 #pragma unroll
@@ -453,7 +471,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             }
             umma_commit(&fin);
         }
-    } else if (warp >= 20) {
+    } else if (warp >= 18) {
         // the state in shared memory: stored, and met with the forward one for dg
         for (int n = 0; n < nch && g.hi; ++n) {
             const long long ci = (sg.c0 + chunk(n)) * a.H + h;
@@ -463,7 +481,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const int idx = (warp - 20) * 32 + lane + 256 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
+                    const int idx = (warp - 18) * 32 + lane + 256 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
                     y[i] = z[i] = make_uint4(0, 0, 0, 0);
                     if (r < a.dk && c < a.dv) {
                         const long long at = ci * a.dk * a.dv + (long long)r * a.dv + c;
@@ -473,7 +491,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 }
             }
             if (!warp_wait(&staged, (uint32_t)n & 1u, &s_abort)) break;
-            if (warp == 20 && lane == 0) {
+            if (warp == 18 && lane == 0) {
                 tma_store_3d(&mhi, smem + SM::OUT, 64 * tile, 0, (int)ci);
                 tma_store_3d(&mlo, smem + SM::OUT + DK * 128, 64 * tile, 0, (int)ci);
                 bulk_commit();
@@ -481,7 +499,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    const int idx = (warp - 20) * 32 + lane + 256 * i;
+                    const int idx = (warp - 18) * 32 + lane + 256 * i;
                     const uint8_t *at = smem + SM::OUT + swz(idx >> 3, idx & 7);
                     const uint4 u = *reinterpret_cast<const uint4 *>(at);
                     const uint4 w = *reinterpret_cast<const uint4 *>(at + DK * 128);
@@ -495,23 +513,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) g.dot[(ci * 2 + tile) * 8 + warp - 20] = s;
+                if (lane == 0) g.dot[(ci * 2 + tile) * 8 + warp - 18] = s;
             }
-            if (warp == 20 && lane == 0) bulk_wait_read_all();
+            if (warp == 18 && lane == 0) bulk_wait_read_all();
             warp_arrive(&unstaged);
         }
-        if (warp == 20 && lane == 0) bulk_wait_all();
-    } else if (warp >= 18) {
-        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (warp - 18 < nch) load_decays(gn, a, sg.row + (long long)chunk(warp - 18) * TCC, rows(warp - 18), h, lane);
-        for (int n = warp - 18; n < nch; n += 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
-            if (n + 2 < nch) load_decays(gn, a, sg.row + (long long)chunk(n + 2) * TCC, rows(n + 2), h, lane);
-            if (!warp_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
-            tc_decays(dec[n % ND], gv, lane);
-            warp_arrive(&dfull[n % ND]);
-        }
+        if (warp == 18 && lane == 0) bulk_wait_all();
     } else if (warp >= 8) {
         const int t = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
         for (int n = 0; n < nch; ++n) {
@@ -595,7 +602,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     if (threadIdx.x == 0) {
         if (s_abort)
             for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
+                {
                 (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
+                (void)mbar_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, TC_WAIT_NS);
+            }
         (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
     }
     __syncthreads();
@@ -616,7 +626,6 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 //   warps 20-23 the outputs
 //   warp 24     loads (a ring of NST chunks) and the MMAs of k^T (w v)
 //   warp 25     the other MMAs
-//   warps 26-27 the decays of every other chunk each, up to three chunks ahead
 // Each of these is a chain of latencies some 1500 cycles long; apart from one
 // another they run a chunk or two ahead or behind, and a chunk takes as long as
 // the longest of them, not as all.
@@ -636,7 +645,7 @@ struct FwdShared {
 };
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
-constexpr int FWD_THREADS = 896;
+constexpr int FWD_THREADS = 832;
 
 template <int DK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -701,7 +710,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             auto load = [&](int n) -> bool {
                 const int s = n % NST;
                 if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) return false;
+                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) return false;
                 uint8_t *st = smem + s * SM::STAGE;
+                mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
+                bulk_load(&dec[n % ND], g.dec + (sg.c0 + n) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
                 mbar_expect_tx(&full[s], SM::STAGE);
                 const int t = sg.t + n * TCC;
 #pragma unroll
@@ -799,20 +811,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 umma_commit(&empty[s]);
             }
             umma_commit(&fin);
-        }
-    } else if (warp >= 26) {
-        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto load = [&](int n) {
-            if (n < nch) load_decays(gn, a, sg.row + (long long)n * TCC, min(TCC, sg.len - n * TCC), h, lane);
-        };
-        load(warp - 26);
-        for (int n = warp - 26; n < nch; n += 2) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
-            load(n + 2);
-            if (!warp_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
-            tc_decays(dec[n % ND], gv, lane);
-            warp_arrive(&dfull[n % ND]);
         }
     } else if (warp < 8) {
         typedef Share<DK> SH;
@@ -965,7 +963,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (threadIdx.x == 0) {
         if (s_abort)
             for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
+                {
                 (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
+                (void)mbar_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, TC_WAIT_NS);
+            }
         (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
     }
     __syncthreads();
@@ -989,7 +990,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 // other products are then added (dv's stay apart).  u_i and w_j of dg are the
 // dot products of q_i and k_j with those rows.
 //   warps 0-15  lane quarter q = warp & 3, columns 32 b .. of b = warp >> 2
-//   warp 16     loads;  warp 17 MMAs;  warp 18 decays;  warp 19 dg
+//   warp 16     loads;  warp 17 MMAs;  warp 18 dg
 // Tensor memory: [0, 128) q k^T, then k dS; [128, 256) dO v^T, then P^T dO;
 // [256, 384) dq; [384, 512) dk.  Shared memory holds q, k, v, dO and two 32 KB
 // buffers that take S, then dS, then P^T and Pd^T.  Bound: the bytes of q, k,
@@ -997,6 +998,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 // ---------------------------------------------------------------------------
 struct BackArgs {
     LaArgs a;
+    const TcDecays *dec;   // [chunk][h]
     LaChunks ch;
     int total;             // items where the sequences are dense
     float *part_q, *part_k;
@@ -1016,7 +1018,7 @@ struct BackShared {
 };
 static_assert(BackShared<128, 128>::BYTES + 1024 <= 227 * 1024, "backward shared memory");
 
-constexpr int BACK_THREADS = 640;
+constexpr int BACK_THREADS = 608;
 
 // A thread's 32 columns of a row in bf16 from a swizzled box pair.
 SLSTM_DEVINL float dot_row(const uint8_t *tile, int row, int b, const float (&v)[32])
@@ -1120,6 +1122,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 const int t = packed ? (int)ck.row : ck.n * TCC, b = packed ? 0 : ck.seq;
                 const uint32_t ph = (uint32_t)it & 1u;
                 if (it > 0 && !lane_wait(&bout, ph ^ 1u, &s_abort)) break;
+                if (!lane_wait(&dempty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s_abort)) break;
+                mbar_expect_tx(&dfull[it & 1], sizeof(TcDecays));
+                bulk_load(&dec[it & 1], g.dec + item, sizeof(TcDecays), &dfull[it & 1]);
                 mbar_expect_tx(&full1, 2 * NK * BOX);
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
@@ -1227,24 +1232,6 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             umma_commit(&fin);
         }
     } else if (warp == 18) {
-        float gv[4], gn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto load = [&](int item) {
-            if (item < items) {
-                const LaChunk ck = la_chunk(g.ch, item / a.H);
-                load_decays(gn, a, ck.row, ck.len, item % a.H, lane);
-            }
-        };
-        load(blockIdx.x);
-        int it = 0;
-        for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) gv[i] = gn[i];
-            load(item + gridDim.x);
-            if (!warp_wait(&dempty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s_abort)) break;
-            tc_decays(dec[it & 1], gv, lane);
-            warp_arrive(&dfull[it & 1]);
-        }
-    } else if (warp == 19) {
         // dg of four rows a lane from the parts of r, c, u, w, in 64 bits: the
         // sums over the chunk cancel
         int it = 0;
@@ -1487,6 +1474,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     if (threadIdx.x == 0) {
         if (s_abort && s_loaded > 0) {
             const uint32_t ph = (uint32_t)((s_loaded - 1) / 2) & 1u;
+            const int it = (s_loaded - 1) / 2;
+            (void)mbar_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, TC_WAIT_NS);
             (void)mbar_wait(&full1, ph, TC_WAIT_NS);
             (void)mbar_wait(&full2, ph, TC_WAIT_NS);
             (void)mbar_wait(&fullS, ph, TC_WAIT_NS);
@@ -1546,8 +1535,9 @@ int seg_chunks(const LaArgs &a, int per_item)
     for (int n = 1; n <= nc / 4 && n <= 64; ++n) {
         const int len = (nc + n - 1) / n;
         const long long waves = (base * n + 147) / 148;
-        // the pass for the first states costs about two thirds of a segment
-        const double t = (double)waves * len * (n > 1 ? 1.67 : 1.0);
+        // the pass for the first states costs about half a segment, a block's start
+        // about three chunks, and a segment's state in the scan something too
+        const double t = (double)waves * (len + 3) * (n > 1 ? 1.5 : 1.0) + 0.1 * n;
         if (t < best_t) {
             best_t = t;
             best = len;
@@ -1558,6 +1548,7 @@ int seg_chunks(const LaArgs &a, int per_item)
 
 struct FwdWs {
     char *table, *seg_table;
+    TcDecays *dec;
     float *states, *tot;
     size_t bytes;
 };
@@ -1573,6 +1564,7 @@ FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
     };
     w.table = take(la_table_bytes(a));
     w.seg_table = take(la_table_bytes(a));
+    w.dec = reinterpret_cast<TcDecays *>(take(sizeof(TcDecays) * la_chunk_bound(a, TCC) * a.H));
     if (L < (a.T - 1) / TCC + 1) {
         const size_t items = (size_t)la_chunk_bound(a, L * TCC);
         w.states = reinterpret_cast<float *>(take(4 * items * a.H * a.dk * a.dv));
@@ -1580,6 +1572,12 @@ FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
     }
     w.bytes = (size_t)(p - static_cast<char *>(ws));
     return w;
+}
+
+cudaError_t launch_decays(const LaArgs &a, const LaChunks &ch, TcDecays *dec, cudaStream_t st)
+{
+    la_decay_kernel<<<(unsigned)(((long long)ch.total * a.H + 7) / 8), 256, 0, st>>>(a, ch, dec);
+    return cudaGetLastError();
 }
 
 template <int DK>
@@ -1621,6 +1619,7 @@ bool state_map(CUtensorMap *m, const void *p, const LaArgs &a, long long n, int 
 
 struct BackWs {
     char *table, *seg_table;
+    TcDecays *dec;
     float *seg[2], *tot[2];            // a segment's first states, forward and from the end
     __nv_bfloat16 *hi[2], *lo[2];      // the chunks' states
     float *dot, *dgc, *pq, *pk;
@@ -1640,6 +1639,7 @@ BackWs back_layout(const LaArgs &a, int L, void *ws)
     const size_t rows = a.cu ? (size_t)a.T : (size_t)a.B * a.T;
     w.table = take(la_table_bytes(a));
     w.seg_table = take(la_table_bytes(a));
+    w.dec = reinterpret_cast<TcDecays *>(take(sizeof(TcDecays) * n));
     for (int i = 0; i < 2; ++i) {
         if (L < (a.T - 1) / TCC + 1) {
             const size_t items = (size_t)la_chunk_bound(a, L * TCC) * a.H;
@@ -1693,7 +1693,9 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
     const FwdWs w = fwd_layout(a, L, ws);
     cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
     if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
+    g.dec = w.dec;
     CUtensorMap m[4];
     if (!token_map(&m[0], a.q, a.dk, a.Hqk, a.ldq, a) || !token_map(&m[1], a.k, a.dk, a.Hqk, a.ldk, a) ||
         !token_map(&m[2], a.v, a.dv, a.H, a.ldv, a))
@@ -1737,7 +1739,9 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     const int DK = a.dk <= 64 ? 64 : 128, DV = a.dv <= 64 ? 64 : 128;
     cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
     if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
+    g.dec = w.dec;
     const long long n = (long long)g.ch.total * a.H;
     CUtensorMap m[8];
     bool ok = token_map(&m[0], a.q, a.dk, a.Hqk, a.ldq, a) && token_map(&m[1], a.k, a.dk, a.Hqk, a.ldk, a) &&
@@ -1788,6 +1792,7 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     BackArgs b{};
     b.a = a;
     b.ch = g.ch;
+    b.dec = w.dec;
     b.total = (int)n;
     b.part_q = w.pq;
     b.part_k = w.pk;
