@@ -57,9 +57,9 @@ cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStre
 // E-element deltas in buf[chunk][h], with the decays tot[chunk][h], give way to
 // the state that enters each (back: the gradient of the one that leaves it),
 // starting from first[sequence][h] (null: zero); the last one to `last` (or
-// null).
+// null).  Sequences of `skip` chunks are left alone.
 cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,
-                    float *last, cudaStream_t st);
+                    float *last, cudaStream_t st, int skip = -1);
 
 // bf16 on the tensor cores.
 bool la_tc_takes(const LaArgs &a);

@@ -178,13 +178,15 @@ __global__ void __launch_bounds__(NT) la_delta_kernel(LaArgs a, LaChunks ch, boo
 // once; eight chunks are loaded at a time, ahead of their joining.
 template <int V>
 __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E, bool back, float *buf,
-                                                      const float *__restrict__ tot, const float *first, float *last)
+                                                      const float *__restrict__ tot, const float *first, float *last,
+                                                      int skip)
 {
     const int e = (blockIdx.y * 128 + threadIdx.x) * V;
     const int seq = blockIdx.x / H, h = blockIdx.x % H;
     if (e >= E) return;
     const int c0 = ch.pos ? ch.coff[seq] : seq * ch.nc;
     const int n = ch.pos ? ch.coff[seq + 1] - c0 : ch.nc;
+    if (n == skip) return;
     const long long at = ((long long)seq * H + h) * E + e;
     auto load = [](const float *p, float (&v)[V]) {
         if (V == 4) {
@@ -576,14 +578,14 @@ cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStre
 }
 
 cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,
-                    float *last, cudaStream_t st)
+                    float *last, cudaStream_t st, int skip)
 {
     if (E % 4 == 0)
         la_scan_kernel<4><<<dim3((unsigned)ch.n_seq * H, (E + 511) / 512), 128, 0, st>>>(ch, H, E, back, buf, tot,
-                                                                                       first, last);
+                                                                                       first, last, skip);
     else
         la_scan_kernel<1><<<dim3((unsigned)ch.n_seq * H, (E + 127) / 128), 128, 0, st>>>(ch, H, E, back, buf, tot,
-                                                                                       first, last);
+                                                                                       first, last, skip);
     return cudaGetLastError();
 }
 

@@ -55,11 +55,11 @@ struct TcArgs {
     LaChunks ch;              // the chunks (packed: the table's second view)
     int tiles;                // 64-column tiles of d_v
     // states: where a segment starts and what it leaves
-    const float *init;        // entry states [segment][h], or null: first
-    const float *first;       // entry states [sequence][h] (null: zero)
-    float *fin;               // final states [segment][h], or null: last
+    const float *init;        // entry states [segment][h] of sequences of several segments
+    const float *first;       // entry states [sequence][h] (null: zero) of the others
+    float *fin;               // the pass for `init`: final states [segment][h], of several segments
     float *fin_tot;           // [segment][h] decay of a segment
-    float *last;              // final states [sequence][h], or null
+    float *last;              // final states [sequence][h] of one segment, or null
     __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
     const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
     float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
@@ -84,6 +84,15 @@ SLSTM_DEVINL float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); 
 
 // Byte offset of 16-byte piece p of a row in a 128-byte-swizzled box.
 SLSTM_DEVINL uint32_t swz(int row, int p) { return (uint32_t)row * 128u + (uint32_t)((p ^ (row & 7)) << 4); }
+
+// A box of a tensor on its way into the L2 cache.
+SLSTM_DEVINL void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2, int c3)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
 
 // The first 1024-byte boundary in dynamic shared memory, by an offset: a pointer
 // that goes through an integer is no longer known to be shared memory, and every
@@ -243,34 +252,47 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaArgs a, LaChunks ch, Tc
     tc_decays(out[i], gv, threadIdx.x & 31);
 }
 
+// x w as two bf16 terms, two elements at a time, w itself given as two (wh, wl,
+// each in both halves): hi = x wh rounded, lo = (x wh - hi) + x wl, where the
+// difference is exact (a product of two 8-bit significands less its upper half)
+// and only lo is rounded once more.  Three instructions where widening to fp32,
+// rounding and taking the rest takes ten.
+SLSTM_DEVINL void split2(uint32_t x, uint32_t wh, uint32_t wl, uint32_t &hi, uint32_t &lo)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(x), "r"(wh));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(wh), "r"(hi ^ 0x80008000u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(x), "r"(wl), "r"(r));
+}
+
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
 // times w as two bf16 terms into the boxes at hi and lo; zero where !on.  The
 // loops over columns in these kernels are rolled up on purpose: the warps of a
-// block run seven different codes at once, and unrolled they do not fit the
+// block run six different codes at once, and unrolled they do not fit the
 // instruction cache.
 SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int p0, int p1, float w, bool on)
 {
+    const uint32_t wh = pack2(w, w);
+    const float rest = w - lo_of(wh);
+    const uint32_t wl = pack2(rest, rest);
 #pragma unroll 1
-    for (int p = p0; p < p1; p += 2) {
-        uint4 v[2];
+    for (int p = p0; p < p1; p += 4) {
+        uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < 4; ++k) {
             v[k] = *reinterpret_cast<const uint4 *>(src + swz(t, p + k));
             if (!on) v[k] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            uint32_t y[4], z[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = lo_of(x[i]) * w, b = hi_of(x[i]) * w;
-                y[i] = pack2(a, b);
-                z[i] = pack2(a - lo_of(y[i]), b - hi_of(y[i]));
-            }
+        for (int k = 0; k < 4; ++k) {
+            uint4 y, z;
+            split2(v[k].x, wh, wl, y.x, z.x);
+            split2(v[k].y, wh, wl, y.y, z.y);
+            split2(v[k].z, wh, wl, y.z, z.z);
+            split2(v[k].w, wh, wl, y.w, z.w);
             const uint32_t o = swz(t, p + k);
-            *reinterpret_cast<uint4 *>(hi + o) = make_uint4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<uint4 *>(lo + o) = make_uint4(z[0], z[1], z[2], z[3]);
+            *reinterpret_cast<uint4 *>(hi + o) = y;
+            *reinterpret_cast<uint4 *>(lo + o) = z;
         }
     }
 }
@@ -287,6 +309,7 @@ struct Seg {
     long long row;            // first row
     int t, b;                 // TMA coordinates of the first row
     long long c0;             // index of its first chunk
+    bool only;                // the sequence is one segment
 };
 
 SLSTM_DEVINL bool seg_of(const TcArgs &g, int i, Seg *s)
@@ -301,6 +324,7 @@ SLSTM_DEVINL bool seg_of(const TcArgs &g, int i, Seg *s)
     s->t = packed ? (int)c.row : c.n * g.seg.C;
     s->b = packed ? 0 : c.seq;
     s->c0 = (packed ? (long long)g.ch.coff[c.seq] : (long long)c.seq * g.ch.nc) + (long long)c.n * (g.seg.C / TCC);
+    s->only = c.count == 1;
     return true;
 }
 
@@ -396,7 +420,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     const LaArgs &a = g.a;
     const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
     Seg sg;
-    if (!seg_of(g, item, &sg)) return;
+    if (!seg_of(g, item, &sg) || (g.fin && sg.only)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool back = g.back, packed = g.seg.pos != nullptr;
     if (threadIdx.x == 0) {
@@ -446,6 +470,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, &mx, &full[s], 64 * i, hq, t, sg.b);
                 tma_load_4d(st + SM::NB * BOX, &my, &full[s], 64 * tile, h, t, sg.b);
+                if (n + NST < nch) {   // the chunk that takes this one's place, as far as the L2 cache
+                    const int u = sg.t + chunk(n + NST) * TCC;
+#pragma unroll
+                    for (int i = 0; i < SM::NB; ++i) tma_prefetch_4d(&mx, 64 * i, hq, u, sg.b);
+                    tma_prefetch_4d(&my, 64 * tile, h, u, sg.b);
+                }
             }
             s_loaded = n;
         }
@@ -489,6 +519,14 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                         z[i] = __ldg(reinterpret_cast<const uint4 *>(g.plo + at));
                     }
                 }
+            }
+            if (g.dot && n + 1 < nch) {
+                // the next one's rows of 64 columns (a line each) into the L2 cache
+                const int r = (warp - 18) * 32 + lane;
+                const __nv_bfloat16 *p = r < 128 ? g.phi : g.plo;
+                if ((r & 127) < a.dk)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                        p + ((sg.c0 + chunk(n + 1)) * a.H + h) * a.dk * a.dv + (long long)(r & 127) * a.dv + 64 * tile));
             }
             if (!warp_wait(&staged, (uint32_t)n & 1u, &s_abort)) break;
             if (warp == 18 && lane == 0) {
@@ -543,8 +581,9 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         typedef Share<DK> SH;
         const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
         const long long E = (long long)a.dk * a.dv;
-        const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
-                                  : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
+        const float *src = g.init && !sg.only ? g.init + ((long long)item * a.H + h) * E
+                                              : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E
+                                                         : nullptr);
         float S[SH::N];
         state_load(S, src, a.dk, a.dv, r, col);
         float run = 1.0f;
@@ -593,7 +632,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                         g.hi[((sg.c0 + n) * a.H + h) * E + (long long)r * a.dv + col + i] = __float2bfloat16(S[0]);
         }
         float *dst = g.fin ? g.fin + ((long long)item * a.H + h) * E
-                           : (g.last ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
+                           : (g.last && sg.only ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
         if (dst) state_store(S, dst, a.dk, a.dv, r, col);
         if (g.fin && tile == 0 && threadIdx.x == 0) g.fin_tot[(long long)item * a.H + h] = run;
     }
@@ -723,6 +762,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 tma_load_4d(st + 2 * SM::NB * BOX, &mv, &full[s], 64 * tile, h, t, sg.b);
                 s_loaded = n + 1;
+                if (n + NST < nch) {   // the chunk that takes this one's place, as far as the L2 cache
+                    const int u = t + NST * TCC;
+#pragma unroll
+                    for (int i = 0; i < SM::NB; ++i) {
+                        tma_prefetch_4d(&mq, 64 * i, hq, u, sg.b);
+                        tma_prefetch_4d(&mk, 64 * i, hq, u, sg.b);
+                    }
+                    tma_prefetch_4d(&mv, 64 * tile, h, u, sg.b);
+                }
                 return true;
             };
             bool ok = true;
@@ -816,8 +864,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         typedef Share<DK> SH;
         const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
         const long long E = (long long)a.dk * a.dv;
-        const float *src = g.init ? g.init + ((long long)item * a.H + h) * E
-                                  : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E : nullptr);
+        const float *src = g.init && !sg.only ? g.init + ((long long)item * a.H + h) * E
+                                              : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E
+                                                         : nullptr);
         float S[SH::N];
         state_load(S, src, a.dk, a.dv, r, col);
         bool ok = true;
@@ -844,7 +893,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         if (!ok)
 #pragma unroll
             for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
-        if (g.last) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
+        if (g.last && sg.only) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
     } else if (warp < 12) {
         const int t = (warp & 3) * 32 + lane;
         for (int n = 0; n < nch; ++n) {
@@ -1527,7 +1576,13 @@ bool token_map(CUtensorMap *m, const void *p, int d, int heads, long long ld, co
 int seg_chunks(const LaArgs &a, int per_item)
 {
     const int nc = (a.T - 1) / TCC + 1;
-    if (a.cu) return nc > 4 ? 4 : nc;
+    if (a.cu) {
+        // packed: the lengths are not known here; a segment is as long as an even
+        // share of all chunks, so that the longest sequence takes no longer than
+        // the rest of the work, and one that is no longer is one segment
+        const long long share = ((long long)nc * per_item + 147) / 148;
+        return (int)min((long long)nc, max(share, 4LL));
+    }
     const long long base = (long long)a.B * per_item;
     if (base >= 120 || nc < 8) return nc;
     int best = nc;
@@ -1705,16 +1760,14 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
     if (w.states) {
         TcArgs s = g;
         s.first = nullptr;
-        s.last = nullptr;
         s.fin = w.states;
         s.fin_tot = w.tot;
         // (it stores no chunk's state: the last two maps are not used)
         e = a.dk <= 64 ? launch_state<64>(m[1], m[2], m[1], m[1], s, st)
                        : launch_state<128>(m[1], m[2], m[1], m[1], s, st);
-        if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st);
+        if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st, 1);
         if (e != cudaSuccess) return e;
         g.init = w.states;
-        g.last = nullptr;
     } else if (a.cu && a.sT) {
         const long long HE = (long long)a.H * a.dk * a.dv;
         la_empty_kernel<<<dim3(a.B, (unsigned)min((HE + 1023) / 1024, 64LL)), 256, 0, st>>>(g.seg, HE, a.s0, a.sT);
@@ -1763,7 +1816,7 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
             s.fin_tot = w.tot[i];
             e = DK == 64 ? launch_state<64>(x, y, hi, lo, s, st) : launch_state<128>(x, y, hi, lo, s, st);
             if (e == cudaSuccess)
-                e = la_scan(g.seg, a.H, a.dk * a.dv, s.back, w.seg[i], w.tot[i], first, last, st);
+                e = la_scan(g.seg, a.H, a.dk * a.dv, s.back, w.seg[i], w.tot[i], first, last, st, 1);
             if (e != cudaSuccess) return e;
             s.fin = nullptr;
             s.fin_tot = nullptr;
@@ -1776,9 +1829,9 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
                 e = cudaGetLastError();
                 if (e != cudaSuccess) return e;
             }
-            s.first = first;
-            s.last = last;
         }
+        s.first = first;
+        s.last = last;
         s.hi = w.hi[i];
         s.lo = w.lo[i];
         if (s.back && a.dg) {
