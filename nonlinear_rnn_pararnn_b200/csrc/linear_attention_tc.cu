@@ -106,6 +106,7 @@ SLSTM_DEVINL uint8_t *aligned_smem(uint8_t *raw) { return raw + ((1024u - (smem_
 SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
 {
     const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
     for (int i = 0; i < (1 << 20); ++i) {
         uint32_t ok;
         asm volatile(
@@ -276,15 +277,15 @@ SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t,
     const float rest = w - lo_of(wh);
     const uint32_t wl = pack2(rest, rest);
 #pragma unroll 1
-    for (int p = p0; p < p1; p += 4) {
-        uint4 v[4];
+    for (int p = p0; p < p1; p += 2) {
+        uint4 v[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             v[k] = *reinterpret_cast<const uint4 *>(src + swz(t, p + k));
             if (!on) v[k] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 2; ++k) {
             uint4 y, z;
             split2(v[k].x, wh, wl, y.x, z.x);
             split2(v[k].y, wh, wl, y.y, z.y);
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
                 // both terms of w Y side by side: X is read once for them
                 const uint64_t bd = smem_desc_mn_sw128(smem_u32(smem + SM::Y + (n & 1) * 2 * BOX), BOX);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k)
                     umma_bf16(tmem + (n & 1) * 128, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, idesc,
                               k > 0 ? 1u : 0u);
@@ -762,15 +763,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 tma_load_4d(st + 2 * SM::NB * BOX, &mv, &full[s], 64 * tile, h, t, sg.b);
                 s_loaded = n + 1;
-                if (n + NST < nch) {   // the chunk that takes this one's place, as far as the L2 cache
-                    const int u = t + NST * TCC;
-#pragma unroll
-                    for (int i = 0; i < SM::NB; ++i) {
-                        tma_prefetch_4d(&mq, 64 * i, hq, u, sg.b);
-                        tma_prefetch_4d(&mk, 64 * i, hq, u, sg.b);
-                    }
-                    tma_prefetch_4d(&mv, 64 * tile, h, u, sg.b);
-                }
                 return true;
             };
             bool ok = true;
@@ -787,7 +779,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 const uint64_t kt =
                     smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE + SM::NB * BOX), DK == 128 ? BOX : 0u);
                 const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k)
                     umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
                 umma_commit(&delta);
@@ -845,6 +837,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 // the next chunk's scores go ahead of this one's last product
                 // when its rows have come, and never make it wait
                 if (n + 1 < nch) {
+#pragma unroll 1
                     for (int i = 0; i < (1 << 20) && scored <= n + 1 && !mbar_try_wait(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
                         scores(n + 1, false);
                 }
@@ -852,7 +845,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k)
                     umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
                 umma_commit(&ofull);
@@ -1273,7 +1266,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     const uint64_t pt = smem_desc_k_sw128(sx1 + (k >> 2) * BOX) + 2 * (k & 3);
                     umma_bf16(R3, pt, qd + (2048u >> 4) * k, id_dk, 1u);
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k)
                     umma_bf16(R2, pdt + (2048u >> 4) * k, kd + (2048u >> 4) * k, id_dq, 1u);
                 umma_commit(&bout);
