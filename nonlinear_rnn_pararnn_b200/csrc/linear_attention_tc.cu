@@ -124,6 +124,21 @@ SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
     *(volatile int *)s_abort = 1;
     return false;
 }
+// Whether a phase has completed, without being suspended.
+SLSTM_DEVINL bool done(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0u;
+}
 // One wait of a whole warp: every lane the same answer.
 SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, int *s_abort)
 {
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
-    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], scfull[2];
+    __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
     __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
@@ -712,6 +727,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 2);
+            mbar_init(&vfull[i], 1);
+            mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
@@ -747,22 +764,27 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         if (lane == 0) {
             constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             const int hq = h / (a.H / a.Hqk);
+            // q and k come back into use before v does
             auto load = [&](int n) -> bool {
                 const int s = n % NST;
-                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) return false;
-                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) return false;
+                const uint32_t ph = ((uint32_t)(n / NST) & 1u) ^ 1u;
+                if (!lane_wait(&empty[s], ph, &s_abort)) return false;
                 uint8_t *st = smem + s * SM::STAGE;
-                mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
-                bulk_load(&dec[n % ND], g.dec + (sg.c0 + n) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
-                mbar_expect_tx(&full[s], SM::STAGE);
+                mbar_expect_tx(&full[s], 2 * SM::NB * BOX);
                 const int t = sg.t + n * TCC;
 #pragma unroll
                 for (int i = 0; i < SM::NB; ++i) {
                     tma_load_4d(st + i * BOX, &mq, &full[s], 64 * i, hq, t, sg.b);
                     tma_load_4d(st + (SM::NB + i) * BOX, &mk, &full[s], 64 * i, hq, t, sg.b);
                 }
-                tma_load_4d(st + 2 * SM::NB * BOX, &mv, &full[s], 64 * tile, h, t, sg.b);
-                s_loaded = n + 1;
+                s_loaded = 2 * n + 1;
+                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) return false;
+                if (!lane_wait(&vempty[s], ph, &s_abort)) return false;
+                mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
+                bulk_load(&dec[n % ND], g.dec + (sg.c0 + n) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
+                mbar_expect_tx(&vfull[s], BOX);
+                tma_load_4d(st + 2 * SM::NB * BOX, &mv, &vfull[s], 64 * tile, h, t, sg.b);
+                s_loaded = 2 * n + 2;
                 return true;
             };
             bool ok = true;
@@ -796,8 +818,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             int scored = 0;
             auto scores = [&](int n, bool must) -> bool {
                 const int s = n % NST;
-                if (!must && (!mbar_try_wait(&full[s], (uint32_t)(n / NST) & 1u) ||
-                              (n == ragged && !mbar_try_wait(&tready, 0u))))
+                if (!must && (!done(&full[s], (uint32_t)(n / NST) & 1u) || (n == ragged && !done(&tready, 0u))))
                     return true;
                 if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
                 if (n == ragged && !lane_wait(&tready, 0u, &s_abort)) return false;
@@ -834,14 +855,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         umma_bf16(t_o1, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&sfree);
+                umma_commit(&empty[s]);
                 // the next chunk's scores go ahead of this one's last product
                 // when its rows have come, and never make it wait
                 if (n + 1 < nch) {
 #pragma unroll 1
-                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !mbar_try_wait(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
+                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !done(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
                         scores(n + 1, false);
                 }
-                ok = lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
+                     lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
@@ -849,7 +872,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 for (int k = 0; k < 8; ++k)
                     umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
                 umma_commit(&ofull);
-                umma_commit(&empty[s]);
+                umma_commit(&vempty[s]);
             }
             umma_commit(&fin);
         }
@@ -892,8 +915,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         for (int n = 0; n < nch; ++n) {
             const int s = n % NST, len = min(TCC, sg.len - n * TCC);
             uint8_t *st = smem + s * SM::STAGE;
-            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
             if (n == ragged) {
+                if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
                 if (t >= len)
                     for (int i = 0; i < 2 * SM::NB + 1; ++i) zero_row(st + i * BOX, t);
                 tma_store_fence();
@@ -1004,9 +1028,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     __syncthreads();
     if (threadIdx.x == 0) {
         if (s_abort)
-            for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
-                {
+            for (int n = max(0, (s_loaded + 1) / 2 - NST); 2 * n < s_loaded; ++n) {
                 (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
+                if (2 * n + 1 >= s_loaded) break;
+                (void)mbar_wait(&vfull[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
                 (void)mbar_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, TC_WAIT_NS);
             }
         (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
