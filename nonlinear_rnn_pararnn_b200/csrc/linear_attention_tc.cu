@@ -100,7 +100,7 @@ SLSTM_DEVINL void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2
 SLSTM_DEVINL uint8_t *aligned_smem(uint8_t *raw) { return raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u); }
 
 // Wait for a phase of an mbarrier: the hardware suspends the thread in each try
-// (for up to about the hinted time), and the tries are counted, which costs the
+// (for a time of its own), and the tries are counted, which costs the
 // waiting warps' neighbours less than reading a clock.  False after the last, or
 // once this block has given up.
 SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
@@ -112,11 +112,11 @@ SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
         asm volatile(
             "{\n"
             " .reg .pred p;\n"
-            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
             " selp.u32 %0, 1, 0, p;\n"
             "}\n"
             : "=r"(ok)
-            : "r"(addr), "r"(parity), "r"(20000u)
+            : "r"(addr), "r"(parity)
             : "memory");
         if (ok) return true;
         if (*(volatile int *)s_abort) return false;
