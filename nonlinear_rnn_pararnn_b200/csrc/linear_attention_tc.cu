@@ -281,6 +281,15 @@ SLSTM_DEVINL void split2(uint32_t x, uint32_t wh, uint32_t wl, uint32_t &hi, uin
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(x), "r"(wl), "r"(r));
 }
 
+// x w rounded once, but for the rounding of x wl.
+SLSTM_DEVINL uint32_t times2(uint32_t x, uint32_t wh, uint32_t wl)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(wl));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(wh), "r"(r));
+    return r;
+}
+
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
 // times w as two bf16 terms into the boxes at hi and lo; zero where !on.  The
 // loops over columns in these kernels are rolled up on purpose: the warps of a
@@ -677,16 +686,18 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 //   warps 0-7   the state (lane = row of d_k), its upper term into shared memory
 //   warps 8-11  v times its decays as two bf16 terms
 //   warps 12-19 the weights D (q k) from tensor memory and back as bf16
-//               (lane = query row, half of the keys each)
+//               (lane = query row, half of the keys each), and e^{c_i} q_i beside them
 //   warps 20-23 the outputs
-//   warp 24     loads (a ring of NST chunks) and the MMAs of k^T (w v)
-//   warp 25     the other MMAs
+//   warp 24     the MMAs of k^T (w v);  warp 25 the other MMAs
+//   warp 26     loads (a ring of NST chunks)
 // Each of these is a chain of latencies some 1500 cycles long; apart from one
 // another they run a chunk or two ahead or behind, and a chunk takes as long as
 // the longest of them, not as all.
-// A chunk's products: q k^T (128 x 128), then into one 64-column accumulator
-// each q S, D(q k) v (A from tensor memory) and k^T (w v).  The first of the
-// next chunk is issued before the last of this one where its rows have come.
+// A chunk's products: q k^T (128 x 128; of the next chunk ahead of the last of
+// this one where its rows have come), k^T (w v), and the outputs as one product
+// of [D (q k) | e^{c} q], in tensor memory, with [v ; S]: one accumulator, of
+// which there are two, so that a chunk's outputs are read while the next one's
+// are computed.  (e^{c_i} q_i is rounded to bf16 as the weights are.)
 // ---------------------------------------------------------------------------
 template <int DK>
 struct FwdShared {
@@ -700,7 +711,7 @@ struct FwdShared {
 };
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
-constexpr int FWD_THREADS = 832;
+constexpr int FWD_THREADS = 864;
 
 template <int DK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -713,7 +724,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull, oempty, tready, drained,
+    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull[2], oempty[2], tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
@@ -726,13 +737,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 2);
+            mbar_init(&empty[i], 9);
             mbar_init(&vfull[i], 1);
             mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 24);
+            mbar_init(&dempty[i], 20);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
         mbar_init(&yready, 4);
@@ -741,8 +752,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         mbar_init(&sfree, 1);
         mbar_init(&pready[0], 8);
         mbar_init(&pready[1], 8);
-        mbar_init(&ofull, 1);
-        mbar_init(&oempty, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ofull[i], 1);
+            mbar_init(&oempty[i], 4);
+        }
         mbar_init(&tready, 4);
         mbar_init(&drained, 8);
         mbar_init(&fin, 2);
@@ -755,14 +768,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const uint32_t t_o1 = tmem + 256, t_o2 = tmem + 320, t_delta = tmem + 384;   // scores: 0 and 128
+    const uint32_t t_o = tmem + 256, t_delta = tmem + 384;   // scores: 0 and 128; outputs: t_o and 64 on
     const int nch = sg.nch;
     // the last chunk of a packed sequence holds rows of the next one
     const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
 
-    if (warp == 24) {
+    if (warp == 26) {
         if (lane == 0) {
-            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             const int hq = h / (a.H / a.Hqk);
             // q and k come back into use before v does
             auto load = [&](int n) -> bool {
@@ -787,8 +799,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 s_loaded = 2 * n + 2;
                 return true;
             };
+            for (int n = 0; n < nch; ++n)
+                if (!load(n)) break;
+        }
+    } else if (warp == 24) {
+        if (lane == 0) {
+            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             bool ok = true;
-            for (int n = 0; n < min(NST, nch) && ok; ++n) ok = load(n);
             for (int n = 0; n < nch && ok; ++n) {
                 const int s = n % NST;
                 const uint32_t ph = (uint32_t)n & 1u;
@@ -806,7 +823,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
                 umma_commit(&delta);
                 umma_commit(&empty[s]);
-                if (n + NST < nch) ok = load(n + NST);
             }
             umma_commit(&fin);
         }
@@ -843,35 +859,31 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 const uint8_t *st = smem + s * SM::STAGE;
                 ok = scored > n || scores(n, true);
                 if (!ok) break;
-                ok = lane_wait(&sready, ph, &s_abort) && lane_wait(&oempty, ph ^ 1u, &s_abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
-#pragma unroll
-                for (int i = 0; i < SM::NB; ++i) {
-                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16(t_o1, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
-                }
-                umma_commit(&sfree);
-                umma_commit(&empty[s]);
-                // the next chunk's scores go ahead of this one's last product
-                // when its rows have come, and never make it wait
+                // the next chunk's scores go ahead of this one's outputs when its
+                // rows have come, and never make them wait
                 if (n + 1 < nch) {
 #pragma unroll 1
                     for (int i = 0; i < (1 << 20) && scored <= n + 1 && !done(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
                         scores(n + 1, false);
                 }
-                ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
+                ok = lane_wait(&sready, ph, &s_abort) &&
+                     lane_wait(&oempty[ph], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort) &&
+                     lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
                      lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
+                const uint32_t ta = tmem + ph * 128, td = t_o + ph * 64;
+#pragma unroll 1
+                for (int k = 0; k < DK / 16; ++k)
+                    umma_bf16_ta(td, ta + 32 + 64 * (k / (DK / 32)) + 8 * (k % (DK / 32)), sd + (2048u >> 4) * k, id_o,
+                                 k > 0 ? 1u : 0u);
+                umma_commit(&sfree);
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k)
-                    umma_bf16_ta(t_o2, tmem + (n & 1) * 128 + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
-                umma_commit(&ofull);
+                    umma_bf16_ta(td, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, 1u);
+                umma_commit(&ofull[ph]);
                 umma_commit(&vempty[s]);
             }
             umma_commit(&fin);
@@ -980,9 +992,32 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 tmem_st8(sc + 8 * z, p);
             }
+            // e^{c_i} q_i, this warp's half of the features, behind its weights
+            {
+                const float w = d.row[i];
+                const uint32_t wh = pack2(w, w);
+                const float rest = w - lo_of(wh);
+                const uint32_t wl = pack2(rest, rest);
+                const uint8_t *qb = smem + (n % NST) * SM::STAGE + (DK == 128 ? half * BOX : 0);
+#pragma unroll 1
+                for (int z = 0; z < DK / 32; ++z) {   // 16 features at a time
+                    uint32_t p[8];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(
+                            qb + swz(i, 2 * z + k + (DK == 128 ? 0 : 4 * half)));
+                        p[4 * k] = times2(x.x, wh, wl);
+                        p[4 * k + 1] = times2(x.y, wh, wl);
+                        p[4 * k + 2] = times2(x.z, wh, wl);
+                        p[4 * k + 3] = times2(x.w, wh, wl);
+                    }
+                    tmem_st8(sc + 32 + 8 * z, p);
+                }
+            }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&pready[n & 1]);
+            warp_arrive(&empty[n % NST]);
             warp_arrive(&dempty[n % ND]);
         }
     } else {
@@ -995,26 +1030,21 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = true;
         int n = 0;
         for (; n < nch; ++n) {
-            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
-            const float rowc = dec[n % ND].row[i] * a.scale;
-            warp_arrive(&dempty[n % ND]);
-            ok = ok && warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
+            ok = warp_wait(&ofull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
             const bool on = n * TCC + i < sg.len;
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
-                float u[16], w[16];
-                tmem_ld16x2(t_o1 + la + c, t_o2 + la + c, u, w);
+                float u[16];
+                tmem_ld16(t_o + (n & 1) * 64 + la + c, u);
                 if (c == 48) {
                     tc_fence_before();
-                    warp_arrive(&oempty);
+                    warp_arrive(&oempty[n & 1]);
                 }
                 uint32_t p[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
-                                 fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
+                for (int j = 0; j < 8; ++j) p[j] = pack2(a.scale * u[2 * j], a.scale * u[2 * j + 1]);
                 uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
                 if (on && c < cols) dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
                 if (on && c + 8 < cols) dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
