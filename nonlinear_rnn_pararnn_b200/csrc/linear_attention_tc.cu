@@ -73,6 +73,16 @@ SLSTM_DEVINL float ex2(float x)
     return y;
 }
 
+// One lane of the warp.  Chosen so, and not by its number, the compiler knows that
+// one thread runs what follows, and keeps the operands of MMAs and copies in
+// uniform registers without finding out lane by lane (186 -> 174 us a forward pass).
+SLSTM_DEVINL bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0u;
+}
+
 SLSTM_DEVINL uint32_t pack2(float a, float b)
 {
     const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
@@ -480,7 +490,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     auto rows = [&](int n) { return min(TCC, sg.len - chunk(n) * TCC); };
 
     if (warp == 16) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int hq = h / (a.H / a.Hqk);
             int n = 0;
             for (; n < nch; ++n) {
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             s_loaded = n;
         }
     } else if (warp == 17) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(128, 128, true, true);
             for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
 
     if (warp == 26) {
-        if (lane == 0) {
+        if (elect_one()) {
             const int hq = h / (a.H / a.Hqk);
             // q and k come back into use before v does
             auto load = [&](int n) -> bool {
@@ -803,7 +813,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (!load(n)) break;
         }
     } else if (warp == 24) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
             bool ok = true;
             for (int n = 0; n < nch && ok; ++n) {
@@ -827,7 +837,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             umma_commit(&fin);
         }
     } else if (warp == 25) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_qk = idesc_bf16(128, 128, false, false);
             constexpr uint32_t id_o = idesc_bf16(128, 64, false, true);
             // q k^T of chunk n; unless `must`, only if its rows are there
@@ -1210,7 +1220,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     const int rep = a.H / a.Hqk;
 
     if (warp == 16) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t SB = DK * 128;   // bytes of a box of a state: DK rows, 64 columns
             int it = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
@@ -1252,7 +1262,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             }
         }
     } else if (warp == 17) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_ss = idesc_bf16(128, 128, false, false);   // q k^T, dO v^T
             constexpr uint32_t id_si = idesc_bf16(128, DK, false, false);    // dO S^T, v dS^T
             constexpr uint32_t id_kd = idesc_bf16(128, DV, false, true);     // k dS, P^T dO
