@@ -8,6 +8,7 @@ runs in the library's CUDA kernels; nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -518,16 +519,51 @@ def newton_backward_head(x, Wx, P, R_head, s0, S, dH, *, forget="sigmoid", out: 
 # ---------------------------------------------------------------------------
 # linear attention with a decay for each head
 # ---------------------------------------------------------------------------
+class _On:
+    """The inputs' device made current for a call, where it is not already."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _stream_on(device) -> int:
+    """The device's current stream (what _stream() says, for a tenth of its time)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _need_on(t, name, shape, dtype, device):
+    """_need for a tensor that has to be on the inputs' device; None passes."""
+    if t is None or (t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous()):
+        return
+    _need(t, name, shape, dtype)
+    raise ValueError(f"{name} must be a CUDA tensor on {device}")
+
+
 def _need_tokens(t: torch.Tensor, name: str, lead, heads: int, d: int, dtype, device) -> int:
     """Checks a (*lead, heads, d) tensor whose tokens are contiguous and evenly
     spaced (a slice of a projection's output is); returns their spacing."""
-    if t.device != device or t.device.type != "cuda":
+    if t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
     shape = (*lead, heads, d)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.is_contiguous():
+        return heads * d
     st = t.stride()
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError(f"{name}: the heads and features of a token must be contiguous")
@@ -545,13 +581,25 @@ def _need_tokens(t: torch.Tensor, name: str, lead, heads: int, d: int, dtype, de
     return heads * d if ld is None else ld
 
 
-def _la_config(q, k, v, g, lead, scale):
-    """Checks q, k, v and g; returns the C ABI's config."""
+@functools.lru_cache(maxsize=4096)
+def _la_struct(*fields):
+    return _lib.LinearAttentionConfig(*fields)
+
+
+@functools.lru_cache(maxsize=4096)
+def _la_bytes(fields, B, T, packed, backward) -> int:
+    return int(load().slstm_linear_attention_workspace_size(ctypes.byref(_la_struct(*fields)), B, T, packed, backward))
+
+
+def _la_config(q, k, v, g, lead, scale) -> tuple:
+    """Checks q, k, v and g; returns the fields of the C ABI's config."""
     if v.dim() != len(lead) + 2 or q.dim() != len(lead) + 2:
         raise ValueError(f"q, k and v must have {len(lead) + 2} dimensions")
     Hqk, dk = q.shape[-2:]
     H, dv = v.shape[-2:]
     dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("q must be a CUDA tensor")
     if dt not in _DTYPE:
         raise ValueError(f"q, k and v must be float32 or bfloat16, got {dt}")
     if Hqk < 1 or H % Hqk:
@@ -561,29 +609,19 @@ def _la_config(q, k, v, g, lead, scale):
     ldq = _need_tokens(q, "q", lead, Hqk, dk, dt, dev)
     ldk = _need_tokens(k, "k", lead, Hqk, dk, dt, dev)
     ldv = _need_tokens(v, "v", lead, H, dv, dt, dev)
-    _need(g, "g", (H,) if g.dim() == 1 else (*lead, H))
-    if g.device != dev:
-        raise ValueError(f"g must be a CUDA tensor on {dev}")
-    decay = _lib.SLSTM_DECAY_HEAD if g.dim() == 1 else _lib.SLSTM_DECAY_TOKEN
-    return _lib.LinearAttentionConfig(H, Hqk, dk, dv, _DTYPE[dt], decay, dk ** -0.5 if scale is None else float(scale),
-                                      ldq, ldk, ldv)
+    per_head = g.dim() == 1
+    _need_on(g, "g", (H,) if per_head else (*lead, H), torch.float32, dev)
+    return (H, Hqk, dk, dv, _DTYPE[dt], _lib.SLSTM_DECAY_HEAD if per_head else _lib.SLSTM_DECAY_TOKEN,
+            dk ** -0.5 if scale is None else float(scale), ldq, ldk, ldv)
 
 
-def _need_on(t, name, shape, dtype, device):
-    """_need for a tensor that has to be on the inputs' device; None passes."""
-    if t is not None:
-        _need(t, name, shape, dtype)
-        if t.device != device:
-            raise ValueError(f"{name} must be a CUDA tensor on {device}")
-
-
-def _la_workspace(cfg, B, T, packed, backward, ws, device):
-    n = int(load().slstm_linear_attention_workspace_size(ctypes.byref(cfg), B, T, int(packed), int(backward)))
+def _la_workspace(fields, B, T, packed, backward, ws, device):
+    n = _la_bytes(fields, B, T, packed, backward)
     if n == 0:
         raise ValueError("unsupported sizes")
     if ws is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
-    if ws.device != device or ws.numel() * ws.element_size() < n:
+    if ws.device != device or ws.nbytes < n:
         raise ValueError(f"ws must hold {n} bytes on {device}")
     return ws
 
@@ -609,20 +647,22 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
         raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
     B, T = lead = tuple(q.shape[:2])
     cfg = _la_config(q, k, v, g, lead, scale)
-    H, dv, dev = cfg.H, cfg.d_v, q.device
-    state = (B, H, cfg.d_k, dv)
+    H, _, dk, dv = cfg[:4]
+    dev, state = q.device, (B, H, dk, dv)
     _need_on(s0, "s0", state, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if o is None:
             o = torch.empty(B, T, H, dv, dtype=q.dtype, device=dev)
+        else:
+            _need_on(o, "o", (B, T, H, dv), q.dtype, dev)
         if sT is None:
             sT = torch.empty(state, dtype=torch.float32, device=dev)
-        _need_on(o, "o", (B, T, H, dv), q.dtype, dev)
-        _need_on(sT, "sT", state, torch.float32, dev)
+        else:
+            _need_on(sT, "sT", state, torch.float32, dev)
         ws = _la_workspace(cfg, B, T, False, False, ws, dev)
         check("slstm_linear_attention_forward", load().slstm_linear_attention_forward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(o), _ptr(sT), ctypes.byref(cfg), B, T, _ptr(ws),
-            ws.numel() * ws.element_size(), _stream()))
+            _at(q), _at(k), _at(v), _at(g), _at(s0), _at(o), _at(sT), ctypes.byref(_la_struct(*cfg)), B, T, _at(ws),
+            ws.nbytes, _stream_on(dev)))
     return o, sT
 
 
@@ -634,6 +674,7 @@ def _la_grads(q, v, g, state, out, dev, with_dg):
                "ds0": torch.empty(state, dtype=torch.float32, device=dev)}
         if with_dg:
             out["dg"] = torch.empty(g.shape, dtype=torch.float32, device=dev)
+        return out
     for name, like, dt in (("dq", q.shape, q.dtype), ("dk", q.shape, q.dtype), ("dv", v.shape, v.dtype),
                            ("dg", g.shape, torch.float32), ("ds0", state, torch.float32)):
         if name in ("dq", "dk", "dv") and out.get(name) is None:
@@ -652,17 +693,17 @@ def linear_attention_backward(q, k, v, g, s0, dO, dsT=None, *, scale: float = No
         raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
     B, T = lead = tuple(q.shape[:2])
     cfg = _la_config(q, k, v, g, lead, scale)
-    dev, state = q.device, (B, cfg.H, cfg.d_k, cfg.d_v)
+    dev, state = q.device, (B, cfg[0], cfg[2], cfg[3])
     _need_on(s0, "s0", state, torch.float32, dev)
     _need_on(dO, "dO", v.shape, q.dtype, dev)
     _need_on(dsT, "dsT", state, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
         ws = _la_workspace(cfg, B, T, False, True, ws, dev)
         check("slstm_linear_attention_backward", load().slstm_linear_attention_backward(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(dO), _ptr(dsT), _ptr(out["dq"]), _ptr(out["dk"]),
-            _ptr(out["dv"]), _ptr(out.get("dg")), _ptr(out.get("ds0")), ctypes.byref(cfg), B, T, _ptr(ws),
-            ws.numel() * ws.element_size(), _stream()))
+            _at(q), _at(k), _at(v), _at(g), _at(s0), _at(dO), _at(dsT), _at(out["dq"]), _at(out["dk"]),
+            _at(out["dv"]), _at(out.get("dg")), _at(out.get("ds0")), ctypes.byref(_la_struct(*cfg)), B, T, _at(ws),
+            ws.nbytes, _stream_on(dev)))
     return out
 
 
@@ -676,22 +717,24 @@ def linear_attention_forward_varlen(q, k, v, g, s0, cu_seqlens, *, scale: float 
     lead = tuple(q.shape[:1])
     n_seq = cu_seqlens.numel() - 1
     cfg = _la_config(q, k, v, g, lead, scale)
-    H, dv, dev = cfg.H, cfg.d_v, q.device
-    state = (n_seq, H, cfg.d_k, dv)
+    H, _, dk, dv = cfg[:4]
+    dev, state = q.device, (n_seq, H, dk, dv)
     _need_cu(cu_seqlens, n_seq)
     _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
     _need_on(s0, "s0", state, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if o is None:
             o = torch.empty(lead[0], H, dv, dtype=q.dtype, device=dev)
+        else:
+            _need_on(o, "o", (lead[0], H, dv), q.dtype, dev)
         if sT is None:
             sT = torch.empty(state, dtype=torch.float32, device=dev)
-        _need_on(o, "o", (lead[0], H, dv), q.dtype, dev)
-        _need_on(sT, "sT", state, torch.float32, dev)
+        else:
+            _need_on(sT, "sT", state, torch.float32, dev)
         ws = _la_workspace(cfg, n_seq, lead[0], True, False, ws, dev)
         check("slstm_linear_attention_forward_varlen", load().slstm_linear_attention_forward_varlen(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(cu_seqlens), n_seq, _ptr(o), _ptr(sT),
-            ctypes.byref(cfg), lead[0], _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+            _at(q), _at(k), _at(v), _at(g), _at(s0), _at(cu_seqlens), n_seq, _at(o), _at(sT),
+            ctypes.byref(_la_struct(*cfg)), lead[0], _at(ws), ws.nbytes, _stream_on(dev)))
     return o, sT
 
 
@@ -704,19 +747,19 @@ def linear_attention_backward_varlen(q, k, v, g, s0, cu_seqlens, dO, dsT=None, *
     lead = tuple(q.shape[:1])
     n_seq = cu_seqlens.numel() - 1
     cfg = _la_config(q, k, v, g, lead, scale)
-    dev, state = q.device, (n_seq, cfg.H, cfg.d_k, cfg.d_v)
+    dev, state = q.device, (n_seq, cfg[0], cfg[2], cfg[3])
     _need_cu(cu_seqlens, n_seq)
     _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
     _need_on(s0, "s0", state, torch.float32, dev)
     _need_on(dO, "dO", v.shape, q.dtype, dev)
     _need_on(dsT, "dsT", state, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
         ws = _la_workspace(cfg, n_seq, lead[0], True, True, ws, dev)
         check("slstm_linear_attention_backward_varlen", load().slstm_linear_attention_backward_varlen(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0), _ptr(cu_seqlens), n_seq, _ptr(dO), _ptr(dsT),
-            _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]), _ptr(out.get("dg")), _ptr(out.get("ds0")),
-            ctypes.byref(cfg), lead[0], _ptr(ws), ws.numel() * ws.element_size(), _stream()))
+            _at(q), _at(k), _at(v), _at(g), _at(s0), _at(cu_seqlens), n_seq, _at(dO), _at(dsT),
+            _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), _at(out.get("dg")), _at(out.get("ds0")),
+            ctypes.byref(_la_struct(*cfg)), lead[0], _at(ws), ws.nbytes, _stream_on(dev)))
     return out
 
 
@@ -729,24 +772,32 @@ def linear_attention_step(q, k, v, g, s_prev=None, *, scale: float = None, o: to
         raise ValueError(f"q must be (B, H_qk, d_k), got {tuple(q.shape)}")
     lead = tuple(q.shape[:1])
     cfg = _la_config(q, k, v, g, lead, scale)
+    H, _, dk, dv = cfg[:4]
     B, dev = lead[0], q.device
-    state = (B, cfg.H, cfg.d_k, cfg.d_v)
+    state = (B, H, dk, dv)
     _need_on(s_prev, "s_prev", state, torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if o is None:
-            o = torch.empty(B, cfg.H, cfg.d_v, dtype=q.dtype, device=dev)
+            o = torch.empty(B, H, dv, dtype=q.dtype, device=dev)
+        else:
+            _need_on(o, "o", (B, H, dv), q.dtype, dev)
         if out is None:
             out = torch.empty(state, dtype=torch.float32, device=dev)
-        _need_on(o, "o", (B, cfg.H, cfg.d_v), q.dtype, dev)
-        _need_on(out, "out", state, torch.float32, dev)
+        else:
+            _need_on(out, "out", state, torch.float32, dev)
         check("slstm_linear_attention_step", load().slstm_linear_attention_step(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s_prev), _ptr(out), _ptr(o), ctypes.byref(cfg), B, _stream()))
+            _at(q), _at(k), _at(v), _at(g), _at(s_prev), _at(out), _at(o), ctypes.byref(_la_struct(*cfg)), B, _stream_on(dev)))
     return o, out
 
 
 # ---------------------------------------------------------------------------
 # layer norm
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=4096)
+def _ln_bytes(rows, groups, d) -> int:
+    return int(load().slstm_layer_norm_workspace_size(rows, groups, d))
+
+
 def _ln_dims(x, groups):
     if x.device.type != "cuda" or not x.is_contiguous() or x.dim() < 1 or x.dtype not in _DTYPE:
         raise ValueError("x must be a contiguous float32 or bfloat16 CUDA tensor")
@@ -772,15 +823,16 @@ def layer_norm_forward(x, w, b=None, *, groups: int = 1, eps: float = 1e-5, y_dt
         raise ValueError(f"y must be float32 or bfloat16, got {y_dtype}")
     _need_on(w, "w", (D,), torch.float32, dev)
     _need_on(b, "b", (D,), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if y is None:
             y = torch.empty(x.shape, dtype=y_dtype, device=dev)
-        _need_on(y, "y", x.shape, y_dtype, dev)
+        else:
+            _need_on(y, "y", x.shape, y_dtype, dev)
         stats = torch.empty(2, *x.shape[:-1], groups, dtype=torch.float32, device=dev)
-        mean, rstd = stats[0], stats[1]
+        mean, rstd = stats.unbind()
         check("slstm_layer_norm_forward", load().slstm_layer_norm_forward(
-            _ptr(x), _DTYPE[x.dtype], _ptr(w), _ptr(b), _ptr(y), _DTYPE[y_dtype], _ptr(mean), _ptr(rstd), rows, groups,
-            D // groups, float(eps), _stream()))
+            _at(x), _DTYPE[x.dtype], _at(w), _at(b), _at(y), _DTYPE[y_dtype], _at(mean), _at(rstd), rows, groups,
+            D // groups, float(eps), _stream_on(dev)))
     return y, mean, rstd
 
 
@@ -795,22 +847,24 @@ def layer_norm_backward(x, w, dy, mean, rstd, *, groups: int = 1, out: dict = No
     _need_on(dy, "dy", x.shape, dy.dtype, dev)
     _need_on(mean, "mean", (*x.shape[:-1], groups), torch.float32, dev)
     _need_on(rstd, "rstd", (*x.shape[:-1], groups), torch.float32, dev)
-    with torch.cuda.device(dev):
+    with _On(dev):
         if out is None:
             dwb = torch.empty(2, D, dtype=torch.float32, device=dev)
-            out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dw": dwb[0], "db": dwb[1]}
-        _need_on(out["dx"], "dx", x.shape, x.dtype, dev)
-        _need_on(out["dw"], "dw", (D,), torch.float32, dev)
-        _need_on(out["db"], "db", (D,), torch.float32, dev)
-        n = int(load().slstm_layer_norm_workspace_size(rows, groups, D // groups))
+            dw, db = dwb.unbind()
+            out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=dev), "dw": dw, "db": db}
+        else:
+            _need_on(out["dx"], "dx", x.shape, x.dtype, dev)
+            _need_on(out["dw"], "dw", (D,), torch.float32, dev)
+            _need_on(out["db"], "db", (D,), torch.float32, dev)
+        n = _ln_bytes(rows, groups, D // groups)
         if n == 0:
             raise ValueError("unsupported sizes")
         if ws is None:
             ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        if ws.device != dev or ws.numel() * ws.element_size() < n:
+        elif ws.device != dev or ws.nbytes < n:
             raise ValueError(f"ws must hold {n} bytes on {dev}")
         check("slstm_layer_norm_backward", load().slstm_layer_norm_backward(
-            _ptr(x), _DTYPE[x.dtype], _ptr(w), _ptr(dy), _DTYPE[dy.dtype], _ptr(mean), _ptr(rstd), _ptr(out["dx"]),
-            _ptr(out["dw"]), _ptr(out["db"]), rows, groups, D // groups, _ptr(ws), ws.numel() * ws.element_size(),
-            _stream()))
+            _at(x), _DTYPE[x.dtype], _at(w), _at(dy), _DTYPE[dy.dtype], _at(mean), _at(rstd), _at(out["dx"]),
+            _at(out["dw"]), _at(out["db"]), rows, groups, D // groups, _at(ws), ws.nbytes,
+            _stream_on(dev)))
     return out
