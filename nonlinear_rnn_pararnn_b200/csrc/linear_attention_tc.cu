@@ -104,6 +104,14 @@ SLSTM_DEVINL void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2
                  : "memory");
 }
 
+SLSTM_DEVINL void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // The first 1024-byte boundary in dynamic shared memory, by an offset: a pointer
 // that goes through an integer is no longer known to be shared memory, and every
 // access through it becomes a generic one (564 us where this takes 170 us).
@@ -1284,6 +1292,28 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     tma_load_3d(x1 + i * SB, &mdl, &fullD, 64 * i, 0, item);
                 }
                 s_loaded = 3 * it + 3;
+                // the next item's rows and states into the L2 cache while this one is
+                // computed: a block has room for one item
+                const int next = item + gridDim.x;
+                if (next < items) {
+                    const int h2 = next % a.H, hq2 = h2 / rep;
+                    const LaChunk c2 = la_chunk(g.ch, next / a.H);
+                    const int t2 = packed ? (int)c2.row : c2.n * TCC, b2 = packed ? 0 : c2.seq;
+#pragma unroll
+                    for (int i = 0; i < NK; ++i) {
+                        tma_prefetch_4d(&mq, 64 * i, hq2, t2, b2);
+                        tma_prefetch_4d(&mk, 64 * i, hq2, t2, b2);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        tma_prefetch_4d(&mv, 64 * i, h2, t2, b2);
+                        tma_prefetch_4d(&mg, 64 * i, h2, t2, b2);
+                        tma_prefetch_3d(&msh, 64 * i, 0, next);
+                        tma_prefetch_3d(&msl, 64 * i, 0, next);
+                        tma_prefetch_3d(&mdh, 64 * i, 0, next);
+                        tma_prefetch_3d(&mdl, 64 * i, 0, next);
+                    }
+                }
             }
         }
     } else if (warp == 17) {
