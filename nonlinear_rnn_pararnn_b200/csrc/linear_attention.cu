@@ -20,8 +20,9 @@
 // chunk: the sum of q . dq - k . dk over all later rows is the same number, but
 // cancels over the whole row and keeps little of it.
 //
-// All products are fp32 fused multiply-adds over 64 x 64 tiles (8 x 4 for each
-// of 128 threads); fp32 in, fp32 out needs that, and sizes that are no multiple
+// All products are fp32 fused multiply-adds over 64 x 64 tiles (RT x 4 for each
+// of 1024 / RT threads), the next 32 of the depth on their way from memory
+// meanwhile; fp32 in, fp32 out needs that, and sizes that are no multiple
 // of 8 come here too.  Bound: the FMA pipes.
 #include <cuda_bf16.h>
 
@@ -36,7 +37,14 @@ namespace {
 constexpr int LC = 64;        // rows of a chunk
 constexpr int KB = 32;        // depth of the tiles in shared memory
 constexpr int LDT = 68;       // padded row of a tile (floats)
-constexpr int NT = 128;
+// Rows of a thread's tile.  8: 128 threads, the fewest reads of shared memory for
+// a multiply-add, where the blocks fill the GPU; 4: 256 threads, twice the warps
+// to hide the latencies behind, where they do not (2 x 777 rows, 4 heads of 64:
+// 25 and 40 us; 8 x 1024 rows, both passes: 205 and 150).
+template <int RT>
+constexpr int nt() { return 1024 / RT; }
+template <int RT>
+constexpr int nf() { return 64 * KB / nt<RT>(); }   // elements of a tile that a thread fetches
 
 SLSTM_DEVINL float to_f(float v) { return v; }
 SLSTM_DEVINL float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -53,65 +61,95 @@ struct Op {
     const float *coef;
 };
 
-template <typename T>
-SLSTM_DEVINL void load_tile(float *dst, const Op<T> &a, int k0)
-{
-    const int t = threadIdx.x;
-    if (a.sk == 1) {   // k is contiguous
-#pragma unroll 4
-        for (int i = t; i < 64 * KB; i += NT) {
-            const int m = i / KB, k = i % KB;
-            float v = 0.0f;
-            if (m < a.nm && k0 + k < a.nk) {
-                v = to_f(a.p[m * a.sm + (k0 + k)]);
-                if (a.coef) v *= a.coef[k0 + k];
+// Thread t's elements of the 64 x KB tiles of an operand, in the order in which
+// they are contiguous in memory, and where they go in shared memory.
+template <typename T, int RT>
+struct Feed {
+    const T *p;           // the first element at depth 0
+    long long step;       // to the next
+    int m, k, dm, dk;     // its place, and the next one's
+    SLSTM_DEVINL explicit Feed(const Op<T> &a)
+    {
+        const int t = threadIdx.x;
+        const bool kc = a.sk == 1;
+        m = kc ? t / KB : t % 64;
+        k = kc ? t % KB : t / 64;
+        dm = kc ? nt<RT>() / KB : 0;
+        dk = kc ? 0 : nt<RT>() / 64;
+        p = a.p + m * a.sm + k * a.sk;
+        step = dm * a.sm + dk * a.sk;
+    }
+    SLSTM_DEVINL void fetch(float (&v)[nf<RT>()], const Op<T> &a, int k0) const
+    {
+        const T *q = p + k0 * a.sk;
+#pragma unroll
+        for (int i = 0; i < nf<RT>(); ++i) {
+            const int kk = k0 + k + i * dk;
+            v[i] = 0.0f;
+            if (m + i * dm < a.nm && kk < a.nk) {
+                v[i] = to_f(q[i * step]);
+                if (a.coef) v[i] *= a.coef[kk];
             }
-            dst[k * LDT + m] = v;
-        }
-    } else {
-#pragma unroll 4
-        for (int i = t; i < 64 * KB; i += NT) {
-            const int m = i % 64, k = i / 64;
-            float v = 0.0f;
-            if (m < a.nm && k0 + k < a.nk) {
-                v = to_f(a.p[m * a.sm + (k0 + k) * a.sk]);
-                if (a.coef) v *= a.coef[k0 + k];
-            }
-            dst[k * LDT + m] = v;
         }
     }
-}
+    SLSTM_DEVINL void stow(float *dst, const float (&v)[nf<RT>()]) const
+    {
+#pragma unroll
+        for (int i = 0; i < nf<RT>(); ++i) dst[(k + i * dk) * LDT + m + i * dm] = v[i];
+    }
+};
 
 // acc += A B^T over k < K: thread (ty, tx) = (t / 16, t % 16) holds rows
-// 8 ty .. and columns 4 tx ...
-template <typename TA, typename TB>
-SLSTM_DEVINL void product(float (&acc)[8][4], const Op<TA> &A, const Op<TB> &B, int K, float *sA, float *sB)
+// RT ty .. and columns 4 tx ...
+template <int RT, typename TA, typename TB>
+SLSTM_DEVINL void product(float (&acc)[RT][4], const Op<TA> &A, const Op<TB> &B, int K, float *sA, float *sB)
 {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    float va[nf<RT>()], vb[nf<RT>()];
+    const Feed<TA, RT> fa(A);
+    const Feed<TB, RT> fb(B);
+    // what an operand in shared memory was written by is behind this barrier
+    __syncthreads();
+    fa.fetch(va, A, 0);
+    fb.fetch(vb, B, 0);
     for (int k0 = 0; k0 < K; k0 += KB) {
+        if (k0 > 0) __syncthreads();
+        fa.stow(sA, va);
+        fb.stow(sB, vb);
         __syncthreads();
-        load_tile(sA, A, k0);
-        load_tile(sB, B, k0);
-        __syncthreads();
+        if (k0 + KB < K) {
+            fa.fetch(va, A, k0 + KB);
+            fb.fetch(vb, B, k0 + KB);
+        }
 #pragma unroll 8
         for (int k = 0; k < KB; ++k) {
-            const float4 a0 = *reinterpret_cast<const float4 *>(sA + k * LDT + ty * 8);
-            const float4 a1 = *reinterpret_cast<const float4 *>(sA + k * LDT + ty * 8 + 4);
-            const float4 b = *reinterpret_cast<const float4 *>(sB + k * LDT + tx * 4);
-            const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            const float bv[4] = {b.x, b.y, b.z, b.w};
+            float av[RT], bv[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < RT; i += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(sA + k * LDT + ty * RT + i);
+                av[i] = a.x;
+                av[i + 1] = a.y;
+                av[i + 2] = a.z;
+                av[i + 3] = a.w;
+            }
+            const float4 b = *reinterpret_cast<const float4 *>(sB + k * LDT + tx * 4);
+            bv[0] = b.x;
+            bv[1] = b.y;
+            bv[2] = b.z;
+            bv[3] = b.w;
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
         }
     }
 }
 
-SLSTM_DEVINL void clear(float (&acc)[8][4])
+template <int RT>
+SLSTM_DEVINL void clear(float (&acc)[RT][4])
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
 }
@@ -140,8 +178,8 @@ SLSTM_DEVINL float decay_ij(const Decays &d, int i, int j, int len)
 // What a chunk adds to the state: out[c][h] (d_k x d_v) = sum_j w_j X_j Y_j^T,
 // with X = k, Y = v, w = e^{c_C - c_j} forward, or X = q, Y = dO,
 // w = scale e^{c_i} from the end.
-template <typename T>
-__global__ void __launch_bounds__(NT) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
+template <typename T, int RT>
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 6 : 3) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ Decays d;
@@ -157,16 +195,16 @@ __global__ void __launch_bounds__(NT) la_delta_kernel(LaArgs a, LaChunks ch, boo
     const long long ldx = back ? a.ldq : a.ldk, ldy = back ? (long long)a.H * a.dv : a.ldv;
     const T *X = static_cast<const T *>(back ? a.q : a.k) + ck.row * ldx + (long long)hq * a.dk + m0;
     const T *Y = static_cast<const T *>(back ? a.dO : a.v) + ck.row * ldy + (long long)h * a.dv + n0;
-    float acc[8][4];
+    float acc[RT][4];
     clear(acc);
     product(acc, Op<T>{X, 1, ldx, a.dk - m0, ck.len, w}, Op<T>{Y, 1, ldy, a.dv - n0, ck.len, nullptr}, ck.len, sA, sB);
     float *dst = out + ((long long)c * a.H + h) * a.dk * a.dv;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty * 8 + i, n = n0 + tx * 4 + j;
+            const int m = m0 + ty * RT + i, n = n0 + tx * 4 + j;
             if (m < a.dk && n < a.dv) dst[(long long)m * a.dv + n] = acc[i][j];
         }
 }
@@ -231,8 +269,8 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
 }
 
 // The outputs of a chunk and head.
-template <typename T>
-__global__ void __launch_bounds__(NT) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
+template <typename T, int RT>
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 6 : 3) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ float P[LC][LC + 1];
@@ -248,14 +286,14 @@ __global__ void __launch_bounds__(NT) la_out_kernel(LaArgs a, LaChunks ch, const
     const T *v = static_cast<const T *>(a.v) + ck.row * a.ldv + (long long)h * a.dv;
     const float *S = states + ((long long)c * a.H + h) * a.dk * a.dv;
     T *o = static_cast<T *>(a.o) + ck.row * (long long)a.H * a.dv + (long long)h * a.dv;
-    float acc[8][4];
+    float acc[RT][4];
     clear(acc);
     product(acc, Op<T>{q, a.ldq, 1, ck.len, a.dk, nullptr}, Op<T>{k, a.ldk, 1, ck.len, a.dk, nullptr}, a.dk, sA, sB);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = ty * 8 + i, s = tx * 4 + j;
+            const int r = ty * RT + i, s = tx * 4 + j;
             const float w = decay_ij(d, r, s, ck.len);
             P[r][s] = w == 0.0f ? 0.0f : acc[i][j] * w;
         }
@@ -264,18 +302,18 @@ __global__ void __launch_bounds__(NT) la_out_kernel(LaArgs a, LaChunks ch, const
         product(acc, Op<T>{q, a.ldq, 1, ck.len, a.dk, nullptr}, Op<float>{S + n0, 1, a.dv, a.dv - n0, a.dk, nullptr},
                 a.dk, sA, sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float r = d.row[ty * 8 + i];
+        for (int i = 0; i < RT; ++i) {
+            const float r = d.row[ty * RT + i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] *= r;
         }
         product(acc, Op<float>{&P[0][0], LC + 1, 1, LC, ck.len, nullptr},
                 Op<T>{v + n0, 1, a.ldv, a.dv - n0, ck.len, nullptr}, ck.len, sA, sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                const int r = ty * RT + i, n = n0 + tx * 4 + j;
                 if (r < ck.len && n < a.dv) put(o + (long long)r * a.H * a.dv + n, acc[i][j] * a.scale);
             }
     }
@@ -293,16 +331,16 @@ struct BackShared {
     float sA[KB * LDT], sB[KB * LDT];
     float P[LC][LC + 1], Pd[LC][LC + 1];
     float r[LC], u[LC], w[LC];
-    float cs[8][LC];      // column sums of W of each thread row
-    float red[NT / 32];
+    float cs[16][LC];     // column sums of W of each thread row
+    float red[8];
     Decays d;
 };
 
 // The gradients of a chunk and head.  part_q, part_k: [row][h][d_k] fp32 where
 // heads share a query and key head; dgc: the chunk's sum of dg, [c][h], where
 // the decay belongs to the head.
-template <typename T>
-__global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states,
+template <typename T, int RT>
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2) la_back_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states,
                                                      const float *__restrict__ dstates, float *part_q, float *part_k,
                                                      float *dgc)
 {
@@ -322,21 +360,21 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
     const T *g = static_cast<const T *>(a.dO) + ck.row * ldo + (long long)h * a.dv;
     const float *S = states + ((long long)c * a.H + h) * a.dk * a.dv;
     const float *dS = dstates + ((long long)c * a.H + h) * a.dk * a.dv;
-    for (int i = threadIdx.x; i < LC; i += NT) s.u[i] = s.w[i] = 0.0f;
+    for (int i = threadIdx.x; i < LC; i += nt<RT>()) s.u[i] = s.w[i] = 0.0f;
 
     // D (q k) and scale D (dO v), their products' sums over rows and columns
-    float p[8][4], t[8][4];
+    float p[RT][4], t[RT][4];
     clear(p);
     clear(t);
     product(p, Op<T>{q, a.ldq, 1, len, a.dk, nullptr}, Op<T>{k, a.ldk, 1, len, a.dk, nullptr}, a.dk, s.sA, s.sB);
     product(t, Op<T>{g, ldo, 1, len, a.dv, nullptr}, Op<T>{v, a.ldv, 1, len, a.dv, nullptr}, a.dv, s.sA, s.sB);
     float cs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RT; ++i) {
         float rs = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int r = ty * 8 + i, m = tx * 4 + j;
+            const int r = ty * RT + i, m = tx * 4 + j;
             const float w = a.scale * decay_ij(s.d, r, m, len);
             const float P = w == 0.0f ? 0.0f : w * p[i][j], Pd = w == 0.0f ? 0.0f : w * t[i][j];
             s.P[r][m] = P;
@@ -346,7 +384,7 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
             cs[j] += W;
         }
         rs = sum16(rs);
-        if (tx == 0) s.r[ty * 8 + i] = rs;
+        if (tx == 0) s.r[ty * RT + i] = rs;
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) s.cs[ty][tx * 4 + j] = cs[j];
@@ -356,8 +394,8 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
         product(p, Op<T>{g, ldo, 1, len, a.dv, nullptr},
                 Op<float>{S + (long long)n0 * a.dv, a.dv, 1, a.dk - n0, a.dv, nullptr}, a.dv, s.sA, s.sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = ty * 8 + i;
+        for (int i = 0; i < RT; ++i) {
+            const int r = ty * RT + i;
             const float f = a.scale * s.d.row[r];
             float u = 0.0f;
 #pragma unroll
@@ -375,8 +413,8 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
         product(t, Op<T>{v, a.ldv, 1, len, a.dv, nullptr},
                 Op<float>{dS + (long long)n0 * a.dv, a.dv, 1, a.dk - n0, a.dv, nullptr}, a.dv, s.sA, s.sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = ty * 8 + i;
+        for (int i = 0; i < RT; ++i) {
+            const int r = ty * RT + i;
             const float f = s.d.col[r];
             float w = 0.0f;
 #pragma unroll
@@ -391,10 +429,10 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
         product(t, Op<float>{&s.Pd[0][0], 1, LC + 1, LC, len, nullptr},
                 Op<T>{q + n0, 1, a.ldq, a.dk - n0, len, nullptr}, len, s.sA, s.sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                const int r = ty * RT + i, n = n0 + tx * 4 + j;
                 if (r >= len || n >= a.dk) continue;
                 if (part_q) {
                     const long long at = ((ck.row + r) * a.H + h) * a.dk + n;
@@ -412,18 +450,18 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
         product(t, Op<T>{k, a.ldk, 1, len, a.dk, nullptr}, Op<float>{dS + n0, 1, a.dv, a.dv - n0, a.dk, nullptr}, a.dk,
                 s.sA, s.sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float f = s.d.col[ty * 8 + i];
+        for (int i = 0; i < RT; ++i) {
+            const float f = s.d.col[ty * RT + i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) t[i][j] *= f;
         }
         product(t, Op<float>{&s.P[0][0], 1, LC + 1, LC, len, nullptr},
                 Op<T>{g + n0, 1, ldo, a.dv - n0, len, nullptr}, len, s.sA, s.sB);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int r = ty * 8 + i, n = n0 + tx * 4 + j;
+                const int r = ty * RT + i, n = n0 + tx * 4 + j;
                 if (r < len && n < a.dv)
                     put(static_cast<T *>(a.dv_) + (ck.row + r) * ldo + (long long)h * a.dv + n, t[i][j]);
             }
@@ -431,21 +469,23 @@ __global__ void __launch_bounds__(NT) la_back_kernel(LaArgs a, LaChunks ch, cons
     if (a.dg == nullptr) return;
     // <S_n, dS_{n+1}>, then dg by one warp
     float dot = 0.0f;
-    for (int i = threadIdx.x; i < a.dk * a.dv; i += NT) dot = fmaf(S[i], dS[i], dot);
+    for (int i = threadIdx.x; i < a.dk * a.dv; i += nt<RT>()) dot = fmaf(S[i], dS[i], dot);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = dot;
     __syncthreads();
     if (threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
-    dot = (s.red[0] + s.red[1] + s.red[2] + s.red[3]) * s.d.tot;
+    dot = 0.0f;
+    for (int i = 0; i < nt<RT>() / 32; ++i) dot += s.red[i];
+    dot *= s.d.tot;
     // two rows a lane; sums of up to 64 terms, in 64 bits: they cancel
     double x[2], w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = lane * 2 + i;
         double col = 0.0;
-        for (int y = 0; y < 8; ++y) col += s.cs[y][r];
+        for (int y = 0; y < 64 / RT; ++y) col += s.cs[y][r];
         x[i] = (double)s.r[r] + s.u[r] - col;
         w[i] = s.w[r];
     }
@@ -643,48 +683,46 @@ SimtWs simt_layout(const LaArgs &a, bool backward, void *ws)
     return w;
 }
 
-template <typename T>
+template <typename T, int RT>
 cudaError_t states(const LaArgs &a, const LaChunks &ch, bool back, float *buf, float *tot, cudaStream_t st)
 {
     const int E = a.dk * a.dv;
     const dim3 grid((unsigned)ch.total * a.H, (a.dk + 63) / 64, (a.dv + 63) / 64);
-    la_delta_kernel<T><<<grid, NT, 0, st>>>(a, ch, back, buf, tot);
+    la_delta_kernel<T, RT><<<grid, nt<RT>(), 0, st>>>(a, ch, back, buf, tot);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return la_scan(ch, a.H, E, back, buf, tot, back ? a.dsT : a.s0, back ? a.ds0 : a.sT, st);
 }
 
-template <typename T>
-cudaError_t forward(const LaArgs &a, void *ws, cudaStream_t st)
+template <typename T, int RT>
+cudaError_t forward(const LaArgs &a, const LaChunks &ch, const SimtWs &w, cudaStream_t st)
 {
-    const SimtWs w = simt_layout(a, false, ws);
-    LaChunks ch;
-    cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
-    if (e == cudaSuccess) e = states<T>(a, ch, false, w.S, w.totS, st);
+    cudaError_t e = states<T, RT>(a, ch, false, w.S, w.totS, st);
     if (e != cudaSuccess) return e;
-    la_out_kernel<T><<<(unsigned)ch.total * a.H, NT, 0, st>>>(a, ch, w.S);
+    la_out_kernel<T, RT><<<(unsigned)ch.total * a.H, nt<RT>(), 0, st>>>(a, ch, w.S);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t backward(const LaArgs &a, void *ws, cudaStream_t st)
+template <typename T, int RT>
+cudaError_t backward(const LaArgs &a, const LaChunks &ch, const SimtWs &w, cudaStream_t st)
 {
-    const SimtWs w = simt_layout(a, true, ws);
-    LaChunks ch;
-    cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
-    if (e == cudaSuccess) e = states<T>(a, ch, false, w.S, w.totS, st);
-    if (e == cudaSuccess) e = states<T>(a, ch, true, w.dS, w.totD, st);
+    cudaError_t e = states<T, RT>(a, ch, false, w.S, w.totS, st);
+    if (e == cudaSuccess) e = states<T, RT>(a, ch, true, w.dS, w.totD, st);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(la_back_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(la_back_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)sizeof(BackShared));
     if (e != cudaSuccess) return e;
-    la_back_kernel<T><<<(unsigned)ch.total * a.H, NT, sizeof(BackShared), st>>>(a, ch, w.S, w.dS, w.pq, w.pk, w.dgc);
+    la_back_kernel<T, RT><<<(unsigned)ch.total * a.H, nt<RT>(), sizeof(BackShared), st>>>(a, ch, w.S, w.dS, w.pq, w.pk,
+                                                                                       w.dgc);
     e = cudaGetLastError();
     if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, a.dq, a.dtype, ch, a, st);
     if (e == cudaSuccess && w.pq) e = la_share_sum(w.pk, a.dk_, a.dtype, ch, a, st);
     if (e == cudaSuccess && a.dg && a.per_head) e = la_head_sum(w.dgc, a.dg, ch, a.H, st);
     return e;
 }
+
+// Whether the blocks of a pass leave the SMs fewer than two each.
+bool few(const LaArgs &a, const LaChunks &ch) { return (long long)ch.total * a.H < 2 * 148; }
 
 }  // namespace
 
@@ -695,12 +733,24 @@ size_t la_simt_workspace(const LaArgs &a, bool backward)
 
 cudaError_t la_simt_forward(const LaArgs &a, void *ws, cudaStream_t st)
 {
-    return a.dtype == SLSTM_F32 ? forward<float>(a, ws, st) : forward<__nv_bfloat16>(a, ws, st);
+    const SimtWs w = simt_layout(a, false, ws);
+    LaChunks ch;
+    const cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
+    if (e != cudaSuccess) return e;
+    typedef __nv_bfloat16 bf16;
+    if (a.dtype == SLSTM_F32) return few(a, ch) ? forward<float, 4>(a, ch, w, st) : forward<float, 8>(a, ch, w, st);
+    return few(a, ch) ? forward<bf16, 4>(a, ch, w, st) : forward<bf16, 8>(a, ch, w, st);
 }
 
 cudaError_t la_simt_backward(const LaArgs &a, void *ws, cudaStream_t st)
 {
-    return a.dtype == SLSTM_F32 ? backward<float>(a, ws, st) : backward<__nv_bfloat16>(a, ws, st);
+    const SimtWs w = simt_layout(a, true, ws);
+    LaChunks ch;
+    const cudaError_t e = la_chunks(a, LC, w.table, &ch, st);
+    if (e != cudaSuccess) return e;
+    typedef __nv_bfloat16 bf16;
+    if (a.dtype == SLSTM_F32) return few(a, ch) ? backward<float, 4>(a, ch, w, st) : backward<float, 8>(a, ch, w, st);
+    return few(a, ch) ? backward<bf16, 4>(a, ch, w, st) : backward<bf16, 8>(a, ch, w, st);
 }
 
 // ---------------------------------------------------------------------------
