@@ -702,7 +702,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // columns of v and does all of it while q, k and v are in shared memory, the
 // state in registers:
 //   warps 0-7   the state (lane = row of d_k), its upper term into shared memory
-//   warps 8-11  v times its decays as two bf16 terms
+//               and half of v times its decays as two bf16 terms
+//   warps 8-11  the other half
 //   warps 12-19 the weights D (q k) from tensor memory and back as bf16
 //               (lane = query row, half of the keys each), and e^{c_i} q_i beside them
 //   warps 20-23 the outputs
@@ -764,7 +765,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             mbar_init(&dempty[i], 20);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
-        mbar_init(&yready, 4);
+        mbar_init(&yready, 12);
         mbar_init(&delta, 1);
         mbar_init(&sready, 8);
         mbar_init(&sfree, 1);
@@ -915,8 +916,20 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                                          : nullptr);
         float S[SH::N];
         state_load(S, src, a.dk, a.dv, r, col);
-        bool ok = true;
-        for (int n = 0; n < nch; ++n) {
+        // the other half of v's columns: w v is what the next chunk's product waits for
+        auto scale = [&](int n) -> bool {
+            const int s = n % NST, t = (warp & 3) * 32 + lane, p = 4 + 2 * (warp >> 2);
+            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) ||
+                !warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort))
+                return false;
+            scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, p, p + 2,
+                      dec[n % ND].col[t], t < sg.len - n * TCC);
+            tma_store_fence();
+            warp_arrive(&yready);
+            return true;
+        };
+        bool ok = scale(0);
+        for (int n = 0; n < nch && ok; ++n) {
             const uint32_t ph = (uint32_t)n & 1u;
             if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_abort);
             if (!ok) break;
@@ -928,7 +941,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
             tma_store_fence();
             warp_arrive(&sready);
-            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) && warp_wait(&delta, ph, &s_abort);
+            ok = warp_wait(&delta, ph, &s_abort) && (n + 1 >= nch || scale(n + 1));
             if (!ok) break;
             tc_fence_after();
             state_add(S, dec[n % ND].tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
@@ -957,7 +970,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // the product that read the last terms
             if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_abort)) break;
             const float w = dec[n % ND].col[t];
-            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 8, w, t < len);
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 4, w, t < len);
             tma_store_fence();
             warp_arrive(&yready);
             warp_arrive(&dempty[n % ND]);
