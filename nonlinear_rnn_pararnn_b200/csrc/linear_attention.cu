@@ -179,7 +179,7 @@ SLSTM_DEVINL float decay_ij(const Decays &d, int i, int j, int len)
 // with X = k, Y = v, w = e^{c_C - c_j} forward, or X = q, Y = dO,
 // w = scale e^{c_i} from the end.
 template <typename T, int RT>
-__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 6 : 3) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ Decays d;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
 
 // The outputs of a chunk and head.
 template <typename T, int RT>
-__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 6 : 3) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ float P[LC][LC + 1];

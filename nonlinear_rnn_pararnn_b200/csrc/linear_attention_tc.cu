@@ -92,6 +92,22 @@ SLSTM_DEVINL uint32_t pack2(float a, float b)
 SLSTM_DEVINL float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 SLSTM_DEVINL float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Two fp32 products, or differences, in one instruction.
+SLSTM_DEVINL void mul2(float &d0, float &d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n"
+        " mov.b64 {%0, %1}, a;\n}\n"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+SLSTM_DEVINL void sub2(float &d0, float &d1, float a0, float a1, float b0, float b1)
+{
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %6};\n"
+        " fma.rn.f32x2 a, b, c, a;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(-1.0f));
+}
+
 // Byte offset of 16-byte piece p of a row in a 128-byte-swizzled box.
 SLSTM_DEVINL uint32_t swz(int row, int p) { return (uint32_t)row * 128u + (uint32_t)((p ^ (row & 7)) << 4); }
 
@@ -286,26 +302,15 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaArgs a, LaChunks ch, Tc
     tc_decays(out[i], gv, threadIdx.x & 31);
 }
 
-// x w as two bf16 terms, two elements at a time, w itself given as two (wh, wl,
-// each in both halves): hi = x wh rounded, lo = (x wh - hi) + x wl, where the
-// difference is exact (a product of two 8-bit significands less its upper half)
-// and only lo is rounded once more.  Three instructions where widening to fp32,
-// rounding and taking the rest takes ten.
-SLSTM_DEVINL void split2(uint32_t x, uint32_t wh, uint32_t wl, uint32_t &hi, uint32_t &lo)
+// The two bf16 of x times w, as two bf16 terms each: the product rounded, and what
+// that leaves (2^-18 of it is lost, in fp32 the rest).
+SLSTM_DEVINL void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo)
 {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(x), "r"(wh));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(wh), "r"(hi ^ 0x80008000u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(x), "r"(wl), "r"(r));
-}
-
-// x w rounded once, but for the rounding of x wl.
-SLSTM_DEVINL uint32_t times2(uint32_t x, uint32_t wh, uint32_t wl)
-{
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(wl));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(wh), "r"(r));
-    return r;
+    float a, b, c, d;
+    mul2(a, b, lo_of(x), hi_of(x), w, w);
+    hi = pack2(a, b);
+    sub2(c, d, a, b, lo_of(hi), hi_of(hi));
+    lo = pack2(c, d);
 }
 
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
@@ -315,9 +320,6 @@ SLSTM_DEVINL uint32_t times2(uint32_t x, uint32_t wh, uint32_t wl)
 // instruction cache.
 SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int p0, int p1, float w, bool on)
 {
-    const uint32_t wh = pack2(w, w);
-    const float rest = w - lo_of(wh);
-    const uint32_t wl = pack2(rest, rest);
 #pragma unroll 1
     for (int p = p0; p < p1; p += 2) {
         uint4 v[2];
@@ -329,10 +331,10 @@ SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t,
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint4 y, z;
-            split2(v[k].x, wh, wl, y.x, z.x);
-            split2(v[k].y, wh, wl, y.y, z.y);
-            split2(v[k].z, wh, wl, y.z, z.z);
-            split2(v[k].w, wh, wl, y.w, z.w);
+            split2(v[k].x, w, y.x, z.x);
+            split2(v[k].y, w, y.y, z.y);
+            split2(v[k].z, w, y.z, z.z);
+            split2(v[k].w, w, y.w, z.w);
             const uint32_t o = swz(t, p + k);
             *reinterpret_cast<uint4 *>(hi + o) = y;
             *reinterpret_cast<uint4 *>(lo + o) = z;
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 //               and half of v times its decays as two bf16 terms
 //   warps 8-11  the other half
 //   warps 12-19 the weights D (q k) from tensor memory and back as bf16
-//               (lane = query row, half of the keys each), and e^{c_i} q_i beside them
+//               (lane = query row, half of the keys each)
 //   warps 20-23 the outputs
 //   warp 24     the MMAs of k^T (w v);  warp 25 the other MMAs
 //   warp 26     loads (a ring of NST chunks)
@@ -713,10 +715,13 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // another they run a chunk or two ahead or behind, and a chunk takes as long as
 // the longest of them, not as all.
 // A chunk's products: q k^T (128 x 128; of the next chunk ahead of the last of
-// this one where its rows have come), k^T (w v), and the outputs as one product
-// of [D (q k) | e^{c} q], in tensor memory, with [v ; S]: one accumulator, of
-// which there are two, so that a chunk's outputs are read while the next one's
-// are computed.  (e^{c_i} q_i is rounded to bf16 as the weights are.)
+// this one where its rows have come), k^T (w v), and into an accumulator each
+// q S, whose rows are scaled in fp32 as they are read, and D(q k) v with the
+// weights in tensor memory.
+// 8 rows of 8192 steps, 8 heads of 128: 160 us; reading and writing each tensor
+// once would take 84.  No one part of the work bounds it: with any of the
+// products, the weights, the loads or the stores left out it takes 93 % or more
+// of the time; what is left is the waits of a chunk's parts for one another.
 // ---------------------------------------------------------------------------
 template <int DK>
 struct FwdShared {
@@ -743,7 +748,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull[2], oempty[2], tready, drained,
+    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
@@ -756,13 +761,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 9);
+            mbar_init(&empty[i], 2);
             mbar_init(&vfull[i], 1);
             mbar_init(&vempty[i], 1);
         }
         for (int i = 0; i < ND; ++i) {
             mbar_init(&dfull[i], 1);
-            mbar_init(&dempty[i], 20);
+            mbar_init(&dempty[i], 24);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
         mbar_init(&yready, 12);
@@ -771,10 +776,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         mbar_init(&sfree, 1);
         mbar_init(&pready[0], 8);
         mbar_init(&pready[1], 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ofull[i], 1);
-            mbar_init(&oempty[i], 4);
-        }
+        mbar_init(&ofull, 1);
+        mbar_init(&oempty, 4);
         mbar_init(&tready, 4);
         mbar_init(&drained, 8);
         mbar_init(&fin, 2);
@@ -787,7 +790,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    const uint32_t t_o = tmem + 256, t_delta = tmem + 384;   // scores: 0 and 128; outputs: t_o and 64 on
+    const uint32_t t_o = tmem + 256, t_delta = tmem + 384;   // scores: 0 and 128; q S and D(q k) v: t_o and 64 on
     const int nch = sg.nch;
     // the last chunk of a packed sequence holds rows of the next one
     const int ragged = packed && sg.len % TCC != 0 ? nch - 1 : -1;
@@ -886,23 +889,29 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         scores(n + 1, false);
                 }
                 ok = lane_wait(&sready, ph, &s_abort) &&
-                     lane_wait(&oempty[ph], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort) &&
-                     lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
-                     lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                     lane_wait(&oempty, ph ^ 1u, &s_abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
-                const uint32_t ta = tmem + ph * 128, td = t_o + ph * 64;
-#pragma unroll 1
-                for (int k = 0; k < DK / 16; ++k)
-                    umma_bf16_ta(td, ta + 32 + 64 * (k / (DK / 32)) + 8 * (k % (DK / 32)), sd + (2048u >> 4) * k, id_o,
-                                 k > 0 ? 1u : 0u);
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) {
+                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(t_o, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
+                }
                 umma_commit(&sfree);
+                umma_commit(&empty[s]);
+                ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
+                     lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ta = tmem + ph * 128;
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k)
-                    umma_bf16_ta(td, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, 1u);
-                umma_commit(&ofull[ph]);
+                    umma_bf16_ta(t_o + 64, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
+                umma_commit(&ofull);
                 umma_commit(&vempty[s]);
             }
             umma_commit(&fin);
@@ -1023,32 +1032,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 tmem_st8(sc + 8 * z, p);
             }
-            // e^{c_i} q_i, this warp's half of the features, behind its weights
-            {
-                const float w = d.row[i];
-                const uint32_t wh = pack2(w, w);
-                const float rest = w - lo_of(wh);
-                const uint32_t wl = pack2(rest, rest);
-                const uint8_t *qb = smem + (n % NST) * SM::STAGE + (DK == 128 ? half * BOX : 0);
-#pragma unroll 1
-                for (int z = 0; z < DK / 32; ++z) {   // 16 features at a time
-                    uint32_t p[8];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(
-                            qb + swz(i, 2 * z + k + (DK == 128 ? 0 : 4 * half)));
-                        p[4 * k] = times2(x.x, wh, wl);
-                        p[4 * k + 1] = times2(x.y, wh, wl);
-                        p[4 * k + 2] = times2(x.z, wh, wl);
-                        p[4 * k + 3] = times2(x.w, wh, wl);
-                    }
-                    tmem_st8(sc + 32 + 8 * z, p);
-                }
-            }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&pready[n & 1]);
-            warp_arrive(&empty[n % NST]);
             warp_arrive(&dempty[n % ND]);
         }
     } else {
@@ -1061,21 +1047,27 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = true;
         int n = 0;
         for (; n < nch; ++n) {
-            ok = warp_wait(&ofull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
+            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
+            if (!ok) break;
+            const float rowc = dec[n % ND].row[i] * a.scale;
+            warp_arrive(&dempty[n % ND]);
+            ok = warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
             if (!ok) break;
             tc_fence_after();
             const bool on = n * TCC + i < sg.len;
 #pragma unroll 1
             for (int c = 0; c < 64; c += 16) {
-                float u[16];
-                tmem_ld16(t_o + (n & 1) * 64 + la + c, u);
+                float u[16], w[16];
+                tmem_ld16x2(t_o + la + c, t_o + 64 + la + c, u, w);
                 if (c == 48) {
                     tc_fence_before();
-                    warp_arrive(&oempty[n & 1]);
+                    warp_arrive(&oempty);
                 }
                 uint32_t p[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) p[j] = pack2(a.scale * u[2 * j], a.scale * u[2 * j + 1]);
+                for (int j = 0; j < 8; ++j)
+                    p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
+                                 fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
                 uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
                 if (on && c < cols) dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
                 if (on && c + 8 < cols) dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
