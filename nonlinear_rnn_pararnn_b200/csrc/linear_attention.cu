@@ -61,41 +61,56 @@ struct Op {
     const float *coef;
 };
 
-// Thread t's elements of the 64 x KB tiles of an operand, in the order in which
-// they are contiguous in memory, and where they go in shared memory.
+// Thread t's elements of the 64 x KB tiles of an operand, and where they go in
+// shared memory.  Where k is contiguous in memory a warp's lanes take the 32 k
+// of four rows m and write the four of a lane at once (one by one, 32 rows of
+// shared memory apart, they would meet in the same banks); where m is, 32 m.
 template <typename T, int RT>
 struct Feed {
     const T *p;           // the first element at depth 0
-    long long step;       // to the next
-    int m, k, dm, dk;     // its place, and the next one's
+    int m, k;
+    bool kc;
     SLSTM_DEVINL explicit Feed(const Op<T> &a)
     {
         const int t = threadIdx.x;
-        const bool kc = a.sk == 1;
-        m = kc ? t / KB : t % 64;
+        kc = a.sk == 1;
+        m = kc ? 4 * (t / KB) : t % 64;
         k = kc ? t % KB : t / 64;
-        dm = kc ? nt<RT>() / KB : 0;
-        dk = kc ? 0 : nt<RT>() / 64;
         p = a.p + m * a.sm + k * a.sk;
-        step = dm * a.sm + dk * a.sk;
     }
+    SLSTM_DEVINL static constexpr int dm(int i) { return (i & 3) + (i >> 2) * 4 * (nt<RT>() / KB); }
+    SLSTM_DEVINL static constexpr int dk(int i) { return i * (nt<RT>() / 64); }
     SLSTM_DEVINL void fetch(float (&v)[nf<RT>()], const Op<T> &a, int k0) const
     {
         const T *q = p + k0 * a.sk;
+        if (kc) {
+            const bool on = k0 + k < a.nk;
+            const float w = a.coef && on ? a.coef[k0 + k] : 1.0f;
 #pragma unroll
-        for (int i = 0; i < nf<RT>(); ++i) {
-            const int kk = k0 + k + i * dk;
-            v[i] = 0.0f;
-            if (m + i * dm < a.nm && kk < a.nk) {
-                v[i] = to_f(q[i * step]);
-                if (a.coef) v[i] *= a.coef[kk];
+            for (int i = 0; i < nf<RT>(); ++i) v[i] = on && m + dm(i) < a.nm ? to_f(q[dm(i) * a.sm]) : 0.0f;
+            if (a.coef)
+#pragma unroll
+                for (int i = 0; i < nf<RT>(); ++i) v[i] *= w;
+        } else {
+            const bool on = m < a.nm;
+#pragma unroll
+            for (int i = 0; i < nf<RT>(); ++i) {
+                const int kk = k0 + k + dk(i);
+                v[i] = on && kk < a.nk ? to_f(q[dk(i) * a.sk]) : 0.0f;
+                if (a.coef) v[i] *= kk < a.nk ? a.coef[kk] : 0.0f;
             }
         }
     }
     SLSTM_DEVINL void stow(float *dst, const float (&v)[nf<RT>()]) const
     {
+        if (kc) {
 #pragma unroll
-        for (int i = 0; i < nf<RT>(); ++i) dst[(k + i * dk) * LDT + m + i * dm] = v[i];
+            for (int i = 0; i < nf<RT>(); i += 4)
+                *reinterpret_cast<float4 *>(dst + k * LDT + m + dm(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < nf<RT>(); ++i) dst[(k + dk(i)) * LDT + m] = v[i];
+        }
     }
 };
 
