@@ -615,6 +615,17 @@ def _la_config(q, k, v, g, lead, scale) -> tuple:
             dk ** -0.5 if scale is None else float(scale), ldq, ldk, ldv)
 
 
+def _la_aligned(fields, **tensors):
+    """Where the tensor cores take the call (the rule is the library's), the token
+    tensors start on 16 bytes."""
+    H, Hqk, dk, dv, dtype, _, _, ldq, ldk, ldv = fields
+    if dtype != _lib.SLSTM_BF16 or dk > 128 or dv > 128 or (dk | dv | ldq | ldk | ldv) % 8:
+        return
+    for name, t in tensors.items():
+        if t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned (its sizes and strides are multiples of 8)")
+
+
 def _la_workspace(fields, B, T, packed, backward, ws, device):
     n = _la_bytes(fields, B, T, packed, backward)
     if n == 0:
@@ -659,6 +670,7 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
             sT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
             _need_on(sT, "sT", state, torch.float32, dev)
+        _la_aligned(cfg, q=q, k=k, v=v, o=o)
         ws = _la_workspace(cfg, B, T, False, False, ws, dev)
         check("slstm_linear_attention_forward", load().slstm_linear_attention_forward(
             _at(q), _at(k), _at(v), _at(g), _at(s0), _at(o), _at(sT), ctypes.byref(_la_struct(*cfg)), B, T, _at(ws),
@@ -699,6 +711,7 @@ def linear_attention_backward(q, k, v, g, s0, dO, dsT=None, *, scale: float = No
     _need_on(dsT, "dsT", state, torch.float32, dev)
     with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
+        _la_aligned(cfg, q=q, k=k, v=v, dO=dO, dq=out["dq"], dk=out["dk"], dv=out["dv"])
         ws = _la_workspace(cfg, B, T, False, True, ws, dev)
         check("slstm_linear_attention_backward", load().slstm_linear_attention_backward(
             _at(q), _at(k), _at(v), _at(g), _at(s0), _at(dO), _at(dsT), _at(out["dq"]), _at(out["dk"]),
@@ -731,6 +744,7 @@ def linear_attention_forward_varlen(q, k, v, g, s0, cu_seqlens, *, scale: float 
             sT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
             _need_on(sT, "sT", state, torch.float32, dev)
+        _la_aligned(cfg, q=q, k=k, v=v, o=o)
         ws = _la_workspace(cfg, n_seq, lead[0], True, False, ws, dev)
         check("slstm_linear_attention_forward_varlen", load().slstm_linear_attention_forward_varlen(
             _at(q), _at(k), _at(v), _at(g), _at(s0), _at(cu_seqlens), n_seq, _at(o), _at(sT),
@@ -755,6 +769,7 @@ def linear_attention_backward_varlen(q, k, v, g, s0, cu_seqlens, dO, dsT=None, *
     _need_on(dsT, "dsT", state, torch.float32, dev)
     with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
+        _la_aligned(cfg, q=q, k=k, v=v, dO=dO, dq=out["dq"], dk=out["dk"], dv=out["dv"])
         ws = _la_workspace(cfg, n_seq, lead[0], True, True, ws, dev)
         check("slstm_linear_attention_backward_varlen", load().slstm_linear_attention_backward_varlen(
             _at(q), _at(k), _at(v), _at(g), _at(s0), _at(cu_seqlens), n_seq, _at(dO), _at(dsT),
@@ -786,7 +801,8 @@ def linear_attention_step(q, k, v, g, s_prev=None, *, scale: float = None, o: to
         else:
             _need_on(out, "out", state, torch.float32, dev)
         check("slstm_linear_attention_step", load().slstm_linear_attention_step(
-            _at(q), _at(k), _at(v), _at(g), _at(s_prev), _at(out), _at(o), ctypes.byref(_la_struct(*cfg)), B, _stream_on(dev)))
+            _at(q), _at(k), _at(v), _at(g), _at(s_prev), _at(out), _at(o), ctypes.byref(_la_struct(*cfg)), B,
+            _stream_on(dev)))
     return o, out
 
 

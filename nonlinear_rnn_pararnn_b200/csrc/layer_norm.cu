@@ -5,10 +5,10 @@
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy
 // A slice is held in the registers of its TPR threads (NV pieces of 8 elements
 // each, 16-byte loads where the width and the pointers allow), so x (and dy)
-// are read once (forward 65536 x 1024, fp32 in, bf16 out: 65 us, 6.2 TB/s;
-// backward 65536 x 8 slices of 128 bf16: 86 us, 4.7 TB/s); the variance is the mean of the squared deviations from the
+// are read once; the variance is the mean of the squared deviations from the
 // mean, not a difference of squares.  All sums are fp32.  Bound by the bytes of
-// the tensors.
+// the tensors: forward 65536 x 1024, fp32 in, bf16 out, 65 us (6.2 TB/s);
+// backward 65536 x 8 slices of 128, bf16, 84 us (4.9 TB/s).
 //
 // dw and db: a block keeps one slice index, walks a strided set of its rows and
 // sums them in the registers that hold its columns; the blocks' partial rows
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
             if (b) v[i][e] += bv[0][e];
         }
     }
-    ln_store<TPR, NV, W>(y + at, d, t, v);
+    if (SLSTM_IN(r, n)) ln_store<TPR, NV, W>(y + at, d, t, v);
 }
 
 // part: [gridDim.x][2][groups d], the blocks' sums of dy xhat and dy.
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) xv[i][e] = rs * (yv[i][e] - mp - xv[i][e] * mx);
-        if (on) ln_store<TPR, NV, W>(dx + n * d, d, t, xv);
+        if (on && SLSTM_IN(n, rows * groups)) ln_store<TPR, NV, W>(dx + n * d, d, t, xv);
     }
     // the block's sums, its slots in order
     float *pw = part + (long long)blockIdx.x * 2 * groups * d + (long long)g * d;

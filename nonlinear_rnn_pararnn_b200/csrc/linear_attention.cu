@@ -51,6 +51,8 @@ SLSTM_DEVINL float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 SLSTM_DEVINL void put(float *p, float v) { *p = v; }
 SLSTM_DEVINL void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+SLSTM_DEVINL long long la_rows(const LaArgs &a) { return a.cu ? (long long)a.T : (long long)a.B * a.T; }
+
 // An operand of a 64 x 64 product: element (m, k) at p[m sm + k sk] for
 // m < nm, k < nk, zero outside, times coef[k] where given.
 template <typename T>
@@ -106,7 +108,8 @@ struct Feed {
         if (kc) {
 #pragma unroll
             for (int i = 0; i < nf<RT>(); i += 4)
-                *reinterpret_cast<float4 *>(dst + k * LDT + m + dm(i)) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                *reinterpret_cast<float4 *>(dst + k * LDT + m + dm(i)) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
             for (int i = 0; i < nf<RT>(); ++i) dst[(k + dk(i)) * LDT + m] = v[i];
@@ -194,7 +197,8 @@ SLSTM_DEVINL float decay_ij(const Decays &d, int i, int j, int len)
 // with X = k, Y = v, w = e^{c_C - c_j} forward, or X = q, Y = dO,
 // w = scale e^{c_i} from the end.
 template <typename T, int RT>
-__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2)
+    la_delta_kernel(LaArgs a, LaChunks ch, bool back, float *out, float *tot)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ Decays d;
@@ -220,7 +224,7 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_delta_kernel(LaA
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int m = m0 + ty * RT + i, n = n0 + tx * 4 + j;
-            if (m < a.dk && n < a.dv) dst[(long long)m * a.dv + n] = acc[i][j];
+            if (m < a.dk && n < a.dv && SLSTM_IN(c, ch.total)) dst[(long long)m * a.dv + n] = acc[i][j];
         }
 }
 
@@ -253,8 +257,11 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
         }
     };
     auto store = [](float *p, const float (&v)[V]) {
-        if (V == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[V > 1 ? 1 : 0], v[V > 2 ? 2 : 0], v[V > 3 ? 3 : 0]);
-        else *p = v[0];
+        if (V == 4)
+            *reinterpret_cast<float4 *>(p) =
+                make_float4(v[0], v[V > 1 ? 1 : 0], v[V > 2 ? 2 : 0], v[V > 3 ? 3 : 0]);
+        else
+            *p = v[0];
     };
     float s[V];
 #pragma unroll
@@ -285,7 +292,8 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
 
 // The outputs of a chunk and head.
 template <typename T, int RT>
-__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2)
+    la_out_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states)
 {
     __shared__ __align__(16) float sA[KB * LDT], sB[KB * LDT];
     __shared__ float P[LC][LC + 1];
@@ -329,7 +337,8 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2) la_out_kernel(LaArg
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r < ck.len && n < a.dv) put(o + (long long)r * a.H * a.dv + n, acc[i][j] * a.scale);
+                if (r < ck.len && n < a.dv && SLSTM_IN(ck.row + r, la_rows(a)))
+                    put(o + (long long)r * a.H * a.dv + n, acc[i][j] * a.scale);
             }
     }
 }
@@ -355,9 +364,9 @@ struct BackShared {
 // heads share a query and key head; dgc: the chunk's sum of dg, [c][h], where
 // the decay belongs to the head.
 template <typename T, int RT>
-__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2) la_back_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states,
-                                                     const float *__restrict__ dstates, float *part_q, float *part_k,
-                                                     float *dgc)
+__global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
+    la_back_kernel(LaArgs a, LaChunks ch, const float *__restrict__ states, const float *__restrict__ dstates,
+                   float *part_q, float *part_k, float *dgc)
 {
     extern __shared__ __align__(16) char smem[];
     BackShared &s = *reinterpret_cast<BackShared *>(smem);
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2) la_back_kernel(LaAr
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r >= len || n >= a.dk) continue;
+                if (r >= len || n >= a.dk || !SLSTM_IN(ck.row + r, la_rows(a))) continue;
                 if (part_q) {
                     const long long at = ((ck.row + r) * a.H + h) * a.dk + n;
                     part_q[at] = p[i][j];
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2) la_back_kernel(LaAr
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r < len && n < a.dv)
+                if (r < len && n < a.dv && SLSTM_IN(ck.row + r, la_rows(a)))
                     put(static_cast<T *>(a.dv_) + (ck.row + r) * ldo + (long long)h * a.dv + n, t[i][j]);
             }
     }
@@ -813,7 +822,8 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, cons
             const long long at = base + (long long)r * a.dv + col;
             float s[VEC];
             if (VEC == 4) {
-                const float4 f = s_prev ? __ldcs(reinterpret_cast<const float4 *>(s_prev + at)) : make_float4(0, 0, 0, 0);
+                const float4 f =
+                    s_prev ? __ldcs(reinterpret_cast<const float4 *>(s_prev + at)) : make_float4(0, 0, 0, 0);
                 s[0] = f.x;
                 s[VEC > 1 ? 1 : 0] = f.y;
                 s[VEC > 2 ? 2 : 0] = f.z;

@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
-    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], drained[2], staged, unstaged, fin;
+    __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], drained[2];
+    __shared__ uint64_t staged, unstaged, fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
     const LaArgs &a = g.a;
@@ -570,8 +571,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 const int r = (warp - 18) * 32 + lane;
                 const __nv_bfloat16 *p = r < 128 ? g.phi : g.plo;
                 if ((r & 127) < a.dk)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                        p + ((sg.c0 + chunk(n + 1)) * a.H + h) * a.dk * a.dv + (long long)(r & 127) * a.dv + 64 * tile));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + ((sg.c0 + chunk(n + 1)) * a.H + h) * a.dk * a.dv +
+                                                             (long long)(r & 127) * a.dv + 64 * tile));
             }
             if (!warp_wait(&staged, (uint32_t)n & 1u, &s_abort)) break;
             if (warp == 18 && lane == 0) {
@@ -614,7 +615,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             const TcDecays &d = dec[n % ND];
             const int len = rows(n);
             uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
-            scale_row(st + SM::NB * BOX, y, y + BOX, t, 4 * half, 4 * half + 4, back ? a.scale * d.row[t] : d.col[t], t < len);
+            scale_row(st + SM::NB * BOX, y, y + BOX, t, 4 * half, 4 * half + 4,
+                      back ? a.scale * d.row[t] : d.col[t], t < len);
             // rows behind a packed sequence belong to another one
             if (packed && t >= len)
                 for (int i = half; i < SM::NB; i += 2) zero_row(st + i * BOX, t);
@@ -885,8 +887,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 // rows have come, and never make them wait
                 if (n + 1 < nch) {
 #pragma unroll 1
-                    for (int i = 0; i < (1 << 20) && scored <= n + 1 && !done(&pready[ph], (uint32_t)(n >> 1) & 1u); ++i)
+                    for (int i = 0; i < (1 << 20); ++i) {
+                        if (scored > n + 1 || done(&pready[ph], (uint32_t)(n >> 1) & 1u)) break;
                         scores(n + 1, false);
+                    }
                 }
                 ok = lane_wait(&sready, ph, &s_abort) &&
                      lane_wait(&oempty, ph ^ 1u, &s_abort);
@@ -910,7 +914,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 const uint32_t ta = tmem + ph * 128;
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k)
-                    umma_bf16_ta(t_o + 64, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
+                    umma_bf16_ta(t_o + 64, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o,
+                                 k > 0 ? 1u : 0u);
                 umma_commit(&ofull);
                 umma_commit(&vempty[s]);
             }
@@ -1040,6 +1045,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     } else {
         const int i = (warp & 3) * 32 + lane;   // query row
         const uint32_t la = (uint32_t)((warp & 3) * 32) << 16;
+        [[maybe_unused]] const long long row = sg.row + i, all = a.cu ? (long long)a.T : (long long)a.B * a.T;
         const int cols = min(64, a.dv - tile * 64);
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
                            (long long)h * a.dv + tile * 64;
@@ -1069,7 +1075,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
                                  fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
                 uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
-                if (on && c < cols) dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
+                if (on && c < cols && SLSTM_IN(row + (long long)n * TCC, all))
+                    dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
                 if (on && c + 8 < cols) dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
             }
         }

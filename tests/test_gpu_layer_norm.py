@@ -139,7 +139,8 @@ def test_refusals(cuda_device):
                  lambda: api.layer_norm_forward(x, w, groups=5), lambda: api.layer_norm_forward(x, w, groups=0),
                  lambda: api.layer_norm_forward(x, w.double()), lambda: api.layer_norm_forward(x[:0], w),
                  lambda: api.layer_norm_forward(x, w, y_dtype=torch.float16),
-                 lambda: api.layer_norm_forward(torch.zeros(1, 16385, device="cuda"), torch.zeros(16385, device="cuda")),
+                 lambda: api.layer_norm_forward(torch.zeros(1, 16385, device="cuda"),
+                                                torch.zeros(16385, device="cuda")),
                  lambda: api.layer_norm_backward(x, w, y[:3], m, r), lambda: api.layer_norm_backward(x, w, y, m[:3], r),
                  lambda: api.layer_norm_backward(x, w, y, m, r, groups=2),
                  lambda: api.layer_norm_backward(x, w, y, m, r, ws=torch.empty(8, dtype=torch.uint8, device="cuda"))):
@@ -147,3 +148,20 @@ def test_refusals(cuda_device):
             call()
     with pytest.raises(RuntimeError):
         api.layer_norm_forward(x, w, eps=-1.0)
+
+
+def test_offsets_beyond_32_bits(cuda_device):
+    """More than 2^31 elements: the last rows as they are alone."""
+    D, rows = 1024, 2 ** 21 + 100
+    x = torch.zeros(rows, D, dtype=BF16, device="cuda")
+    tail = torch.randn(64, D, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda").to(BF16)
+    x[-64:] = tail
+    w = torch.ones(D, device="cuda")
+    y, m, r = api.layer_norm_forward(x, w)
+    y1, m1, r1 = api.layer_norm_forward(tail, w)
+    assert torch.equal(y[-64:], y1) and torch.equal(m[-64:], m1) and torch.equal(r[-64:], r1)
+    out = api.layer_norm_backward(x, w, x, m, r)
+    out1 = api.layer_norm_backward(tail, w, tail, m1, r1)
+    assert torch.equal(out["dx"][-64:], out1["dx"]) and (out["dx"][:-64] == 0).all()
+    # the other rows add nothing, the order of the others may change: 64 terms
+    assert torch.allclose(out["db"], out1["db"], rtol=0, atol=64 * 64 * U * 6)

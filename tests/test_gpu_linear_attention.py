@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 
 
-def _inputs(lead, Hqk, H, dk, dv, dtype, seed, *, per_head=False, nseq=None, s0=True, resets=0, fused=False, grads=True):
+def _inputs(lead, Hqk, H, dk, dv, dtype, seed, *, per_head=False, nseq=None, s0=True, resets=0, fused=False,
+            grads=True):
     gen = torch.Generator(device="cuda").manual_seed(seed)
 
     def r(*s):
@@ -412,3 +413,142 @@ def test_with_the_norms(dtype, cuda_device):
         b = b.detach()
         err = float((a.double().cpu() - b).norm() / b.norm())
         assert err <= bound, (name, err)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [-0.7, 0.0])
+def test_scales(scale, dtype, cuda_device):
+    x = _inputs((1, 200), 1, 2, 64, 64, dtype, 17)
+    want, _ = _dense(x, scale)
+    _, size = _dense(x, abs(scale))
+    got = _run(x, scale)
+    _check(got, want, size, dtype, 200, 64, 64, 1)
+    if scale == 0.0:
+        assert (got["o"] == 0).all() and (got["dq"] == 0).all()
+
+
+@pytest.mark.parametrize("dk,dv,per_head", [(64, 128, False), (128, 64, True)])
+def test_long_rows_in_segments(dk, dv, per_head, cuda_device):
+    """One long row of few heads, dense and packed: its chunks are shared out in segments, whose first
+    states come from a pass of their own."""
+    T = 3000
+    x = _inputs((1, T), 1, 2, dk, dv, BF16, 18, per_head=per_head, resets=0 if per_head else 900)
+    scale = dk ** -0.5
+    want, size = _dense(x, scale)
+    got = _run(x, scale)
+    _check(got, want, size, BF16, T, dk, dv, 2)
+    p = {n: (y if n in ("s0", "dsT") or (n == "g" and per_head) else y[0]) for n, y in x.items()}
+    # packed behind a short sequence and an empty one, which are one segment and none
+    cut = 40
+    cu = torch.tensor([0, cut, cut, T], dtype=torch.int32, device="cuda")
+    s0 = torch.cat([x["s0"]] * 3)
+    dsT = torch.cat([x["dsT"]] * 3)
+    got = {}
+    got["o"], got["sT"] = api.linear_attention_forward_varlen(p["q"], p["k"], p["v"], p["g"], s0, cu, scale=scale)
+    got.update(api.linear_attention_backward_varlen(p["q"], p["k"], p["v"], p["g"], s0, cu, p["dO"], dsT, scale=scale))
+    assert torch.equal(got["sT"][1], s0[1]) and torch.equal(got["ds0"][1], dsT[1])
+    total = [0.0, 0.0]
+    for i, at in ((0, slice(0, cut)), (2, slice(cut, T))):
+        one = {n: (y if n == "g" and per_head else y[at]) for n, y in p.items() if n in ("q", "k", "v", "g", "dO")}
+        want, size = ref.values({**one, "s0": s0[i], "dsT": dsT[i]}, scale)
+        part = {m: got[m][at] for m in ("o", "dq", "dk", "dv")}
+        part.update({m: got[m][i] for m in ("sT", "ds0")})
+        if per_head:
+            total = [total[0] + want["dg"], total[1] + size["dg"]]
+        else:
+            part["dg"] = got["dg"][at]
+        _check(part, want, size, BF16, T, dk, dv, 2, i)
+    if per_head:
+        _check({"dg": got["dg"]}, {"dg": total[0]}, {"dg": total[1]}, BF16, T, dk, dv, 2)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_short_sequences(dtype, cuda_device):
+    """Thousands of sequences of no or a few tokens, as many offsets as several rounds of the table."""
+    gen = torch.Generator().manual_seed(19)
+    lens = torch.randint(0, 4, (3001,), generator=gen)
+    cu = torch.zeros(3002, dtype=torch.int64)
+    cu[1:] = torch.cumsum(lens, 0)
+    total = int(cu[-1])
+    x = _inputs((total,), 1, 1, 16, 16, dtype, 20, nseq=3001, grads=False)
+    cut = cu.to(torch.int32).cuda()
+    o, sT = api.linear_attention_forward_varlen(x["q"], x["k"], x["v"], x["g"], x["s0"], cut, scale=0.25)
+    # all sequences at once, padded to three tokens whose decay is none and whose key is nothing
+    at = (torch.arange(3)[None] + cu[:-1, None]).clamp(max=total - 1).cuda()
+    live = (torch.arange(3)[None] < lens[:, None]).cuda()
+    q, k, v, g = (x[n].double()[at] for n in ("q", "k", "v", "g"))
+    k, g = k * live[..., None, None], g * live[..., None]
+    s, mag = x["s0"].double(), x["s0"].double().abs()
+    for t in range(3):
+        a = torch.exp(g[:, t])[..., None, None]
+        s = a * s + k[:, t, :, :, None] * v[:, t, :, None, :]
+        mag = a * mag + (k[:, t, :, :, None] * v[:, t, :, None, :]).abs()
+        want = 0.25 * (s * q[:, t, :, :, None]).sum(2)
+        size = 0.25 * (mag * q[:, t, :, :, None].abs()).sum(2)
+        on = live[:, t]
+        _check({"o": o[at[:, t]][on]}, {"o": want[on]}, {"o": size[on]}, dtype, 3, 16, 16, 1)
+    _check({"sT": sT}, {"sT": s}, {"sT": mag}, dtype, 3, 16, 16, 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_in_a_graph_and_on_another_stream(dtype, cuda_device):
+    x = _inputs((6,), 2, 4, 64, 64, dtype, 21, grads=False)
+    want_o, want_s = api.linear_attention_step(x["q"], x["k"], x["v"], x["g"], x["s0"])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        y = {n: t.clone() for n, t in x.items() if t is not None}   # made on that stream
+        o, s = api.linear_attention_step(y["q"], y["k"], y["v"], y["g"], y["s0"])
+    st.synchronize()
+    assert torch.equal(o, want_o) and torch.equal(s, want_s)
+    state = x["s0"].clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        o, _ = api.linear_attention_step(x["q"], x["k"], x["v"], x["g"], state, out=state)
+    state.copy_(x["s0"])
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want_o) and torch.equal(state, want_s)
+    gr.replay()   # a token more
+    torch.cuda.synchronize()
+    o2, s2 = api.linear_attention_step(x["q"], x["k"], x["v"], x["g"], want_s)
+    assert torch.equal(o, o2) and torch.equal(state, s2)
+
+
+def test_misaligned_rows(cuda_device):
+    """Rows that start on no 16 bytes: refused where the tensor cores would take them, taken elsewhere."""
+    x = _inputs((2, 20), 1, 1, 16, 16, BF16, 22)
+    wide = torch.zeros(2, 20, 24, dtype=BF16, device="cuda")
+    wide[..., 4:20] = x["q"][:, :, 0]
+    with pytest.raises(ValueError, match="aligned"):
+        api.linear_attention_forward(wide[..., 4:20].unsqueeze(2), x["k"], x["v"], x["g"], x["s0"])
+    odd = torch.zeros(2, 20, 19, dtype=BF16, device="cuda")
+    odd[..., 3:] = x["q"][:, :, 0]
+    o, sT = api.linear_attention_forward(odd[..., 3:].unsqueeze(2), x["k"], x["v"], x["g"], x["s0"], scale=0.25)
+    want, size = _dense(x, 0.25)
+    _check({"o": o, "sT": sT}, want, size, BF16, 20, 16, 16, 1)
+
+
+def test_checked_build_runs_clean(cuda_device):
+    """The bounds-checked build sees no access out of range on ragged sizes."""
+    import ctypes
+
+    from nonlinear_rnn_pararnn_b200 import _lib
+    with _lib.checked_library() as lib:
+        assert lib.slstm_check_clear() == _lib.SLSTM_OK
+        for dtype in (F32, BF16):
+            for d in (24, 33):
+                x = _inputs((2, 133), 1, 2, d, d, dtype, 23, fused=True)
+                _run(x, 1.0)
+                api.linear_attention_step(*(x[n][:, 0].contiguous() for n in ("q", "k", "v", "g")), x["s0"])
+            x = _inputs((90,), 1, 1, 40, 40, dtype, 24, nseq=3)
+            cu = torch.tensor([2, 2, 70, 88], dtype=torch.int32, device="cuda")
+            api.linear_attention_forward_varlen(x["q"], x["k"], x["v"], x["g"], x["s0"], cu)
+            api.linear_attention_backward_varlen(x["q"], x["k"], x["v"], x["g"], x["s0"], cu, x["dO"], x["dsT"])
+            for D in (64, 100):
+                z = torch.randn(33, D, device="cuda").to(dtype)
+                w = torch.ones(D, device="cuda")
+                y, m, r = api.layer_norm_forward(z, w)
+                api.layer_norm_backward(z, w, y, m, r)
+        out = (ctypes.c_longlong * 4)()
+        assert lib.slstm_check_status(out) == _lib.SLSTM_OK and out[0] == 0, list(out)
