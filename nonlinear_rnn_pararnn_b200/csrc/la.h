@@ -50,8 +50,10 @@ struct LaChunks {
 };
 size_t la_table_bytes(const LaArgs &a);
 int la_chunk_bound(const LaArgs &a, int C);
-// Fill the table (packed) at `mem` on `st`.
-cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st);
+// Fill the table (packed) at `mem` on `st`; with out2, a second one for chunks of
+// C2 rows at mem2 in the same launch.
+cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st, int C2 = 0,
+                      void *mem2 = nullptr, LaChunks *out2 = nullptr);
 
 // The states over the chunks (or segments) of each sequence, elementwise: the
 // E-element deltas in buf[chunk][h], with the decays tot[chunk][h], give way to
@@ -68,9 +70,10 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st);
 size_t la_tc_backward_workspace(const LaArgs &a);
 cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st);
 
-// Sums of the fp32 per-head partial gradients over the heads that share a
-// query and key head: out[row][hq][d] = sum over r of part[row][hq * rep + r][d].
-cudaError_t la_share_sum(const float *part, void *out, int dtype, const LaChunks &ch, const LaArgs &a, cudaStream_t st);
+// Sums of the fp32 per-head partial gradients over the heads that share a query
+// and key head, into a.dq and a.dk_: dq[row][hq][d] = sum over r of
+// pq[row][hq * rep + r][d].
+cudaError_t la_share_sum(const float *pq, const float *pk, const LaChunks &ch, const LaArgs &a, cudaStream_t st);
 // dg[h] = sum of part[c][h] over the chunks in order.
 cudaError_t la_head_sum(const float *part, float *dg, const LaChunks &ch, int H, cudaStream_t st);
 

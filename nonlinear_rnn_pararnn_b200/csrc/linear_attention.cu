@@ -538,20 +538,43 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
     }
 }
 
-// One thread for each element of dq or dk.
-template <typename T>
-__global__ void __launch_bounds__(256) la_share_kernel(const float *__restrict__ part, T *out, LaChunks ch,
-                                                       long long rows, int Hqk, int rep, int dk)
+// V elements of dq (blockIdx.y = 0) or dk a thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) la_share_kernel(const float *__restrict__ pq, const float *__restrict__ pk, T *dq,
+                                                       T *dk_, LaChunks ch, long long rows, int Hqk, int rep, int dk)
 {
+    const float *part = blockIdx.y ? pk : pq;
+    T *out = blockIdx.y ? dk_ : dq;
     // packed: the rows of the sequences only
-    const long long w = (long long)Hqk * dk, i0 = ch.pos ? ch.pos[0] * w : 0;
+    const int per = dk / V;   // pieces of a head
+    const long long w = (long long)Hqk * per, i0 = ch.pos ? ch.pos[0] * w : 0;
     const long long n = ch.pos ? ch.pos[ch.n_seq] * w : rows * w;
     for (long long i = i0 + (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-        const int d = (int)(i % dk);
-        const long long rh = i / dk;   // row * Hqk + hq
-        float s = 0.0f;
-        for (int r = 0; r < rep; ++r) s += part[(rh * rep + r) * dk + d];
-        put(out + i, s);
+        const long long rh = i / per;   // row * Hqk + hq
+        const int d = (int)(i - rh * per) * V;
+        const float *p = part + rh * rep * dk + d;
+        float s[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[k] = 0.0f;
+#pragma unroll 4
+        for (int r = 0; r < rep; ++r, p += dk) {
+            if (V == 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(p);
+                s[0] += f.x;
+                s[V > 1 ? 1 : 0] += f.y;
+                s[V > 2 ? 2 : 0] += f.z;
+                s[V > 3 ? 3 : 0] += f.w;
+            } else {
+                s[0] += *p;
+            }
+        }
+        // (four elements of a type stand on their own width: out is aligned to them)
+        struct alignas(V * sizeof(T)) Piece {
+            T v[V];
+        } piece;
+#pragma unroll
+        for (int k = 0; k < V; ++k) put(&piece.v[k], s[k]);
+        *reinterpret_cast<Piece *>(out + rh * dk + d) = piece;
     }
 }
 
@@ -574,11 +597,16 @@ __global__ void __launch_bounds__(256) la_head_sum_kernel(const float *__restric
 }
 
 // The table of packed sequences: offsets clamped into [0, T] and raised to the
-// largest before them, and the chunks before each sequence.  One block, 1024
-// offsets at a time.
+// largest before them, and the chunks before each sequence.  One block a table,
+// 1024 offsets at a time.
 __global__ void __launch_bounds__(1024) la_table_kernel(const int *__restrict__ cu, int n_seq, int T, int C, int *pos,
-                                                        int *coff)
+                                                        int *coff, int C2, int *pos2, int *coff2)
 {
+    if (blockIdx.x == 1) {
+        C = C2;
+        pos = pos2;
+        coff = coff2;
+    }
     __shared__ int wm[32], ws[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int top = 0, sum = 0;   // the largest offset, and the chunks, of the tiles before
@@ -629,15 +657,22 @@ int la_chunk_bound(const LaArgs &a, int C)
     return a.cu ? a.T / C + a.B : a.B * ((a.T - 1) / C + 1);
 }
 
-cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st)
+cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st, int C2, void *mem2,
+                      LaChunks *out2)
 {
-    *out = LaChunks{a.B, a.T, C, (a.T - 1) / C + 1, la_chunk_bound(a, C), nullptr, nullptr};
+    int *tab[2][2] = {};
+    for (int i = 0; i < 2; ++i) {
+        LaChunks *o = i ? out2 : out;
+        if (o == nullptr) break;
+        const int c = i ? C2 : C;
+        *o = LaChunks{a.B, a.T, c, (a.T - 1) / c + 1, la_chunk_bound(a, c), nullptr, nullptr};
+        if (a.cu == nullptr) continue;
+        char *p = static_cast<char *>(i ? mem2 : mem);
+        o->pos = tab[i][0] = reinterpret_cast<int *>(p);
+        o->coff = tab[i][1] = reinterpret_cast<int *>(p + up256(4 * ((size_t)a.B + 1)));
+    }
     if (a.cu == nullptr) return cudaSuccess;
-    int *pos = static_cast<int *>(mem);
-    int *coff = reinterpret_cast<int *>(static_cast<char *>(mem) + up256(4 * ((size_t)a.B + 1)));
-    la_table_kernel<<<1, 1024, 0, st>>>(a.cu, a.B, a.T, C, pos, coff);
-    out->pos = pos;
-    out->coff = coff;
+    la_table_kernel<<<out2 ? 2 : 1, 1024, 0, st>>>(a.cu, a.B, a.T, C, tab[0][0], tab[0][1], C2, tab[1][0], tab[1][1]);
     return cudaGetLastError();
 }
 
@@ -653,17 +688,27 @@ cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, con
     return cudaGetLastError();
 }
 
-cudaError_t la_share_sum(const float *part, void *out, int dtype, const LaChunks &ch, const LaArgs &a, cudaStream_t st)
+namespace {
+
+template <typename T>
+cudaError_t share_sum(const float *pq, const float *pk, const LaChunks &ch, const LaArgs &a, cudaStream_t st)
 {
     const long long rows = a.cu ? a.T : (long long)a.B * a.T;
-    const long long n = rows * a.Hqk * a.dk;
-    const int blocks = (int)min((n + 255) / 256, (long long)148 * 32);
-    if (dtype == SLSTM_F32)
-        la_share_kernel<<<blocks, 256, 0, st>>>(part, static_cast<float *>(out), ch, rows, a.Hqk, a.H / a.Hqk, a.dk);
-    else
-        la_share_kernel<<<blocks, 256, 0, st>>>(part, static_cast<__nv_bfloat16 *>(out), ch, rows, a.Hqk,
-                                                a.H / a.Hqk, a.dk);
+    T *dq = static_cast<T *>(a.dq), *dk = static_cast<T *>(a.dk_);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(dq) | reinterpret_cast<uintptr_t>(dk);
+    const bool four = a.dk % 4 == 0 && at % (4 * sizeof(T)) == 0;
+    const long long n = rows * a.Hqk * (four ? a.dk / 4 : a.dk);
+    const dim3 grid((unsigned)min((n + 255) / 256, (long long)148 * 16), 2);
+    if (four) la_share_kernel<T, 4><<<grid, 256, 0, st>>>(pq, pk, dq, dk, ch, rows, a.Hqk, a.H / a.Hqk, a.dk);
+    else la_share_kernel<T, 1><<<grid, 256, 0, st>>>(pq, pk, dq, dk, ch, rows, a.Hqk, a.H / a.Hqk, a.dk);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t la_share_sum(const float *pq, const float *pk, const LaChunks &ch, const LaArgs &a, cudaStream_t st)
+{
+    return a.dtype == SLSTM_F32 ? share_sum<float>(pq, pk, ch, a, st) : share_sum<__nv_bfloat16>(pq, pk, ch, a, st);
 }
 
 cudaError_t la_head_sum(const float *part, float *dg, const LaChunks &ch, int H, cudaStream_t st)
@@ -739,8 +784,7 @@ cudaError_t backward(const LaArgs &a, const LaChunks &ch, const SimtWs &w, cudaS
     la_back_kernel<T, RT><<<(unsigned)ch.total * a.H, nt<RT>(), sizeof(BackShared), st>>>(a, ch, w.S, w.dS, w.pq, w.pk,
                                                                                        w.dgc);
     e = cudaGetLastError();
-    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, a.dq, a.dtype, ch, a, st);
-    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pk, a.dk_, a.dtype, ch, a, st);
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, w.pk, ch, a, st);
     if (e == cudaSuccess && a.dg && a.per_head) e = la_head_sum(w.dgc, a.dg, ch, a.H, st);
     return e;
 }

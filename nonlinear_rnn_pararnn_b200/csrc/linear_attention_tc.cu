@@ -451,8 +451,10 @@ constexpr int STATE_THREADS = 832;
 
 template <int DK>
 __global__ void __launch_bounds__(STATE_THREADS, 1)
-    la_state_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
-                    const __grid_constant__ CUtensorMap mhi, const __grid_constant__ CUtensorMap mlo, TcArgs g)
+    la_state_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap my0,
+                    const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap my1,
+                    const __grid_constant__ CUtensorMap mhi, const __grid_constant__ CUtensorMap mlo,
+                    const __grid_constant__ TcArgs g0, const __grid_constant__ TcArgs g1)
 {
     typedef StateShared<DK> SM;
     constexpr int NST = SM::NST;
@@ -463,6 +465,9 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     __shared__ uint64_t staged, unstaged, fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
+    // the passes of both directions for the segments' first states run in one launch
+    const TcArgs &g = blockIdx.y == 0 ? g0 : g1;
+    const CUtensorMap *mx = blockIdx.y == 0 ? &mx0 : &mx1, *my = blockIdx.y == 0 ? &my0 : &my1;
     const LaArgs &a = g.a;
     const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
     Seg sg;
@@ -514,13 +519,13 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 mbar_expect_tx(&full[s], SM::STAGE);
                 const int t = sg.t + chunk(n) * TCC;
 #pragma unroll
-                for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, &mx, &full[s], 64 * i, hq, t, sg.b);
-                tma_load_4d(st + SM::NB * BOX, &my, &full[s], 64 * tile, h, t, sg.b);
+                for (int i = 0; i < SM::NB; ++i) tma_load_4d(st + i * BOX, mx, &full[s], 64 * i, hq, t, sg.b);
+                tma_load_4d(st + SM::NB * BOX, my, &full[s], 64 * tile, h, t, sg.b);
                 if (n + NST < nch) {   // the chunk that takes this one's place, as far as the L2 cache
                     const int u = sg.t + chunk(n + NST) * TCC;
 #pragma unroll
-                    for (int i = 0; i < SM::NB; ++i) tma_prefetch_4d(&mx, 64 * i, hq, u, sg.b);
-                    tma_prefetch_4d(&my, 64 * tile, h, u, sg.b);
+                    for (int i = 0; i < SM::NB; ++i) tma_prefetch_4d(mx, 64 * i, hq, u, sg.b);
+                    tma_prefetch_4d(my, 64 * tile, h, u, sg.b);
                 }
             }
             s_loaded = n;
@@ -1766,15 +1771,24 @@ cudaError_t launch_decays(const LaArgs &a, const LaChunks &ch, TcDecays *dec, cu
     return cudaGetLastError();
 }
 
+// One direction (g1 null) or both; hi, lo: where the chunks' states go, if they do.
 template <int DK>
-cudaError_t launch_state(const CUtensorMap &x, const CUtensorMap &y, const CUtensorMap &hi, const CUtensorMap &lo,
-                         const TcArgs &g, cudaStream_t st)
+cudaError_t launch_state(const CUtensorMap *xy, const CUtensorMap *hilo, const TcArgs &g0, const TcArgs *g1,
+                         cudaStream_t st)
 {
     const int bytes = StateShared<DK>::BYTES;
     cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    la_state_kernel<DK><<<(unsigned)g.seg.total * g.a.H * g.tiles, STATE_THREADS, bytes, st>>>(x, y, hi, lo, g);
+    const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, g1 ? 2 : 1);
+    la_state_kernel<DK><<<grid, STATE_THREADS, bytes, st>>>(xy[0], xy[1], xy[g1 ? 2 : 0], xy[g1 ? 3 : 1], hilo[0],
+                                                          hilo[1], g0, g1 ? *g1 : g0);
     return cudaGetLastError();
+}
+
+cudaError_t launch_states(const CUtensorMap *xy, const CUtensorMap *hilo, const TcArgs &g0, const TcArgs *g1,
+                          cudaStream_t st)
+{
+    return g0.a.dk <= 64 ? launch_state<64>(xy, hilo, g0, g1, st) : launch_state<128>(xy, hilo, g0, g1, st);
 }
 
 template <int DK>
@@ -1877,8 +1891,7 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
     g.tiles = (a.dv + 63) / 64;
     const int L = seg_chunks(a, a.H * g.tiles);
     const FwdWs w = fwd_layout(a, L, ws);
-    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
-    if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg);
     if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
     g.dec = w.dec;
@@ -1893,9 +1906,8 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
         s.first = nullptr;
         s.fin = w.states;
         s.fin_tot = w.tot;
-        // (it stores no chunk's state: the last two maps are not used)
-        e = a.dk <= 64 ? launch_state<64>(m[1], m[2], m[1], m[1], s, st)
-                       : launch_state<128>(m[1], m[2], m[1], m[1], s, st);
+        const CUtensorMap xy[4] = {m[1], m[2], m[1], m[2]};
+        e = launch_states(xy, xy, s, nullptr, st);   // (it stores no chunk's state)
         if (e == cudaSuccess) e = la_scan(g.seg, a.H, a.dk * a.dv, false, w.states, w.tot, a.s0, a.sT, st, 1);
         if (e != cudaSuccess) return e;
         g.init = w.states;
@@ -1921,8 +1933,7 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     const int L = seg_chunks(a, a.H * g.tiles);
     const BackWs w = back_layout(a, L, ws);
     const int DK = a.dk <= 64 ? 64 : 128, DV = a.dv <= 64 ? 64 : 128;
-    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st);
-    if (e == cudaSuccess) e = la_chunks(a, L * TCC, w.seg_table, &g.seg, st);
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg);
     if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
     g.dec = w.dec;
@@ -1934,43 +1945,42 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     for (int i = 0; i < 2; ++i)
         ok = ok && state_map(&m[4 + 2 * i], w.hi[i], a, n, DK) && state_map(&m[5 + 2 * i], w.lo[i], a, n, DK);
     if (!ok) return cudaErrorInvalidValue;
-    // the states: forward, then from the end (which meets the forward ones for dg)
-    for (int i = 0; i < 2; ++i) {
-        TcArgs s = g;
-        s.back = i == 1;
-        const CUtensorMap &x = s.back ? m[0] : m[1], &y = s.back ? m[3] : m[2];
-        const CUtensorMap &hi = m[4 + 2 * i], &lo = m[5 + 2 * i];
-        const float *first = s.back ? a.dsT : a.s0;
-        float *last = s.back ? a.ds0 : nullptr;
-        if (w.seg[i]) {
-            s.fin = w.seg[i];
-            s.fin_tot = w.tot[i];
-            e = DK == 64 ? launch_state<64>(x, y, hi, lo, s, st) : launch_state<128>(x, y, hi, lo, s, st);
-            if (e == cudaSuccess)
-                e = la_scan(g.seg, a.H, a.dk * a.dv, s.back, w.seg[i], w.tot[i], first, last, st, 1);
-            if (e != cudaSuccess) return e;
-            s.fin = nullptr;
-            s.fin_tot = nullptr;
-            s.init = w.seg[i];
-        } else {
-            if (a.cu && last) {
-                const long long HE = (long long)a.H * a.dk * a.dv;
-                la_empty_kernel<<<dim3(a.B, (unsigned)min((HE + 1023) / 1024, 64LL)), 256, 0, st>>>(g.seg, HE, first,
-                                                                                                  last);
-                e = cudaGetLastError();
-                if (e != cudaSuccess) return e;
-            }
+    const CUtensorMap xy[4] = {m[1], m[2], m[0], m[3]};
+    TcArgs dir[2] = {g, g};
+    const float *first[2] = {a.s0, a.dsT};
+    float *last[2] = {nullptr, a.ds0};
+    dir[1].back = true;
+    if (w.seg[0]) {
+        for (int i = 0; i < 2; ++i) {
+            dir[i].fin = w.seg[i];
+            dir[i].fin_tot = w.tot[i];
         }
-        s.first = first;
-        s.last = last;
+        e = launch_states(xy, xy, dir[0], &dir[1], st);
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+            e = la_scan(g.seg, a.H, a.dk * a.dv, i == 1, w.seg[i], w.tot[i], first[i], last[i], st, 1);
+        if (e != cudaSuccess) return e;
+    } else if (a.cu && a.ds0) {
+        const long long HE = (long long)a.H * a.dk * a.dv;
+        la_empty_kernel<<<dim3(a.B, (unsigned)min((HE + 1023) / 1024, 64LL)), 256, 0, st>>>(g.seg, HE, a.dsT, a.ds0);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    // the chunks' states: forward, then from the end (which meets the forward ones for dg)
+    for (int i = 0; i < 2; ++i) {
+        TcArgs &s = dir[i];
+        s.fin = nullptr;
+        s.fin_tot = nullptr;
+        s.init = w.seg[i];
+        s.first = first[i];
+        s.last = last[i];
         s.hi = w.hi[i];
         s.lo = w.lo[i];
-        if (s.back && a.dg) {
+        if (i == 1 && a.dg) {
             s.phi = w.hi[0];
             s.plo = w.lo[0];
             s.dot = w.dot;
         }
-        e = DK == 64 ? launch_state<64>(x, y, hi, lo, s, st) : launch_state<128>(x, y, hi, lo, s, st);
+        e = launch_states(xy + 2 * i, &m[4 + 2 * i], s, nullptr, st);
         if (e != cudaSuccess) return e;
     }
     BackArgs b{};
@@ -1985,8 +1995,7 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     b.tiles = g.tiles;
     if (DK == 64) e = DV == 64 ? launch_back<64, 64>(m, b, (int)n, st) : launch_back<64, 128>(m, b, (int)n, st);
     else e = DV == 64 ? launch_back<128, 64>(m, b, (int)n, st) : launch_back<128, 128>(m, b, (int)n, st);
-    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, a.dq, a.dtype, g.ch, a, st);
-    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pk, a.dk_, a.dtype, g.ch, a, st);
+    if (e == cudaSuccess && w.pq) e = la_share_sum(w.pq, w.pk, g.ch, a, st);
     if (e == cudaSuccess && a.dg && a.per_head) e = la_head_sum(w.dgc, a.dg, g.ch, a.H, st);
     return e;
 }
