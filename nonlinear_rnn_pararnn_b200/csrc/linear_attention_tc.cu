@@ -1353,13 +1353,14 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 }
             };
             const uint32_t sm = smem_u32(smem), sx0 = smem_u32(x0), sx1 = smem_u32(x1);
-            int it = 0;
+            int it = 0, ragged = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
                 const uint32_t ph = (uint32_t)it & 1u;
                 if (!lane_wait(&full1, ph, &s_abort)) break;
-                if (packed) {
+                if (packed && la_chunk(g.ch, item / a.H).len < TCC) {
                     // rows behind a ragged chunk are cleared before they are read
-                    if (!lane_wait(&tready, ph, &s_abort)) break;
+                    if (!lane_wait(&tready, (uint32_t)ragged & 1u, &s_abort)) break;
+                    ++ragged;
                 }
                 if (it > 0 && !lane_wait(&tfree, ph ^ 1u, &s_abort)) break;
                 tc_fence_after();
@@ -1490,7 +1491,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             const uint32_t ph = (uint32_t)it & 1u;
             h = item % a.H;
             ck = la_chunk(g.ch, item / a.H);
-            if (packed) {
+            if (packed && ck.len < TCC) {
                 ok = warp_wait(&full1, ph, &s_abort) && warp_wait(&full2, ph, &s_abort);
                 if (!ok) break;
                 if (r >= ck.len)
