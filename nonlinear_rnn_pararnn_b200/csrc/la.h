@@ -4,6 +4,8 @@
 // slstm_api.cu.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -69,6 +71,22 @@ size_t la_tc_forward_workspace(const LaArgs &a);
 cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st);
 size_t la_tc_backward_workspace(const LaArgs &a);
 cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st);
+
+// Lets kernel F have `bytes` of dynamic shared memory; asks the runtime once for
+// each device.
+template <auto *F>
+cudaError_t la_allow_shared(int bytes)
+{
+    static std::atomic<unsigned long long> asked{0ull};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (asked.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(F, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) asked.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Sums of the fp32 per-head partial gradients over the heads that share a query
 // and key head, into a.dq and a.dk_: dq[row][hq][d] = sum over r of

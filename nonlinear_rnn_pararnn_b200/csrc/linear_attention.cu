@@ -51,7 +51,10 @@ SLSTM_DEVINL float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 SLSTM_DEVINL void put(float *p, float v) { *p = v; }
 SLSTM_DEVINL void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-SLSTM_DEVINL long long la_rows(const LaArgs &a) { return a.cu ? (long long)a.T : (long long)a.B * a.T; }
+[[maybe_unused]] SLSTM_DEVINL long long la_rows(const LaArgs &a)
+{
+    return a.cu ? (long long)a.T : (long long)a.B * a.T;
+}
 
 // An operand of a 64 x 64 product: element (m, k) at p[m sm + k sk] for
 // m < nm, k < nk, zero outside, times coef[k] where given.
@@ -778,8 +781,7 @@ cudaError_t backward(const LaArgs &a, const LaChunks &ch, const SimtWs &w, cudaS
     cudaError_t e = states<T, RT>(a, ch, false, w.S, w.totS, st);
     if (e == cudaSuccess) e = states<T, RT>(a, ch, true, w.dS, w.totD, st);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(la_back_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(BackShared));
+        e = la_allow_shared<la_back_kernel<T, RT>>((int)sizeof(BackShared));
     if (e != cudaSuccess) return e;
     la_back_kernel<T, RT><<<(unsigned)ch.total * a.H, nt<RT>(), sizeof(BackShared), st>>>(a, ch, w.S, w.dS, w.pq, w.pk,
                                                                                        w.dgc);

@@ -1778,7 +1778,7 @@ cudaError_t launch_state(const CUtensorMap *xy, const CUtensorMap *hilo, const T
                          cudaStream_t st)
 {
     const int bytes = StateShared<DK>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(la_state_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = la_allow_shared<la_state_kernel<DK>>(bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, g1 ? 2 : 1);
     la_state_kernel<DK><<<grid, STATE_THREADS, bytes, st>>>(xy[0], xy[1], xy[g1 ? 2 : 0], xy[g1 ? 3 : 1], hilo[0],
@@ -1796,7 +1796,7 @@ template <int DK>
 cudaError_t launch_forward(const CUtensorMap *m, const TcArgs &g, cudaStream_t st)
 {
     const int bytes = FwdShared<DK>::BYTES;
-    cudaError_t e = cudaFuncSetAttribute(la_forward_kernel<DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = la_allow_shared<la_forward_kernel<DK>>(bytes);
     if (e != cudaSuccess) return e;
     la_forward_kernel<DK>
         <<<(unsigned)g.seg.total * g.a.H * g.tiles, FWD_THREADS, bytes, st>>>(m[0], m[1], m[2], g);
@@ -1864,8 +1864,7 @@ template <int DK, int DV>
 cudaError_t launch_back(const CUtensorMap *m, const BackArgs &g, int items, cudaStream_t st)
 {
     const int bytes = BackShared<DK, DV>::BYTES;
-    cudaError_t e =
-        cudaFuncSetAttribute(la_backward_kernel<DK, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = la_allow_shared<la_backward_kernel<DK, DV>>(bytes);
     if (e != cudaSuccess) return e;
     la_backward_kernel<DK, DV><<<min(items, 148), BACK_THREADS, bytes, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6],
                                                                            m[7], g);
