@@ -23,7 +23,9 @@
 // All products are fp32 fused multiply-adds over 64 x 64 tiles (RT x 4 for each
 // of 1024 / RT threads), the next 32 of the depth on their way from memory
 // meanwhile; fp32 in, fp32 out needs that, and sizes that are no multiple
-// of 8 come here too.  Bound: the FMA pipes.
+// of 8 come here too.  Bound: the FMA pipes, of
+// which the gradients of 8 x 1024 rows, 4 heads of 64, keep a third busy (fetching
+// instructions and operands the rest of the time).
 #include <cuda_bf16.h>
 
 #define SLSTM_FILE_ID 11
@@ -40,7 +42,7 @@ constexpr int LDT = 68;       // padded row of a tile (floats)
 // Rows of a thread's tile.  8: 128 threads, the fewest reads of shared memory for
 // a multiply-add, where the blocks fill the GPU; 4: 256 threads, twice the warps
 // to hide the latencies behind, where they do not (2 x 777 rows, 4 heads of 64:
-// 25 and 40 us; 8 x 1024 rows, both passes: 205 and 150).
+// 25 and 40 us; gradients of 8 x 1024 rows: 200 and 127).
 template <int RT>
 constexpr int nt() { return 1024 / RT; }
 template <int RT>
