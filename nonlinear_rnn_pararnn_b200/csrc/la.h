@@ -49,13 +49,15 @@ struct LaChunks {
     int nc;                   // dense: chunks of a sequence
     int total;                // an upper bound of the chunks (dense: the number)
     const int *pos, *coff;    // packed: [n_seq + 1] each; else null
+    const int *order;         // packed, where asked for: the chunks, long ones first; else null
 };
 size_t la_table_bytes(const LaArgs &a);
 int la_chunk_bound(const LaArgs &a, int C);
+size_t la_order_bytes(const LaArgs &a, int C);   // of the order of chunks of C rows
 // Fill the table (packed) at `mem` on `st`; with out2, a second one for chunks of
-// C2 rows at mem2 in the same launch.
+// C2 rows at mem2 in the same launch, its order at `order` (la_order_bytes).
 cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st, int C2 = 0,
-                      void *mem2 = nullptr, LaChunks *out2 = nullptr);
+                      void *mem2 = nullptr, LaChunks *out2 = nullptr, void *order = nullptr);
 
 // The states over the chunks (or segments) of each sequence, elementwise: the
 // E-element deltas in buf[chunk][h], with the decays tot[chunk][h], give way to

@@ -603,9 +603,11 @@ __global__ void __launch_bounds__(256) la_head_sum_kernel(const float *__restric
 
 // The table of packed sequences: offsets clamped into [0, T] and raised to the
 // largest before them, and the chunks before each sequence.  One block a table,
-// 1024 offsets at a time.
+// 1024 offsets at a time.  The second table's chunks are also put in an order,
+// long ones first (by 64 classes of length; within one, as it comes): blocks take
+// them in that order, and what is left for the last SMs is short.
 __global__ void __launch_bounds__(1024) la_table_kernel(const int *__restrict__ cu, int n_seq, int T, int C, int *pos,
-                                                        int *coff, int C2, int *pos2, int *coff2)
+                                                        int *coff, int C2, int *pos2, int *coff2, int *order)
 {
     if (blockIdx.x == 1) {
         C = C2;
@@ -649,6 +651,22 @@ __global__ void __launch_bounds__(1024) la_table_kernel(const int *__restrict__ 
         for (int w = 0; w < 32; ++w) sum += ws[w];
         __syncthreads();
     }
+    if (blockIdx.x == 0 || order == nullptr) return;
+    __shared__ int at[64];
+    const LaChunks t{n_seq, T, C, 0, 0, pos, coff, nullptr};
+    auto kind = [&](int i) { return 63 - (int)((long long)(la_chunk(t, i).len - 1) * 64 / C); };
+    if (threadIdx.x < 64) at[threadIdx.x] = 0;
+    __syncthreads();   // the table is written, too
+    for (int i = threadIdx.x; i < sum; i += 1024) atomicAdd(&at[kind(i)], 1);
+    __syncthreads();
+    if (threadIdx.x == 0)
+        for (int k = 0, n = 0; k < 64; ++k) {
+            const int m = at[k];
+            at[k] = n;
+            n += m;
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < sum; i += 1024) order[atomicAdd(&at[kind(i)], 1)] = i;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -662,22 +680,26 @@ int la_chunk_bound(const LaArgs &a, int C)
     return a.cu ? a.T / C + a.B : a.B * ((a.T - 1) / C + 1);
 }
 
+size_t la_order_bytes(const LaArgs &a, int C) { return a.cu ? up256(4 * (size_t)la_chunk_bound(a, C)) : 0; }
+
 cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStream_t st, int C2, void *mem2,
-                      LaChunks *out2)
+                      LaChunks *out2, void *order)
 {
     int *tab[2][2] = {};
     for (int i = 0; i < 2; ++i) {
         LaChunks *o = i ? out2 : out;
         if (o == nullptr) break;
         const int c = i ? C2 : C;
-        *o = LaChunks{a.B, a.T, c, (a.T - 1) / c + 1, la_chunk_bound(a, c), nullptr, nullptr};
+        *o = LaChunks{a.B, a.T, c, (a.T - 1) / c + 1, la_chunk_bound(a, c), nullptr, nullptr, nullptr};
         if (a.cu == nullptr) continue;
         char *p = static_cast<char *>(i ? mem2 : mem);
         o->pos = tab[i][0] = reinterpret_cast<int *>(p);
         o->coff = tab[i][1] = reinterpret_cast<int *>(p + up256(4 * ((size_t)a.B + 1)));
     }
     if (a.cu == nullptr) return cudaSuccess;
-    la_table_kernel<<<out2 ? 2 : 1, 1024, 0, st>>>(a.cu, a.B, a.T, C, tab[0][0], tab[0][1], C2, tab[1][0], tab[1][1]);
+    if (out2) out2->order = static_cast<int *>(order);
+    la_table_kernel<<<out2 ? 2 : 1, 1024, 0, st>>>(a.cu, a.B, a.T, C, tab[0][0], tab[0][1], C2, tab[1][0], tab[1][1],
+                                                   static_cast<int *>(order));
     return cudaGetLastError();
 }
 

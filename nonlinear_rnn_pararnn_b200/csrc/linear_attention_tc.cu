@@ -351,16 +351,20 @@ SLSTM_DEVINL void zero_row(uint8_t *box, int t)
 // Where a segment lies.
 struct Seg {
     int seq, nch, len;        // sequence, chunks, rows
+    int item;                 // its index
     long long row;            // first row
     int t, b;                 // TMA coordinates of the first row
     long long c0;             // index of its first chunk
     bool only;                // the sequence is one segment
 };
 
+// The i-th segment in the order in which the blocks take them.
 SLSTM_DEVINL bool seg_of(const TcArgs &g, int i, Seg *s)
 {
+    if (g.seg.pos && i >= g.seg.coff[g.seg.n_seq]) return false;
+    i = g.seg.order ? g.seg.order[i] : i;
     const LaChunk c = la_chunk(g.seg, i);
-    if (c.len <= 0) return false;
+    s->item = i;
     s->seq = c.seq;
     s->len = c.len;
     s->nch = (c.len + TCC - 1) / TCC;
@@ -633,7 +637,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         typedef Share<DK> SH;
         const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
         const long long E = (long long)a.dk * a.dv;
-        const float *src = g.init && !sg.only ? g.init + ((long long)item * a.H + h) * E
+        const float *src = g.init && !sg.only ? g.init + ((long long)sg.item * a.H + h) * E
                                               : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E
                                                          : nullptr);
         float S[SH::N];
@@ -683,10 +687,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                     for (int i = 0; i < SH::N && col + i < a.dv; ++i)
                         g.hi[((sg.c0 + n) * a.H + h) * E + (long long)r * a.dv + col + i] = __float2bfloat16(S[0]);
         }
-        float *dst = g.fin ? g.fin + ((long long)item * a.H + h) * E
+        float *dst = g.fin ? g.fin + ((long long)sg.item * a.H + h) * E
                            : (g.last && sg.only ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
         if (dst) state_store(S, dst, a.dk, a.dv, r, col);
-        if (g.fin && tile == 0 && threadIdx.x == 0) g.fin_tot[(long long)item * a.H + h] = run;
+        if (g.fin && tile == 0 && threadIdx.x == 0) g.fin_tot[(long long)sg.item * a.H + h] = run;
     }
     tc_fence_before();
     __syncthreads();
@@ -930,7 +934,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         typedef Share<DK> SH;
         const int r = SH::row(warp, lane), c0 = SH::col(warp), col = tile * 64 + c0;
         const long long E = (long long)a.dk * a.dv;
-        const float *src = g.init && !sg.only ? g.init + ((long long)item * a.H + h) * E
+        const float *src = g.init && !sg.only ? g.init + ((long long)sg.item * a.H + h) * E
                                               : (g.first ? g.first + ((long long)sg.seq * a.H + h) * E
                                                          : nullptr);
         float S[SH::N];
@@ -1739,7 +1743,7 @@ int seg_chunks(const LaArgs &a, int per_item)
 }
 
 struct FwdWs {
-    char *table, *seg_table;
+    char *table, *seg_table, *order;
     TcDecays *dec;
     float *states, *tot;
     size_t bytes;
@@ -1756,6 +1760,7 @@ FwdWs fwd_layout(const LaArgs &a, int L, void *ws)
     };
     w.table = take(la_table_bytes(a));
     w.seg_table = take(la_table_bytes(a));
+    w.order = take(la_order_bytes(a, L * TCC));
     w.dec = reinterpret_cast<TcDecays *>(take(sizeof(TcDecays) * la_chunk_bound(a, TCC) * a.H));
     if (L < (a.T - 1) / TCC + 1) {
         const size_t items = (size_t)la_chunk_bound(a, L * TCC);
@@ -1819,7 +1824,7 @@ bool state_map(CUtensorMap *m, const void *p, const LaArgs &a, long long n, int 
 }
 
 struct BackWs {
-    char *table, *seg_table;
+    char *table, *seg_table, *order;
     TcDecays *dec;
     float *seg[2], *tot[2];            // a segment's first states, forward and from the end
     __nv_bfloat16 *hi[2], *lo[2];      // the chunks' states
@@ -1840,6 +1845,7 @@ BackWs back_layout(const LaArgs &a, int L, void *ws)
     const size_t rows = a.cu ? (size_t)a.T : (size_t)a.B * a.T;
     w.table = take(la_table_bytes(a));
     w.seg_table = take(la_table_bytes(a));
+    w.order = take(la_order_bytes(a, L * TCC));
     w.dec = reinterpret_cast<TcDecays *>(take(sizeof(TcDecays) * n));
     for (int i = 0; i < 2; ++i) {
         if (L < (a.T - 1) / TCC + 1) {
@@ -1891,7 +1897,8 @@ cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st)
     g.tiles = (a.dv + 63) / 64;
     const int L = seg_chunks(a, a.H * g.tiles);
     const FwdWs w = fwd_layout(a, L, ws);
-    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg);
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg,
+                              w.order);
     if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
     g.dec = w.dec;
@@ -1933,7 +1940,8 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     const int L = seg_chunks(a, a.H * g.tiles);
     const BackWs w = back_layout(a, L, ws);
     const int DK = a.dk <= 64 ? 64 : 128, DV = a.dv <= 64 ? 64 : 128;
-    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg);
+    cudaError_t e = la_chunks(a, TCC, w.table, &g.ch, st, L * TCC, w.seg_table, &g.seg,
+                              w.order);
     if (e == cudaSuccess) e = launch_decays(a, g.ch, w.dec, st);
     if (e != cudaSuccess) return e;
     g.dec = w.dec;
