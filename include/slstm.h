@@ -646,6 +646,9 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
  *   g      fp32 log decays, (B, T, H) for SLSTM_DECAY_TOKEN or (H,) for
  *          SLSTM_DECAY_HEAD.  -inf (and anything below -87.3, whose factor is
  *          no normal fp32 number) clears the state before its token.
+ *          Positive ones, growth, are taken while they sum to less than 80 over
+ *          any 128 consecutive tokens (chunks are put together from powers that
+ *          leave fp32 beyond that).
  *   s0     (B, H, d_k, d_v) fp32 or NULL (zeros); sT likewise, the state after
  *          the last token, or NULL; sT may be s0
  *   o      (B, T, H, d_v) of `dtype`, contiguous
