@@ -4,12 +4,13 @@
 // products are 128 x 128 x d tiles.
 //
 // What needs how many bits: products of q, k, v and dO with one another are
-// exact in the fp32 accumulators.  The weights D (q k) are rounded to bf16
-// where they enter the product with v, as the outputs are.  The state is held
-// in fp32 registers; what is added to it, a row of v times its decay, is split
-// into two bf16 terms (2^-17 of it left), since the final state is an fp32
-// output.  Where the state enters a product for a bf16 output its upper term
-// does; for the gradient of the decay, an fp32 output, both do.
+// exact in the fp32 accumulators, and the state is held in fp32 registers.  What
+// else enters a product, the state, a row of v times its decay and the weights
+// D (q k) of the outputs, is split into two bf16 terms, which leave 2^-17 of it at
+// most, so that an output is rounded to bf16 once.  (In single bf16 terms the
+// outputs of 8 rows of 8192 steps are 2.35e-3 off in the 2-norm, 1.66e-3 of it
+// their own rounding, and the call takes 169 us instead of 186.)  The gradients'
+// weights are rounded to bf16, and the product k dS takes the upper term alone.
 //
 // Every mbarrier wait is bounded in time; on expiry the block marks itself,
 // waits (bounded) for its own loads and MMAs, writes NaN over its outputs,
@@ -302,15 +303,22 @@ __global__ void __launch_bounds__(256) la_decay_kernel(LaArgs a, LaChunks ch, Tc
     tc_decays(out[i], gv, threadIdx.x & 31);
 }
 
-// The two bf16 of x times w, as two bf16 terms each: the product rounded, and what
-// that leaves (2^-18 of it is lost, in fp32 the rest).
-SLSTM_DEVINL void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo)
+// Two numbers as two bf16 terms each: the number rounded, and what that leaves,
+// rounded (2^-17 of the number is lost at most).
+SLSTM_DEVINL void two_terms(float a, float b, uint32_t &hi, uint32_t &lo)
 {
-    float a, b, c, d;
-    mul2(a, b, lo_of(x), hi_of(x), w, w);
+    float c, d;
     hi = pack2(a, b);
     sub2(c, d, a, b, lo_of(hi), hi_of(hi));
     lo = pack2(c, d);
+}
+
+// The two bf16 of x times w, as two bf16 terms each.
+SLSTM_DEVINL void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo)
+{
+    float a, b;
+    mul2(a, b, lo_of(x), hi_of(x), w, w);
+    two_terms(a, b, hi, lo);
 }
 
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // The forward pass of a segment: one block walks the chunks of one head and 64
 // columns of v and does all of it while q, k and v are in shared memory, the
 // state in registers:
-//   warps 0-7   the state (lane = row of d_k), its upper term into shared memory
+//   warps 0-7   the state (lane = row of d_k), its two terms into shared memory
 //               and half of v times its decays as two bf16 terms
 //   warps 8-11  the other half
 //   warps 12-19 the weights D (q k) from tensor memory and back as bf16
@@ -728,7 +736,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // A chunk's products: q k^T (128 x 128; of the next chunk ahead of the last of
 // this one where its rows have come), k^T (w v), and into an accumulator each
 // q S, whose rows are scaled in fp32 as they are read, and D(q k) v with the
-// weights in tensor memory.
+// weights in tensor memory, in the place of their scores.
 // 8 rows of 8192 steps, 8 heads of 128: 160 us; reading and writing each tensor
 // once would take 84.  No one part of the work bounds it: with any of the
 // products, the weights, the loads or the stores left out it takes 93 % or more
@@ -759,7 +767,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready, sfree, pready[2], ofull, oempty, tready, drained,
+    __shared__ uint64_t yready, delta, sready, sfree, lready[2], pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_loaded;
@@ -785,8 +793,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         mbar_init(&delta, 1);
         mbar_init(&sready, 8);
         mbar_init(&sfree, 1);
-        mbar_init(&pready[0], 8);
-        mbar_init(&pready[1], 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&lready[i], 8);
+            mbar_init(&pready[i], 8);
+        }
         mbar_init(&ofull, 1);
         mbar_init(&oempty, 4);
         mbar_init(&tready, 4);
@@ -915,6 +925,18 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         umma_bf16(t_o, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
                 }
                 umma_commit(&sfree);
+                // the state's lower term has come to where k was
+                ok = lane_wait(&lready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ld = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), BOX);
+#pragma unroll
+                for (int i = 0; i < SM::NB; ++i) {
+                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16(t_o, qd + 2 * k, ld + (2048u >> 4) * (4 * i + k), id_o, 1u);
+                }
                 umma_commit(&empty[s]);
                 ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
                      lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
@@ -922,11 +944,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 tc_fence_after();
                 const uint32_t ta = tmem + ph * 128;
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k)
-                    umma_bf16_ta(t_o + 64, ta + 64 * (k / 4) + 8 * (k & 3), vd + (2048u >> 4) * k, id_o,
-                                 k > 0 ? 1u : 0u);
-                umma_commit(&ofull);
+                for (int k = 0; k < 8; ++k) {
+                    umma_bf16_ta(t_o + 64, ta + 16 * k, vd + (2048u >> 4) * k, id_o, k > 0 ? 1u : 0u);
+                    umma_bf16_ta(t_o + 64, ta + 16 * k + 8, vd + (2048u >> 4) * k, id_o, 1u);
+                }
                 umma_commit(&vempty[s]);
+                umma_commit(&ofull);
             }
             umma_commit(&fin);
         }
@@ -964,7 +987,24 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
             tma_store_fence();
             warp_arrive(&sready);
-            ok = warp_wait(&delta, ph, &s_abort) && (n + 1 >= nch || scale(n + 1));
+            // the lower term goes where the chunk's keys were, once both products
+            // that read them are done: there is no room for a buffer of its own
+            ok = warp_wait(&delta, ph, &s_abort) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
+            if (!ok) break;
+            uint8_t *low = smem + (n % NST) * SM::STAGE + SM::NB * BOX;
+            // (the upper terms are rounded again: kept over the waits they spill)
+#pragma unroll
+            for (int i = 0; i < SH::N; ++i) asm volatile("" : "+f"(S[i]));
+#pragma unroll
+            for (int i = 0; i < SH::N / 8; ++i) {
+                uint32_t y[4], z[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) two_terms(S[8 * i + 2 * j], S[8 * i + 2 * j + 1], y[j], z[j]);
+                *reinterpret_cast<uint4 *>(low + swz(r, c0 / 8 + i)) = make_uint4(z[0], z[1], z[2], z[3]);
+            }
+            tma_store_fence();
+            warp_arrive(&lready[ph]);
+            ok = n + 1 >= nch || scale(n + 1);
             if (!ok) break;
             tc_fence_after();
             state_add(S, dec[n % ND].tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
@@ -1007,7 +1047,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             if (!warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
             tc_fence_after();
             const TcDecays &d = dec[n % ND];
-            // 64 keys of this warp; their bf16 weights over the first half of their scores
+            // 64 keys of this warp; the two terms of 16 weights in the place of their scores
             const uint32_t sc = tmem + (n & 1) * 128 + 64 * half + la;
             const float ri = d.rq[i], li = d.loc[i];
             const int f = max(d.first[i] - 32 * q, 0);   // first key of its own 32 that reaches the query
@@ -1015,7 +1055,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll 1
             for (int z = 0; z < 4; ++z) {   // 16 keys at a time
                 const int b = 2 * half + (z >> 1), key = 64 * half + 16 * z;
-                uint32_t p[8];
+                uint32_t p[16];   // 8 columns of the upper terms, 8 of the lower
                 if (b <= q) {
                     float v[16];
                     tmem_ld16(sc + 16 * z, v);
@@ -1023,8 +1063,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 e = *reinterpret_cast<const float4 *>(&d.cq[q - 1][key + j]);
-                            p[j / 2] = pack2(v[j] * (ri * e.x), v[j + 1] * (ri * e.y));
-                            p[j / 2 + 1] = pack2(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w));
+                            two_terms(v[j] * (ri * e.x), v[j + 1] * (ri * e.y), p[j / 2], p[8 + j / 2]);
+                            two_terms(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w), p[j / 2 + 1], p[9 + j / 2]);
                         }
                     } else {
                         const int k0 = 16 * (z & 1) - f;
@@ -1036,15 +1076,15 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 x[k] = (uint32_t)(k0 + j + k) <= span ? v[j + k] * e[k] : 0.0f;
-                            p[j / 2] = pack2(x[0], x[1]);
-                            p[j / 2 + 1] = pack2(x[2], x[3]);
+                            two_terms(x[0], x[1], p[j / 2], p[8 + j / 2]);
+                            two_terms(x[2], x[3], p[j / 2 + 1], p[9 + j / 2]);
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) p[j] = 0u;
+                    for (int j = 0; j < 16; ++j) p[j] = 0u;
                 }
-                tmem_st8(sc + 8 * z, p);
+                tmem_st16(sc + 16 * z, p);
             }
             tmem_wait_st();
             tc_fence_before();
