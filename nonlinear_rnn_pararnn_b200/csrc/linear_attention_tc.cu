@@ -5,12 +5,12 @@
 //
 // What needs how many bits: products of q, k, v and dO with one another are
 // exact in the fp32 accumulators, and the state is held in fp32 registers.  What
-// else enters a product, the state, a row of v times its decay and the weights
-// D (q k) of the outputs, is split into two bf16 terms, which leave 2^-17 of it at
-// most, so that an output is rounded to bf16 once.  (In single bf16 terms the
-// outputs of 8 rows of 8192 steps are 2.35e-3 off in the 2-norm, 1.66e-3 of it
-// their own rounding, and the call takes 169 us instead of 186.)  The gradients'
-// weights are rounded to bf16, and the product k dS takes the upper term alone.
+// else enters a product, the states and their gradients, a row of v or dO times
+// its decay and the weights D (q k) and D (dO v), is split into two bf16 terms,
+// which leave 2^-17 of it at most, so that a bf16 output is rounded once.  (With
+// weights and q S, k dS in single terms, 8 rows of 8192 steps: o 2.35e-3 off in
+// the 2-norm, 1.66e-3 of it its own rounding; 169 us instead of 186 forward, 542
+// instead of 585 for the gradients.)
 //
 // Every mbarrier wait is bounded in time; on expiry the block marks itself,
 // waits (bounded) for its own loads and MMAs, writes NaN over its outputs,
@@ -1161,16 +1161,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 //   row and column sums of W = P (dO v) for dg;  then
 //   dq = Pd k + scale e^{c_i} dO S^T,   dk = Pd^T q + e^{c_C - c_j} v dS^T,
 //   dv = P^T dO + e^{c_C - c_j} k dS
-// with P^T and Pd^T in shared memory (Pd^T read both ways round).  The products
-// with the states come first; their rows are scaled in tensor memory, where the
-// other products are then added (dv's stay apart).  u_i and w_j of dg are the
-// dot products of q_i and k_j with those rows.
+// with two terms each of P^T in tensor memory and of Pd^T in shared memory (read
+// both ways round).  The products with the states come first; their rows are
+// scaled in tensor memory, where the other products are then added.  u_i and w_j
+// of dg are the dot products of q_i and k_j with those rows.
 //   warps 0-15  lane quarter q = warp & 3, columns 32 b .. of b = warp >> 2
 //   warp 16     loads;  warp 17 MMAs;  warp 18 dg
-// Tensor memory: [0, 128) q k^T, then k dS; [128, 256) dO v^T, then P^T dO;
+// Tensor memory: [0, 128) q k^T, then dv; [128, 256) dO v^T, then P^T;
 // [256, 384) dq; [384, 512) dk.  Shared memory holds q, k, v, dO and two 32 KB
-// buffers that take S, then dS, then P^T and Pd^T.  Bound: the bytes of q, k,
-// v, dO, the two states and the gradients.
+// buffers that take the terms of S, then of dS, then of Pd^T.  Bound: the bytes
+// of q, k, v, dO, the two states and the gradients.
 // ---------------------------------------------------------------------------
 struct BackArgs {
     LaArgs a;
@@ -1429,28 +1429,34 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 for (int i = 0; i < NK; ++i) {
                     const uint64_t ad = smem_desc_k_sw128(sm + SM::K + i * BOX);
                     const uint64_t bd = smem_desc_mn_sw128(sx0 + i * 64 * 128, SB);
+                    const uint64_t ld = smem_desc_mn_sw128(sx1 + i * 64 * 128, SB);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
                         umma_bf16(R0, ad + 2 * k, bd + (2048u >> 4) * k, id_kd, (i > 0 || k > 0) ? 1u : 0u);
+                        umma_bf16(R0, ad + 2 * k, ld + (2048u >> 4) * k, id_kd, 1u);
+                    }
                 }
                 umma_commit(&bx);
                 if (!lane_wait(&pready, ph, &s_abort)) break;
                 tc_fence_after();
                 const uint64_t gd = smem_desc_mn_sw128(sm + SM::G, BOX), qd = smem_desc_mn_sw128(sm + SM::Q, BOX),
-                               kd = smem_desc_mn_sw128(sm + SM::K, BOX), pdt = smem_desc_mn_sw128(sx1, BOX);
-#pragma unroll
+                               kd = smem_desc_mn_sw128(sm + SM::K, BOX);
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
-                    const uint64_t pt = smem_desc_k_sw128(sx0 + (k >> 2) * BOX) + 2 * (k & 3);
-                    umma_bf16(R1, pt, gd + (2048u >> 4) * k, id_kd, k > 0 ? 1u : 0u);
-                }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint64_t pt = smem_desc_k_sw128(sx1 + (k >> 2) * BOX) + 2 * (k & 3);
-                    umma_bf16(R3, pt, qd + (2048u >> 4) * k, id_dk, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k, gd + (2048u >> 4) * k, id_kd, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k + 8, gd + (2048u >> 4) * k, id_kd, 1u);
                 }
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k)
-                    umma_bf16(R2, pdt + (2048u >> 4) * k, kd + (2048u >> 4) * k, id_dq, 1u);
+                for (int t = 0; t < 2; ++t) {
+                    const uint32_t x = t ? sx1 : sx0;   // the terms of Pd^T
+                    const uint64_t pdt = smem_desc_mn_sw128(x, BOX);
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t pt = smem_desc_k_sw128(x + (k >> 2) * BOX) + 2 * (k & 3);
+                        umma_bf16(R3, pt, qd + (2048u >> 4) * k, id_dk, 1u);
+                        umma_bf16(R2, pdt + (2048u >> 4) * k, kd + (2048u >> 4) * k, id_dq, 1u);
+                    }
+                }
                 umma_commit(&bout);
             }
             umma_commit(&fin);
@@ -1548,7 +1554,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const TcDecays &d = dec[it & 1];
-            uint32_t p[16], pd[16];
+            uint32_t pd[16], pl[16];   // the two terms of Pd
             if (b >= q) {
                 float csum = 0.0f;
                 // e^{c_i - c_j}: column i, this thread's j
@@ -1557,6 +1563,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
 #pragma unroll
                 for (int z = 0; z < 32; z += 16) {
                     float s[16], t[16];
+                    uint32_t p[16];   // 8 columns of the upper terms of P, 8 of the lower
                     tmem_ld16x2(R0 + at + z, R1 + at + z, s, t);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
@@ -1585,11 +1592,12 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                             s[j + k] = off ? pp[k] * t[j + k] : 0.0f;
                             csum += s[j + k];
                         }
-                        p[(z + j) / 2] = pack2(pp[0], pp[1]);
-                        p[(z + j) / 2 + 1] = pack2(pp[2], pp[3]);
-                        pd[(z + j) / 2] = pack2(pq[0], pq[1]);
-                        pd[(z + j) / 2 + 1] = pack2(pq[2], pq[3]);
+                        two_terms(pp[0], pp[1], p[j / 2], p[8 + j / 2]);
+                        two_terms(pp[2], pp[3], p[j / 2 + 1], p[9 + j / 2]);
+                        two_terms(pq[0], pq[1], pd[(z + j) / 2], pl[(z + j) / 2]);
+                        two_terms(pq[2], pq[3], pd[(z + j) / 2 + 1], pl[(z + j) / 2 + 1]);
                     }
+                    tmem_st16(R1 + at + z, p);
                     // 16 columns summed over the lanes: each step halves the columns a lane holds
 #pragma unroll
                     for (int o = 8; o > 0; o >>= 1) {
@@ -1606,7 +1614,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 sums[4 + b][r] = csum;
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) p[j] = pd[j] = 0u;
+                for (int j = 0; j < 16; ++j) pd[j] = pl[j] = 0u;
+                tmem_st16(R1 + at, pd);
+                tmem_st16(R1 + at + 16, pd);
             }
             tc_fence_before();
             warp_arrive(&scfree);
@@ -1635,15 +1645,24 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 tmem_st32(R3 + at, v);
                 sums[12 + b][r] = dot_row(smem + SM::K, r, b, v);
             }
-            tmem_wait_st();
             ok = warp_wait(&bx, ph, &s_abort);
             if (!ok) break;
+            tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t o = (b >> 1) * BOX + swz(r, 4 * (b & 1) + k);
-                *reinterpret_cast<uint4 *>(x0 + o) = make_uint4(p[4 * k], p[4 * k + 1], p[4 * k + 2], p[4 * k + 3]);
-                *reinterpret_cast<uint4 *>(x1 + o) = make_uint4(pd[4 * k], pd[4 * k + 1], pd[4 * k + 2], pd[4 * k + 3]);
+                *reinterpret_cast<uint4 *>(x0 + o) = make_uint4(pd[4 * k], pd[4 * k + 1], pd[4 * k + 2], pd[4 * k + 3]);
+                *reinterpret_cast<uint4 *>(x1 + o) = make_uint4(pl[4 * k], pl[4 * k + 1], pl[4 * k + 2], pl[4 * k + 3]);
             }
+            // the states' part of dv
+            if (b < DV / 32) {
+                float v[32];
+                tmem_ld32(R0 + at, v);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= colr;
+                tmem_st32(R0 + at, v);
+            }
+            tmem_wait_st();
             tma_store_fence();
             tc_fence_before();
             warp_arrive(&pready);
@@ -1658,15 +1677,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             const long long ldv = (long long)a.H * a.dv;
             if (b < DV / 32) {
                 float v[32];
-                {
-                    float s[16], t[16];
-#pragma unroll
-                    for (int z = 0; z < 32; z += 16) {
-                        tmem_ld16x2(R0 + at + z, R1 + at + z, s, t);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[z + j] = fmaf(colr, s[j], t[j]);
-                    }
-                }
+                tmem_ld32(R0 + at, v);
                 put_rows(static_cast<__nv_bfloat16 *>(a.dv_) + row * ldv + (long long)h * a.dv + 32 * b, ldv, v,
                          a.dv - 32 * b, rows, stage, lane);
             }

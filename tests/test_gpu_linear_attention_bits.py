@@ -49,3 +49,12 @@ def test_outputs_and_states(B, T, Hqk, H, dk, dv, more, cuda_device):
     scale = dk ** -0.5
     want, size = _dense(x, scale)
     _within(_run(x, scale), want, size, T, dk, dv, H // Hqk)
+
+
+@pytest.mark.parametrize("B,T,Hqk,H,dk,dv,more", CASES)
+def test_gradients(B, T, Hqk, H, dk, dv, more, cuda_device):
+    x = _inputs((B, T), Hqk, H, dk, dv, BF16, 201 + T, **more)
+    scale = dk ** -0.5
+    want, size = _dense(x, scale)
+    got = _run(x, scale)
+    _within({n: got[n] for n in ("dq", "dk", "dv", "ds0")}, want, size, T, dk, dv, H // Hqk)
