@@ -32,18 +32,22 @@ constexpr uint64_t TC_WAIT_NS = 1000000000ull;
 constexpr int ND = 4;                        // chunks whose decays are held
 
 // The decays of a chunk.  D_ij = e^{c_i - c_j} of rows i in 32-row block q and
-// j in an earlier one is rq[i] cq[q - 1][j], by way of the block's first row
-// (both factors are at most 1 where nothing grows): one exponential a row and
-// three a column in place of one an element.  Inside a block it is the
-// exponential of loc[i] - loc[j].
+// j in an earlier one is rq[i] cq[q][j], by way of the block's first row (both
+// factors are at most 1 where nothing grows): one exponential a row and three a
+// column in place of one an element.  Inside a block it is the exponential of
+// c_i - c_j: c_i less that of the block's first row as a multiple of 1/16 (16 bits,
+// so that differences are exact) and a rest, as behind strong decays both numbers
+// are large and their difference is not.
 struct alignas(16) TcDecays {
-    float loc[TCC];       // c_i less that of the first row of its 32
-    int first[TCC];
+    float loc[TCC], rest[TCC];
     float row[TCC], col[TCC];
-    float rq[TCC];        // e^{loc}, 0 behind a row of the block that clears
-    uint32_t mask[TCC];   // rows of the row's 32 that it reaches: itself and those behind it, up to a clear
-    float cq[3][96];      // [q - 1][j], j < 32 q; 0 where the state is cleared after j, up to row 32 q
+    float rq[TCC];             // e^{loc}, 0 behind a row of the block that clears
+    uint32_t mask[TCC];        // rows of the row's 32 that it reaches: itself and those behind it, up to a clear
+    float cq_[192];            // cq(q)[j], j < 32 q; 0 where the state is cleared after j, up to row 32 q
+    signed char first[TCC];    // the last row up to this one that clears the state, or -1
     float tot;
+    SLSTM_DEVINL float *cq(int q) { return cq_ + 16 * q * (q - 1); }
+    SLSTM_DEVINL const float *cq(int q) const { return cq_ + 16 * q * (q - 1); }
 };
 static_assert(sizeof(TcDecays) % 16 == 0, "an array of them in shared memory, read 16 bytes at a time");
 
@@ -199,8 +203,7 @@ SLSTM_DEVINL void load_decays(float (&gv)[4], const LaArgs &a, long long row, in
 }
 
 // The decays of a chunk by one warp into `d` (la_decays for the fields there).
-// The sums run in 64 bits; what is left of them once the 32-row block's first
-// row is taken off is fp32.
+// The sums and their differences run in 64 bits.
 SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
 {
     constexpr uint32_t ALL = 0xffffffffu;
@@ -239,23 +242,23 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
     }
     const double base = __shfl_sync(ALL, c[0], lane & 24);   // of the block's first row
     const int b = 32 * (lane >> 3);
-    const float to_base = (float)base, to_end = (float)(all - base);
-    float to_q[3];
+    double to_q[3];
     int fq[3];
 #pragma unroll
     for (int q = 1; q < 4; ++q) {
-        to_q[q - 1] = (float)(__shfl_sync(ALL, c[0], 8 * q) - base);
+        to_q[q - 1] = __shfl_sync(ALL, c[0], 8 * q);
         fq[q - 1] = __shfl_sync(ALL, f[0], 8 * q);
     }
-    float loc[4], row[4], col[4], rq[4];
-    int4 fi;
+    float loc[4], rest[4], row[4], col[4], rq[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = lane * 4 + i;
-        loc[i] = (float)(c[i] - base);
-        row[i] = f[i] >= 0 ? 0.0f : ex2(to_base + loc[i]);
-        col[i] = allf > t ? 0.0f : ex2(to_end - loc[i]);
-        rq[i] = f[i] > b ? 0.0f : ex2(loc[i]);
+        const double x = c[i] - base;
+        loc[i] = rintf((float)x * 16.0f) * 0.0625f;
+        rest[i] = (float)(x - (double)loc[i]);
+        row[i] = f[i] >= 0 ? 0.0f : ex2((float)c[i]);
+        col[i] = allf > t ? 0.0f : ex2((float)(all - c[i]));
+        rq[i] = f[i] > b ? 0.0f : ex2((float)x);
     }
     // the block's rows that clear, then for each row the run up to the next of them
     uint32_t clears = 0u;
@@ -271,19 +274,20 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
         mk[i] = from & (next ? (next & (0u - next)) - 1u : ~0u);
     }
     *reinterpret_cast<uint4 *>(d.mask + lane * 4) = make_uint4(mk[0], mk[1], mk[2], mk[3]);
-    fi = make_int4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4 *>(d.loc + lane * 4) = make_float4(loc[0], loc[1], loc[2], loc[3]);
     *reinterpret_cast<float4 *>(d.row + lane * 4) = make_float4(row[0], row[1], row[2], row[3]);
     *reinterpret_cast<float4 *>(d.col + lane * 4) = make_float4(col[0], col[1], col[2], col[3]);
     *reinterpret_cast<float4 *>(d.rq + lane * 4) = make_float4(rq[0], rq[1], rq[2], rq[3]);
-    *reinterpret_cast<int4 *>(d.first + lane * 4) = fi;
+    *reinterpret_cast<float4 *>(d.rest + lane * 4) = make_float4(rest[0], rest[1], rest[2], rest[3]);
+    *reinterpret_cast<char4 *>(d.first + lane * 4) =
+        make_char4((signed char)f[0], (signed char)f[1], (signed char)f[2], (signed char)f[3]);
 #pragma unroll
     for (int q = 1; q < 4; ++q)
         if (b < 32 * q) {
             float e[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = fq[q - 1] > lane * 4 + i ? 0.0f : ex2(to_q[q - 1] - loc[i]);
-            *reinterpret_cast<float4 *>(&d.cq[q - 1][lane * 4]) = make_float4(e[0], e[1], e[2], e[3]);
+            for (int i = 0; i < 4; ++i) e[i] = fq[q - 1] > lane * 4 + i ? 0.0f : ex2((float)(to_q[q - 1] - c[i]));
+            *reinterpret_cast<float4 *>(d.cq(q) + lane * 4) = make_float4(e[0], e[1], e[2], e[3]);
         }
     if (lane == 0) d.tot = allf >= 0 ? 0.0f : ex2((float)all);
 }
@@ -1049,7 +1053,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             const TcDecays &d = dec[n % ND];
             // 64 keys of this warp; the two terms of 16 weights in the place of their scores
             const uint32_t sc = tmem + (n & 1) * 128 + 64 * half + la;
-            const float ri = d.rq[i], li = d.loc[i];
+            const float ri = d.rq[i], li = d.loc[i], mi = d.rest[i];
             const int f = max(d.first[i] - 32 * q, 0);   // first key of its own 32 that reaches the query
             const uint32_t span = (uint32_t)(lane - f);
 #pragma unroll 1
@@ -1062,7 +1066,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     if (b < q) {
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
-                            const float4 e = *reinterpret_cast<const float4 *>(&d.cq[q - 1][key + j]);
+                            const float4 e = *reinterpret_cast<const float4 *>(d.cq(q) + key + j);
                             two_terms(v[j] * (ri * e.x), v[j + 1] * (ri * e.y), p[j / 2], p[8 + j / 2]);
                             two_terms(v[j + 2] * (ri * e.z), v[j + 3] * (ri * e.w), p[j / 2 + 1], p[9 + j / 2]);
                         }
@@ -1071,7 +1075,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 16; j += 4) {
                             const float4 l = *reinterpret_cast<const float4 *>(&d.loc[key + j]);
-                            const float e[4] = {ex2(li - l.x), ex2(li - l.y), ex2(li - l.z), ex2(li - l.w)};
+                            const float4 m = *reinterpret_cast<const float4 *>(&d.rest[key + j]);
+                            const float e[4] = {ex2((li - l.x) + (mi - m.x)), ex2((li - l.y) + (mi - m.y)),
+                                                ex2((li - l.z) + (mi - m.z)), ex2((li - l.w) + (mi - m.w))};
                             float x[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
@@ -1558,7 +1564,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             if (b >= q) {
                 float csum = 0.0f;
                 // e^{c_i - c_j}: column i, this thread's j
-                const float cj = b > q ? d.cq[b > q ? b - 1 : 0][r] * a.scale : 0.0f, lj = d.loc[r];
+                const float cj = b > q ? d.cq(b)[r] * a.scale : 0.0f, lj = d.loc[r], mj = d.rest[r];
                 const uint32_t mask = d.mask[r];
 #pragma unroll
                 for (int z = 0; z < 32; z += 16) {
@@ -1576,10 +1582,11 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                             w[3] = cj * e.w;
                         } else {
                             const float4 l = *reinterpret_cast<const float4 *>(&d.loc[32 * b + z + j]);
-                            w[0] = ex2(l.x - lj) * a.scale;
-                            w[1] = ex2(l.y - lj) * a.scale;
-                            w[2] = ex2(l.z - lj) * a.scale;
-                            w[3] = ex2(l.w - lj) * a.scale;
+                            const float4 m = *reinterpret_cast<const float4 *>(&d.rest[32 * b + z + j]);
+                            w[0] = ex2((l.x - lj) + (m.x - mj)) * a.scale;
+                            w[1] = ex2((l.y - lj) + (m.y - mj)) * a.scale;
+                            w[2] = ex2((l.z - lj) + (m.z - mj)) * a.scale;
+                            w[3] = ex2((l.w - lj) + (m.w - mj)) * a.scale;
                         }
                         float pp[4], pq[4];
 #pragma unroll

@@ -58,3 +58,23 @@ def test_gradients(B, T, Hqk, H, dk, dv, more, cuda_device):
     want, size = _dense(x, scale)
     got = _run(x, scale)
     _within({n: got[n] for n in ("dq", "dk", "dv", "ds0")}, want, size, T, dk, dv, H // Hqk)
+
+
+@pytest.mark.parametrize("strong,times", [(-80.0, 20), (-40.0, 10), (-20.0, 16), (-87.0, 31)])
+@pytest.mark.parametrize("block", [0, 1, 3])
+def test_behind_strong_decays(strong, times, block, cuda_device):
+    """Strong decays that clear nothing, in front of mild ones in the same 32 tokens: the sums of the log decays
+    are large there, and the weights come from their differences."""
+    T = 128
+    x = _inputs((2, T), 1, 2, 64, 64, BF16, 300 + times)
+    x["g"] = x["g"] * 0.25
+    x["g"][:, 32 * block:32 * block + times] = strong
+    want, size = _dense(x, 0.125)
+    got = _run(x, 0.125)
+    if block == 3:
+        # the states are sums over the n tokens behind the strong ones: a row of v in two terms, the roundings of
+        # the sum, the exponentials of numbers below 16
+        n = T - 96 - times
+        off = float((got["sT"].double() - want["sT"]).norm() / want["sT"].norm())
+        assert off <= 2.0 ** -17 + (n + 16 + 8) * 2.0 ** -24, off
+    _within(got, want, size, T, 64, 64, 2)
