@@ -877,7 +877,8 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, cons
     const T *q = static_cast<const T *>(a.q) + b * a.ldq + (long long)hq * a.dk;
     const T *k = static_cast<const T *>(a.k) + b * a.ldk + (long long)hq * a.dk;
     const T *v = static_cast<const T *>(a.v) + b * a.ldv + (long long)h * a.dv;
-    const float decay = expf(a.g[a.per_head ? h : (long long)b * a.H + h]);
+    const float g = a.g[a.per_head ? h : (long long)b * a.H + h], decay = expf(g);
+    if (la_clears(g)) s_prev = nullptr;   // not times zero: what is cleared may be infinite or no number
     const long long base = ((long long)b * a.H + h) * a.dk * a.dv;
     float o[VEC], vv[VEC];
 #pragma unroll
