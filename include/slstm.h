@@ -645,7 +645,8 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
  *          and consecutive sequences T tokens
  *   g      fp32 log decays, (B, T, H) for SLSTM_DECAY_TOKEN or (H,) for
  *          SLSTM_DECAY_HEAD.  -inf (and anything below -87.3, whose factor is
- *          no normal fp32 number) clears the state before its token.
+ *          no normal fp32 number) clears the state before its token, whatever
+ *          the state holds.
  *          Positive ones, growth, are taken while they sum to less than 80 over
  *          any 128 consecutive tokens (chunks are put together from powers that
  *          leave fp32 beyond that).

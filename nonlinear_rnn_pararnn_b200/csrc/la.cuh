@@ -48,13 +48,17 @@ SLSTM_DEVINL LaChunk la_chunk(const LaChunks &t, int c)
 // neither -inf nor a large finite value spoils the differences of the others.
 SLSTM_DEVINL bool la_clears(float g) { return g < -87.3f; }
 
+// What a state becomes over a chunk: tot s + delta, or delta alone where the
+// chunk clears it (tot < 0), since zero times what is cleared need not be zero.
+SLSTM_DEVINL float la_carry(float tot, float s, float delta) { return tot < 0.0f ? delta : fmaf(tot, s, delta); }
+
 // The decays inside a chunk of C = 32 P rows, by one warp; lane l holds rows
 // P l .. P l + P - 1.  With c_i the sum of log2 decays up to and with row i:
 //   cum[i]    c_i in 64 bits (differences of far rows stay exact)
 //   first[i]  the last row <= i that clears the state, or -1
 //   row[i]    e^{c_i}: from the state that enters to row i (0 behind a clear)
 //   col[j]    e^{c_C - c_j}: from row j to the state that leaves (0 before one)
-//   *tot      e^{c_C}
+//   *tot      e^{c_C}, or -1 where a row clears (la_carry)
 // Rows behind `len` decay nothing.
 template <int P>
 SLSTM_DEVINL void la_decays(const float *g, long long g0, int gstride, int len, int lane, double *cum, int *first,
@@ -102,7 +106,7 @@ SLSTM_DEVINL void la_decays(const float *g, long long g0, int gstride, int len, 
         row[t] = fi >= 0 ? 0.0f : exp2f((float)c);
         col[t] = allf > t ? 0.0f : exp2f((float)(all - c));
     }
-    if (lane == 0) *tot = allf >= 0 ? 0.0f : exp2f((float)all);
+    if (lane == 0) *tot = allf >= 0 ? -1.0f : exp2f((float)all);
 }
 
 }  // namespace slstm

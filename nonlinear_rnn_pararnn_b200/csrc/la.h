@@ -60,8 +60,8 @@ cudaError_t la_chunks(const LaArgs &a, int C, void *mem, LaChunks *out, cudaStre
                       void *mem2 = nullptr, LaChunks *out2 = nullptr, void *order = nullptr);
 
 // The states over the chunks (or segments) of each sequence, elementwise: the
-// E-element deltas in buf[chunk][h], with the decays tot[chunk][h], give way to
-// the state that enters each (back: the gradient of the one that leaves it),
+// E-element deltas in buf[chunk][h], with the decays tot[chunk][h] (negative: the
+// state is cleared), give way to the state that enters each (back: the gradient of the one that leaves it),
 // starting from first[sequence][h] (null: zero); the last one to `last` (or
 // null).  Sequences of `skip` chunks are left alone.
 cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, const float *tot, const float *first,

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
             if (i0 + i < n) {
                 store(p + i * step, s);
 #pragma unroll
-                for (int k = 0; k < V; ++k) s[k] = fmaf(tt[i], s[k], dl[i][k]);
+                for (int k = 0; k < V; ++k) s[k] = la_carry(tt[i], s[k], dl[i][k]);
             }
     }
     if (last) store(last + at, s);
@@ -332,8 +332,9 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2)
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const float r = d.row[ty * RT + i];
+            const bool on = d.first[ty * RT + i] < 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] *= r;
+            for (int j = 0; j < 4; ++j) acc[i][j] = on ? acc[i][j] * r : 0.0f;
         }
         product(acc, Op<float>{&P[0][0], LC + 1, 1, LC, ck.len, nullptr},
                 Op<T>{v + n0, 1, a.ldv, a.dv - n0, ck.len, nullptr}, ck.len, sA, sB);
@@ -426,11 +427,12 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
         for (int i = 0; i < RT; ++i) {
             const int r = ty * RT + i;
             const float f = a.scale * s.d.row[r];
+            const bool on = s.d.first[r] < 0;
             float u = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = n0 + tx * 4 + j;
-                p[i][j] *= f;
+                p[i][j] = on ? p[i][j] * f : 0.0f;
                 if (r < len && n < a.dk) u = fmaf(to_f(q[r * a.ldq + n]), p[i][j], u);
             }
             u = sum16(u);
@@ -445,11 +447,12 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
         for (int i = 0; i < RT; ++i) {
             const int r = ty * RT + i;
             const float f = s.d.col[r];
+            const bool on = s.d.first[LC - 1] <= r;
             float w = 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = n0 + tx * 4 + j;
-                t[i][j] *= f;
+                t[i][j] = on ? t[i][j] * f : 0.0f;
                 if (r < len && n < a.dk) w = fmaf(to_f(k[r * a.ldk + n]), t[i][j], w);
             }
             w = sum16(w);
@@ -481,8 +484,9 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const float f = s.d.col[ty * RT + i];
+            const bool on = s.d.first[LC - 1] <= ty * RT + i;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[i][j] *= f;
+            for (int j = 0; j < 4; ++j) t[i][j] = on ? t[i][j] * f : 0.0f;
         }
         product(t, Op<float>{&s.P[0][0], 1, LC + 1, LC, len, nullptr},
                 Op<T>{g + n0, 1, ldo, a.dv - n0, len, nullptr}, len, s.sA, s.sB);
@@ -507,7 +511,7 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
     const int lane = threadIdx.x;
     dot = 0.0f;
     for (int i = 0; i < nt<RT>() / 32; ++i) dot += s.red[i];
-    dot *= s.d.tot;
+    dot = s.d.tot < 0.0f ? 0.0f : dot * s.d.tot;
     // two rows a lane; sums of up to 64 terms, in 64 bits: they cancel
     double x[2], w[2];
 #pragma unroll
@@ -519,14 +523,16 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
         w[i] = s.w[r];
     }
     double xs = x[0] + x[1], ws = w[0] + w[1];
-    const double xl = xs, wl = ws;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double xu = __shfl_down_sync(0xffffffffu, xs, o), wu = __shfl_up_sync(0xffffffffu, ws, o);
         if (lane + o < 32) xs += xu;
         if (lane >= o) ws += wu;
     }
-    const double xa = xs - xl, wb = ws - wl;   // rows behind, rows before this lane's
+    // rows behind, rows before this lane's (no differences: a sum may be no number)
+    double xa = __shfl_down_sync(0xffffffffu, xs, 1), wb = __shfl_up_sync(0xffffffffu, ws, 1);
+    if (lane == 31) xa = 0.0;
+    if (lane == 0) wb = 0.0;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

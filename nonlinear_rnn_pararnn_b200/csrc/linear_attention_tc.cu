@@ -45,7 +45,7 @@ struct alignas(16) TcDecays {
     uint32_t mask[TCC];        // rows of the row's 32 that it reaches: itself and those behind it, up to a clear
     float cq_[192];            // cq(q)[j], j < 32 q; 0 where the state is cleared after j, up to row 32 q
     signed char first[TCC];    // the last row up to this one that clears the state, or -1
-    float tot;
+    float tot;                 // e^{c_C}, or -1 where a row clears
     SLSTM_DEVINL float *cq(int q) { return cq_ + 16 * q * (q - 1); }
     SLSTM_DEVINL const float *cq(int q) const { return cq_ + 16 * q * (q - 1); }
 };
@@ -63,7 +63,7 @@ struct TcArgs {
     const float *init;        // entry states [segment][h] of sequences of several segments
     const float *first;       // entry states [sequence][h] (null: zero) of the others
     float *fin;               // the pass for `init`: final states [segment][h], of several segments
-    float *fin_tot;           // [segment][h] decay of a segment
+    float *fin_tot;           // [segment][h] decay of a segment (-1: it clears)
     float *last;              // final states [sequence][h] of one segment, or null
     __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
     const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
@@ -289,7 +289,7 @@ SLSTM_DEVINL void tc_decays(TcDecays &d, const float (&gv)[4], int lane)
             for (int i = 0; i < 4; ++i) e[i] = fq[q - 1] > lane * 4 + i ? 0.0f : ex2((float)(to_q[q - 1] - c[i]));
             *reinterpret_cast<float4 *>(d.cq(q) + lane * 4) = make_float4(e[0], e[1], e[2], e[3]);
         }
-    if (lane == 0) d.tot = allf >= 0 ? 0.0f : ex2((float)all);
+    if (lane == 0) d.tot = allf >= 0 ? -1.0f : ex2((float)all);
 }
 
 // The decays of every chunk and head, [chunk][h], a warp each: about 250
@@ -400,7 +400,8 @@ struct Share {
     SLSTM_DEVINL static int col(int warp) { return 32 * (warp >> 2) + (DK == 128 ? 0 : 16 * ((warp >> 1) & 1)); }
 };
 
-// S <- tot S + the sum of the two accumulators at `at` and 64 columns on.
+// S <- tot S (nothing where it is cleared) + the sum of the two accumulators at
+// `at` and 64 columns on.
 template <int N>
 SLSTM_DEVINL void state_add(float (&S)[N], float tot, uint32_t at)
 {
@@ -409,7 +410,7 @@ SLSTM_DEVINL void state_add(float (&S)[N], float tot, uint32_t at)
         float v[16], w[16];
         tmem_ld16x2(at + z, at + 64 + z, v, w);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[z + i] = fmaf(tot, S[z + i], v[i] + w[i]);
+        for (int i = 0; i < 16; ++i) S[z + i] = la_carry(tot, S[z + i], v[i] + w[i]);
     }
 }
 
@@ -685,7 +686,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             }
             tc_fence_after();
             const float tot = dec[n % ND].tot;
-            run *= tot;
+            run = run < 0.0f || tot < 0.0f ? -1.0f : run * tot;
             state_add(S, tot, tmem + (n & 1) * 128 + c0 + ((uint32_t)((warp & 3) * 32) << 16));
             tc_fence_before();
             warp_arrive(&drained[n & 1]);
@@ -1111,6 +1112,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
             if (!ok) break;
             const float rowc = dec[n % ND].row[i] * a.scale;
+            const bool open = dec[n % ND].first[i] < 0;   // the state reaches the row
             warp_arrive(&dempty[n % ND]);
             ok = warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
             if (!ok) break;
@@ -1127,8 +1129,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 uint32_t p[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    p[j] = pack2(fmaf(rowc, u[2 * j], a.scale * w[2 * j]),
-                                 fmaf(rowc, u[2 * j + 1], a.scale * w[2 * j + 1]));
+                    p[j] = pack2(fmaf(rowc, open ? u[2 * j] : 0.0f, a.scale * w[2 * j]),
+                                 fmaf(rowc, open ? u[2 * j + 1] : 0.0f, a.scale * w[2 * j + 1]));
                 uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
                 if (on && c < cols && SLSTM_IN(row + (long long)n * TCC, all))
                     dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
@@ -1498,7 +1500,6 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     xs += v;
                     ws += y;
                 }
-                const double xl = xs, wl = ws;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const double xu = __shfl_down_sync(0xffffffffu, xs, o), wu = __shfl_up_sync(0xffffffffu, ws, o);
@@ -1510,7 +1511,11 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
                 dot = __shfl_sync(0xffffffffu, dot, 0) * (double)d.tot;
-                double back = xs - xl, front = ws - wl;   // rows behind this lane's, rows before
+                if (d.tot < 0.0f) dot = 0.0;
+                // rows behind this lane's, rows before (no differences: a sum may be no number)
+                double back = __shfl_down_sync(0xffffffffu, xs, 1), front = __shfl_up_sync(0xffffffffu, ws, 1);
+                if (lane == 31) back = 0.0;
+                if (lane == 0) front = 0.0;
                 float out[4], sum = 0.0f;
 #pragma unroll
                 for (int i = 3; i >= 0; --i) {
@@ -1635,8 +1640,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 float v[32];
                 tmem_ld32(R2 + at, v);
                 const float f = a.scale * d.row[r];
+                const bool open = d.first[r] < 0;   // the state reaches the row
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= f;
+                for (int j = 0; j < 32; ++j) v[j] = open ? v[j] * f : 0.0f;
                 tmem_st32(R2 + at, v);
                 sums[8 + b][r] = dot_row(smem + SM::Q, r, b, v);
             }
@@ -1644,11 +1650,12 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const float colr = d.col[r];
+            const bool out = d.first[TCC - 1] <= r;   // the row reaches the state
             if (b < DK / 32) {
                 float v[32];
                 tmem_ld32(R3 + at, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= colr;
+                for (int j = 0; j < 32; ++j) v[j] = out ? v[j] * colr : 0.0f;
                 tmem_st32(R3 + at, v);
                 sums[12 + b][r] = dot_row(smem + SM::K, r, b, v);
             }
@@ -1666,7 +1673,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 float v[32];
                 tmem_ld32(R0 + at, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= colr;
+                for (int j = 0; j < 32; ++j) v[j] = out ? v[j] * colr : 0.0f;
                 tmem_st32(R0 + at, v);
             }
             tmem_wait_st();
