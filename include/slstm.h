@@ -658,6 +658,8 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
  * states entering a product split into two bf16 terms wherever an fp32 output
  * depends on it), everything else on the CUDA cores.  Gradients of q, k, v
  * have `dtype` and are contiguous, those of g and s0 are fp32.
+ * On the tensor cores a wait that runs out (a fault of the device) leaves NaN in
+ * every output element that depends on what was waited for.
  * A token whose q, k, v or g is not finite spoils its sequence, earlier tokens
  * of its 128 included, never another sequence.
  */
@@ -673,6 +675,12 @@ typedef struct {
     float scale;
     long long ld_q, ld_k, ld_v;  /* elements between tokens, at least the
                                     heads x features of one                  */
+    int debug_fault;             /* 0 in normal use.  n > 0: on the tensor
+                                    cores a block loads no n-th chunk, so that
+                                    its bounded waits run out (a self-test)  */
+    int wait_limit_us;           /* upper bound of one bounded wait on the
+                                    tensor cores, in microseconds (0: the
+                                    default of 2 seconds)                    */
 } slstm_linear_attention_config;
 
 /*

@@ -65,7 +65,8 @@ class NewtonConfig(ctypes.Structure):
 class LinearAttentionConfig(ctypes.Structure):
     _fields_ = [("H", ctypes.c_int), ("H_qk", ctypes.c_int), ("d_k", ctypes.c_int), ("d_v", ctypes.c_int),
                 ("dtype", ctypes.c_int), ("decay", ctypes.c_int), ("scale", ctypes.c_float),
-                ("ld_q", ctypes.c_longlong), ("ld_k", ctypes.c_longlong), ("ld_v", ctypes.c_longlong)]
+                ("ld_q", ctypes.c_longlong), ("ld_k", ctypes.c_longlong), ("ld_v", ctypes.c_longlong),
+                ("debug_fault", ctypes.c_int), ("wait_limit_us", ctypes.c_int)]
 
 
 STATS_BYTES = 4 * 4 + 2 * 4 * SLSTM_STATS_HISTORY + 2 * 4

@@ -32,6 +32,8 @@ struct LaArgs {
     const float *dsT;
     void *dq, *dk_, *dv_;
     float *dg, *ds0;
+    // tensor cores: what a wait may try, and the self-test of its running out
+    int tries, debug_fault;
 };
 
 size_t la_simt_workspace(const LaArgs &a, bool backward);
@@ -69,6 +71,7 @@ cudaError_t la_scan(const LaChunks &ch, int H, int E, bool back, float *buf, con
 
 // bf16 on the tensor cores.
 bool la_tc_takes(const LaArgs &a);
+int la_tc_tries(int wait_limit_us);
 size_t la_tc_forward_workspace(const LaArgs &a);
 cudaError_t la_tc_forward(const LaArgs &a, void *ws, cudaStream_t st);
 size_t la_tc_backward_workspace(const LaArgs &a);

@@ -12,9 +12,10 @@
 // the 2-norm, 1.66e-3 of it its own rounding; 169 us instead of 186 forward, 542
 // instead of 585 for the gradients.)
 //
-// Every mbarrier wait is bounded in time; on expiry the block marks itself,
-// waits (bounded) for its own loads and MMAs, writes NaN over its outputs,
-// frees its tensor memory and returns.
+// Every mbarrier wait is bounded in its tries (of about 4 us each when they
+// fail); on expiry the block marks itself, waits (bounded) for its own loads and
+// MMAs, writes NaN over the outputs that it has not made, frees its tensor memory
+// and returns.
 #include <cuda_bf16.h>
 
 #define SLSTM_FILE_ID 13
@@ -29,6 +30,12 @@ namespace {
 constexpr int TCC = 128;                     // rows of a chunk
 constexpr uint32_t BOX = TCC * 128;          // bytes of 128 rows of 64 bf16
 constexpr uint64_t TC_WAIT_NS = 1000000000ull;
+constexpr int TRY_US = 4;                    // a try of a wait that fails: 3.96 us, measured
+
+// A block's waits, in shared memory.
+struct Waits {
+    int gave_up, tries;
+};
 constexpr int ND = 4;                        // chunks whose decays are held
 
 // The decays of a chunk.  D_ij = e^{c_i - c_j} of rows i in 32-row block q and
@@ -94,6 +101,8 @@ SLSTM_DEVINL uint32_t pack2(float a, float b)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+SLSTM_DEVINL __nv_bfloat16 bf16_nan() { return __float2bfloat16(__int_as_float(0x7fc00000)); }
+
 SLSTM_DEVINL float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
 SLSTM_DEVINL float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
@@ -142,11 +151,11 @@ SLSTM_DEVINL uint8_t *aligned_smem(uint8_t *raw) { return raw + ((1024u - (smem_
 // (for a time of its own), and the tries are counted, which costs the
 // waiting warps' neighbours less than reading a clock.  False after the last, or
 // once this block has given up.
-SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, Waits *w)
 {
     const uint32_t addr = smem_u32(bar);
 #pragma unroll 1
-    for (int i = 0; i < (1 << 20); ++i) {
+    for (int i = 1;; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n"
@@ -158,9 +167,10 @@ SLSTM_DEVINL bool lane_wait(uint64_t *bar, uint32_t parity, int *s_abort)
             : "r"(addr), "r"(parity)
             : "memory");
         if (ok) return true;
-        if (*(volatile int *)s_abort) return false;
+        if (*(volatile int *)&w->gave_up) return false;
+        if (i >= w->tries) break;
     }
-    *(volatile int *)s_abort = 1;
+    *(volatile int *)&w->gave_up = 1;
     return false;
 }
 // Whether a phase has completed, without being suspended.
@@ -179,9 +189,9 @@ SLSTM_DEVINL bool done(uint64_t *bar, uint32_t parity)
     return ok != 0u;
 }
 // One wait of a whole warp: every lane the same answer.
-SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, int *s_abort)
+SLSTM_DEVINL bool warp_wait(uint64_t *bar, uint32_t parity, Waits *w)
 {
-    return __all_sync(0xffffffffu, lane_wait(bar, parity, s_abort));
+    return __all_sync(0xffffffffu, lane_wait(bar, parity, w));
 }
 
 // The warp's shared-memory writes (and its reads of tensor memory) before the
@@ -481,7 +491,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     __shared__ uint64_t full[NST], empty[NST], dfull[ND], dempty[ND], yready[2], delta[2], drained[2];
     __shared__ uint64_t staged, unstaged, fin;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_loaded;
+    __shared__ Waits s_wait;
+    __shared__ int s_loaded;
     // the passes of both directions for the segments' first states run in one launch
     const TcArgs &g = blockIdx.y == 0 ? g0 : g1;
     const CUtensorMap *mx = blockIdx.y == 0 ? &mx0 : &mx1, *my = blockIdx.y == 0 ? &my0 : &my1;
@@ -509,7 +520,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         mbar_init(&unstaged, 8);
         mbar_init(&fin, 1);
         mbar_init_fence();
-        s_abort = 0;
+        s_wait.gave_up = 0;
+        s_wait.tries = a.tries;
         s_loaded = 0;
     }
     if (warp == 0) tmem_alloc<256>(&s_tmem);
@@ -526,10 +538,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         if (elect_one()) {
             const int hq = h / (a.H / a.Hqk);
             int n = 0;
-            for (; n < nch; ++n) {
+            for (; n < nch && n + 1 != a.debug_fault; ++n) {
                 const int s = n % NST;
-                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_abort)) break;
-                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) break;
+                if (!lane_wait(&empty[s], ((uint32_t)(n / NST) & 1u) ^ 1u, &s_wait)) break;
+                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_wait)) break;
                 uint8_t *st = smem + s * SM::STAGE;
                 mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
                 bulk_load(&dec[n % ND], g.dec + (sg.c0 + chunk(n)) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
@@ -552,9 +564,9 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             constexpr uint32_t idesc = idesc_bf16(128, 128, true, true);
             for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
-                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
-                if (!lane_wait(&yready[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
-                if (!lane_wait(&drained[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort)) break;
+                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
+                if (!lane_wait(&yready[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait)) break;
+                if (!lane_wait(&drained[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_wait)) break;
                 tc_fence_after();
                 // the 64 rows of a narrow d_k twice: no step from one 64 to the next
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
@@ -596,7 +608,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                     asm volatile("prefetch.global.L2 [%0];" ::"l"(p + ((sg.c0 + chunk(n + 1)) * a.H + h) * a.dk * a.dv +
                                                              (long long)(r & 127) * a.dv + 64 * tile));
             }
-            if (!warp_wait(&staged, (uint32_t)n & 1u, &s_abort)) break;
+            if (!warp_wait(&staged, (uint32_t)n & 1u, &s_wait)) break;
             if (warp == 18 && lane == 0) {
                 tma_store_3d(&mhi, smem + SM::OUT, 64 * tile, 0, (int)ci);
                 tma_store_3d(&mlo, smem + SM::OUT + DK * 128, 64 * tile, 0, (int)ci);
@@ -629,10 +641,10 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         const int t = (warp & 3) * 32 + lane, half = (warp >> 2) & 1;
         for (int n = 0; n < nch; ++n) {
             const int s = n % NST;
-            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
-            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait)) break;
+            if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
             // the product that read this buffer two chunks ago
-            if (n > 1 && !warp_wait(&delta[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_abort)) break;
+            if (n > 1 && !warp_wait(&delta[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_wait)) break;
             uint8_t *st = smem + s * SM::STAGE;
             const TcDecays &d = dec[n % ND];
             const int len = rows(n);
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
             if (g.hi) {
-                if (n > 0 && !warp_wait(&unstaged, (uint32_t)(n - 1) & 1u, &s_abort)) {
+                if (n > 0 && !warp_wait(&unstaged, (uint32_t)(n - 1) & 1u, &s_wait)) {
                     ok = false;
                     break;
                 }
@@ -679,8 +691,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 tma_store_fence();
                 warp_arrive(&staged);
             }
-            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort) ||
-                !warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) {
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait) ||
+                !warp_wait(&delta[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait)) {
                 ok = false;
                 break;
             }
@@ -695,10 +707,6 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         if (!ok) {
 #pragma unroll
             for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
-            if (g.hi && r < a.dk)
-                for (int n = 0; n < nch; ++n)
-                    for (int i = 0; i < SH::N && col + i < a.dv; ++i)
-                        g.hi[((sg.c0 + n) * a.H + h) * E + (long long)r * a.dv + col + i] = __float2bfloat16(S[0]);
         }
         float *dst = g.fin ? g.fin + ((long long)sg.item * a.H + h) * E
                            : (g.last && sg.only ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
@@ -708,7 +716,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
-        if (s_abort)
+        if (s_wait.gave_up)
             for (int n = max(0, s_loaded - NST); n < s_loaded; ++n)
                 {
                 (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
@@ -720,6 +728,19 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
     if (warp == 0) {
         tc_fence_after();
         tmem_free<256>(tmem);
+    }
+    if (!s_wait.gave_up || !g.hi) return;
+    // what this block has not stored is not known any more
+    Seg lost;
+    seg_of(g, item, &lost);
+    const int cols = min(64, a.dv - 64 * tile);
+#pragma unroll 1
+    for (int n = 0; n < lost.nch; ++n) {
+        const long long ci = (lost.c0 + n) * a.H + h;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < a.dk * cols; i += STATE_THREADS)
+            g.hi[ci * a.dk * a.dv + (long long)(i / cols) * a.dv + 64 * tile + i % cols] = bf16_nan();
+        if (g.dot && threadIdx.x < 8) g.dot[(ci * 2 + tile) * 8 + threadIdx.x] = __int_as_float(0x7fc00000);
     }
 }
 
@@ -775,7 +796,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     __shared__ uint64_t yready, delta, sready, sfree, lready[2], pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_loaded;
+    __shared__ Waits s_wait;
+    __shared__ int s_loaded;
     const LaArgs &a = g.a;
     const int tile = blockIdx.x % g.tiles, h = (blockIdx.x / g.tiles) % a.H, item = blockIdx.x / (g.tiles * a.H);
     Seg sg;
@@ -808,7 +830,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         mbar_init(&drained, 8);
         mbar_init(&fin, 2);
         mbar_init_fence();
-        s_abort = 0;
+        s_wait.gave_up = 0;
+        s_wait.tries = a.tries;
         s_loaded = 0;
     }
     if (warp == 0) tmem_alloc<512>(&s_tmem);
@@ -828,7 +851,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             auto load = [&](int n) -> bool {
                 const int s = n % NST;
                 const uint32_t ph = ((uint32_t)(n / NST) & 1u) ^ 1u;
-                if (!lane_wait(&empty[s], ph, &s_abort)) return false;
+                if (!lane_wait(&empty[s], ph, &s_wait)) return false;
                 uint8_t *st = smem + s * SM::STAGE;
                 mbar_expect_tx(&full[s], 2 * SM::NB * BOX);
                 const int t = sg.t + n * TCC;
@@ -838,8 +861,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     tma_load_4d(st + (SM::NB + i) * BOX, &mk, &full[s], 64 * i, hq, t, sg.b);
                 }
                 s_loaded = 2 * n + 1;
-                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_abort)) return false;
-                if (!lane_wait(&vempty[s], ph, &s_abort)) return false;
+                if (!lane_wait(&dempty[n % ND], ((uint32_t)(n / ND) & 1u) ^ 1u, &s_wait)) return false;
+                if (!lane_wait(&vempty[s], ph, &s_wait)) return false;
                 mbar_expect_tx(&dfull[n % ND], sizeof(TcDecays));
                 bulk_load(&dec[n % ND], g.dec + (sg.c0 + n) * a.H + h, sizeof(TcDecays), &dfull[n % ND]);
                 mbar_expect_tx(&vfull[s], BOX);
@@ -847,7 +870,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 s_loaded = 2 * n + 2;
                 return true;
             };
-            for (int n = 0; n < nch; ++n)
+            for (int n = 0; n < nch && n + 1 != a.debug_fault; ++n)
                 if (!load(n)) break;
         }
     } else if (warp == 24) {
@@ -857,8 +880,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             for (int n = 0; n < nch && ok; ++n) {
                 const int s = n % NST;
                 const uint32_t ph = (uint32_t)n & 1u;
-                ok = lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort) && lane_wait(&yready, ph, &s_abort) &&
-                     lane_wait(&drained, ph ^ 1u, &s_abort);
+                ok = lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait) && lane_wait(&yready, ph, &s_wait) &&
+                     lane_wait(&drained, ph ^ 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
                 // both terms of w v side by side: k is read once for them; the
@@ -884,8 +907,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 const int s = n % NST;
                 if (!must && (!done(&full[s], (uint32_t)(n / NST) & 1u) || (n == ragged && !done(&tready, 0u))))
                     return true;
-                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) return false;
-                if (n == ragged && !lane_wait(&tready, 0u, &s_abort)) return false;
+                if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) return false;
+                if (n == ragged && !lane_wait(&tready, 0u, &s_wait)) return false;
                 scored = n + 1;
                 tc_fence_after();
                 const uint8_t *st = smem + s * SM::STAGE;
@@ -912,12 +935,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (n + 1 < nch) {
 #pragma unroll 1
                     for (int i = 0; i < (1 << 20); ++i) {
-                        if (scored > n + 1 || done(&pready[ph], (uint32_t)(n >> 1) & 1u)) break;
+                        if (scored > n + 1 || done(&pready[ph], (uint32_t)(n >> 1) & 1u) ||
+                            *(volatile int *)&s_wait.gave_up)
+                            break;
                         scores(n + 1, false);
                     }
                 }
-                ok = lane_wait(&sready, ph, &s_abort) &&
-                     lane_wait(&oempty, ph ^ 1u, &s_abort);
+                ok = lane_wait(&sready, ph, &s_wait) &&
+                     lane_wait(&oempty, ph ^ 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
@@ -931,7 +956,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 umma_commit(&sfree);
                 // the state's lower term has come to where k was
-                ok = lane_wait(&lready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                ok = lane_wait(&lready[ph], (uint32_t)(n >> 1) & 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t ld = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), BOX);
@@ -943,8 +968,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         umma_bf16(t_o, qd + 2 * k, ld + (2048u >> 4) * (4 * i + k), id_o, 1u);
                 }
                 umma_commit(&empty[s]);
-                ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) &&
-                     lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_abort);
+                ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) &&
+                     lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t ta = tmem + ph * 128;
@@ -970,8 +995,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         // the other half of v's columns: w v is what the next chunk's product waits for
         auto scale = [&](int n) -> bool {
             const int s = n % NST, t = (warp & 3) * 32 + lane, p = 4 + 2 * (warp >> 2);
-            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort) ||
-                !warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort))
+            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) ||
+                !warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait))
                 return false;
             scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, p, p + 2,
                       dec[n % ND].col[t], t < sg.len - n * TCC);
@@ -982,7 +1007,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = scale(0);
         for (int n = 0; n < nch && ok; ++n) {
             const uint32_t ph = (uint32_t)n & 1u;
-            if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_abort);
+            if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_wait);
             if (!ok) break;
             // the state's upper term, row r: the B operand of q S
 #pragma unroll
@@ -994,7 +1019,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             warp_arrive(&sready);
             // the lower term goes where the chunk's keys were, once both products
             // that read them are done: there is no room for a buffer of its own
-            ok = warp_wait(&delta, ph, &s_abort) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort);
+            ok = warp_wait(&delta, ph, &s_wait) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait);
             if (!ok) break;
             uint8_t *low = smem + (n % NST) * SM::STAGE + SM::NB * BOX;
             // (the upper terms are rounded again: kept over the waits they spill)
@@ -1026,17 +1051,17 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         for (int n = 0; n < nch; ++n) {
             const int s = n % NST, len = min(TCC, sg.len - n * TCC);
             uint8_t *st = smem + s * SM::STAGE;
-            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+            if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
             if (n == ragged) {
-                if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_abort)) break;
+                if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
                 if (t >= len)
                     for (int i = 0; i < 2 * SM::NB + 1; ++i) zero_row(st + i * BOX, t);
                 tma_store_fence();
                 warp_arrive(&tready);
             }
-            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait)) break;
             // the product that read the last terms
-            if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_abort)) break;
+            if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_wait)) break;
             const float w = dec[n % ND].col[t];
             scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 4, w, t < len);
             tma_store_fence();
@@ -1048,8 +1073,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         const int i = q * 32 + lane;   // query row
         const uint32_t la = (uint32_t)(q * 32) << 16;
         for (int n = 0; n < nch; ++n) {
-            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort)) break;
-            if (!warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_abort)) break;
+            if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait)) break;
+            if (!warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait)) break;
             tc_fence_after();
             const TcDecays &d = dec[n % ND];
             // 64 keys of this warp; the two terms of 16 weights in the place of their scores
@@ -1109,12 +1134,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = true;
         int n = 0;
         for (; n < nch; ++n) {
-            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_abort);
+            ok = warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait);
             if (!ok) break;
             const float rowc = dec[n % ND].row[i] * a.scale;
             const bool open = dec[n % ND].first[i] < 0;   // the state reaches the row
             warp_arrive(&dempty[n % ND]);
-            ok = warp_wait(&ofull, (uint32_t)n & 1u, &s_abort);
+            ok = warp_wait(&ofull, (uint32_t)n & 1u, &s_wait);
             if (!ok) break;
             tc_fence_after();
             const bool on = n * TCC + i < sg.len;
@@ -1139,12 +1164,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         }
         if (!ok)
             for (; n < nch && n * TCC + i < sg.len; ++n)
-                for (int j = 0; j < cols; ++j) o[n * step + j] = __float2bfloat16(__int_as_float(0x7fc00000));
+                for (int j = 0; j < cols; ++j) o[n * step + j] = bf16_nan();
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
-        if (s_abort)
+        if (s_wait.gave_up)
             for (int n = max(0, (s_loaded + 1) / 2 - NST); 2 * n < s_loaded; ++n) {
                 (void)mbar_wait(&full[n % NST], (uint32_t)(n / NST) & 1u, TC_WAIT_NS);
                 if (2 * n + 1 >= s_loaded) break;
@@ -1280,7 +1305,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     __shared__ uint64_t full1, full2, fullS, fullD, dfull[2], dempty[2], bsc, bdqi, bdki, bx, scfree, pready, bout,
         tfree, xfree, tready, sumfree, fin;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_loaded;
+    __shared__ Waits s_wait;
+    __shared__ int s_loaded;
     const LaArgs &a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool packed = g.ch.pos != nullptr;
@@ -1308,7 +1334,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         mbar_init(&sumfree, 1);
         mbar_init(&fin, 1);
         mbar_init_fence();
-        s_abort = 0;
+        s_wait.gave_up = 0;
+        s_wait.tries = a.tries;
         s_loaded = 0;
     }
     if (warp == 0) tmem_alloc<512>(&s_tmem);
@@ -1324,12 +1351,13 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             constexpr uint32_t SB = DK * 128;   // bytes of a box of a state: DK rows, 64 columns
             int it = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+                if (it + 1 == a.debug_fault) break;
                 const int h = item % a.H, c = item / a.H, hq = h / rep;
                 const LaChunk ck = la_chunk(g.ch, c);
                 const int t = packed ? (int)ck.row : ck.n * TCC, b = packed ? 0 : ck.seq;
                 const uint32_t ph = (uint32_t)it & 1u;
-                if (it > 0 && !lane_wait(&bout, ph ^ 1u, &s_abort)) break;
-                if (!lane_wait(&dempty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s_abort)) break;
+                if (it > 0 && !lane_wait(&bout, ph ^ 1u, &s_wait)) break;
+                if (!lane_wait(&dempty[it & 1], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s_wait)) break;
                 mbar_expect_tx(&dfull[it & 1], sizeof(TcDecays));
                 bulk_load(&dec[it & 1], g.dec + item, sizeof(TcDecays), &dfull[it & 1]);
                 mbar_expect_tx(&full1, 2 * NK * BOX);
@@ -1345,7 +1373,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     tma_load_4d(smem + SM::G + i * BOX, &mg, &full2, 64 * i, h, t, b);
                 }
                 s_loaded = 3 * it + 1;
-                if (it > 0 && !lane_wait(&xfree, ph ^ 1u, &s_abort)) break;
+                if (it > 0 && !lane_wait(&xfree, ph ^ 1u, &s_wait)) break;
                 mbar_expect_tx(&fullS, 2 * NV * SB);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -1353,7 +1381,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     tma_load_3d(x1 + i * SB, &msl, &fullS, 64 * i, 0, item);
                 }
                 s_loaded = 3 * it + 2;
-                if (!lane_wait(&bdqi, ph, &s_abort)) break;
+                if (!lane_wait(&bdqi, ph, &s_wait)) break;
                 mbar_expect_tx(&fullD, 2 * NV * SB);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -1408,30 +1436,30 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             int it = 0, ragged = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
                 const uint32_t ph = (uint32_t)it & 1u;
-                if (!lane_wait(&full1, ph, &s_abort)) break;
+                if (!lane_wait(&full1, ph, &s_wait)) break;
                 if (packed && la_chunk(g.ch, item / a.H).len < TCC) {
                     // rows behind a ragged chunk are cleared before they are read
-                    if (!lane_wait(&tready, (uint32_t)ragged & 1u, &s_abort)) break;
+                    if (!lane_wait(&tready, (uint32_t)ragged & 1u, &s_wait)) break;
                     ++ragged;
                 }
-                if (it > 0 && !lane_wait(&tfree, ph ^ 1u, &s_abort)) break;
+                if (it > 0 && !lane_wait(&tfree, ph ^ 1u, &s_wait)) break;
                 tc_fence_after();
                 inner(R0, sm + SM::K, sm + SM::Q, BOX, NK, id_ss, false);
-                if (!lane_wait(&full2, ph, &s_abort)) break;
+                if (!lane_wait(&full2, ph, &s_wait)) break;
                 tc_fence_after();
                 inner(R1, sm + SM::V, sm + SM::G, BOX, NV, id_ss, false);
                 umma_commit(&bsc);
-                if (!lane_wait(&fullS, ph, &s_abort)) break;
+                if (!lane_wait(&fullS, ph, &s_wait)) break;
                 tc_fence_after();
                 inner(R2, sm + SM::G, sx0, SB, NV, id_si, false);
                 inner(R2, sm + SM::G, sx1, SB, NV, id_si, true);
                 umma_commit(&bdqi);
-                if (!lane_wait(&fullD, ph, &s_abort)) break;
+                if (!lane_wait(&fullD, ph, &s_wait)) break;
                 tc_fence_after();
                 inner(R3, sm + SM::V, sx0, SB, NV, id_si, false);
                 inner(R3, sm + SM::V, sx1, SB, NV, id_si, true);
                 umma_commit(&bdki);
-                if (!lane_wait(&scfree, ph, &s_abort)) break;
+                if (!lane_wait(&scfree, ph, &s_wait)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
@@ -1445,7 +1473,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     }
                 }
                 umma_commit(&bx);
-                if (!lane_wait(&pready, ph, &s_abort)) break;
+                if (!lane_wait(&pready, ph, &s_wait)) break;
                 tc_fence_after();
                 const uint64_t gd = smem_desc_mn_sw128(sm + SM::G, BOX), qd = smem_desc_mn_sw128(sm + SM::Q, BOX),
                                kd = smem_desc_mn_sw128(sm + SM::K, BOX);
@@ -1476,8 +1504,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
             const int h = item % a.H, c = item / a.H;
             const uint32_t ph = (uint32_t)it & 1u;
-            if (!warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_abort)) break;
-            if (!warp_wait(&pready, ph, &s_abort)) break;
+            if (!warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_wait)) break;
+            if (!warp_wait(&pready, ph, &s_wait)) break;
             if (a.dg) {
                 const TcDecays &d = dec[it & 1];
                 const LaChunk ck = la_chunk(g.ch, c);
@@ -1553,15 +1581,15 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             h = item % a.H;
             ck = la_chunk(g.ch, item / a.H);
             if (packed && ck.len < TCC) {
-                ok = warp_wait(&full1, ph, &s_abort) && warp_wait(&full2, ph, &s_abort);
+                ok = warp_wait(&full1, ph, &s_wait) && warp_wait(&full2, ph, &s_wait);
                 if (!ok) break;
                 if (r >= ck.len)
                     for (int i = b; i < 2 * (NK + NV); i += 4) zero_row(smem + i * BOX, r);
                 tma_store_fence();
                 warp_arrive(&tready);
             }
-            ok = warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_abort) && warp_wait(&bsc, ph, &s_abort);
-            if (ok && it > 0) ok = warp_wait(&sumfree, ph ^ 1u, &s_abort);
+            ok = warp_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, &s_wait) && warp_wait(&bsc, ph, &s_wait);
+            if (ok && it > 0) ok = warp_wait(&sumfree, ph ^ 1u, &s_wait);
             if (!ok) break;
             tc_fence_after();
             const TcDecays &d = dec[it & 1];
@@ -1633,7 +1661,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             tc_fence_before();
             warp_arrive(&scfree);
             // the states' part of dq and dk: scaled in place, dotted with q and k
-            ok = warp_wait(&bdqi, ph, &s_abort);
+            ok = warp_wait(&bdqi, ph, &s_wait);
             if (!ok) break;
             tc_fence_after();
             if (b < DK / 32) {
@@ -1646,7 +1674,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 tmem_st32(R2 + at, v);
                 sums[8 + b][r] = dot_row(smem + SM::Q, r, b, v);
             }
-            ok = warp_wait(&bdki, ph, &s_abort);
+            ok = warp_wait(&bdki, ph, &s_wait);
             if (!ok) break;
             tc_fence_after();
             const float colr = d.col[r];
@@ -1659,7 +1687,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 tmem_st32(R3 + at, v);
                 sums[12 + b][r] = dot_row(smem + SM::K, r, b, v);
             }
-            ok = warp_wait(&bx, ph, &s_abort);
+            ok = warp_wait(&bx, ph, &s_wait);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
@@ -1681,7 +1709,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             tc_fence_before();
             warp_arrive(&pready);
             warp_arrive(&dempty[it & 1]);
-            ok = warp_wait(&bout, ph, &s_abort);
+            ok = warp_wait(&bout, ph, &s_wait);
             if (!ok) break;
             tc_fence_after();
             const long long row = ck.row + q * 32;
@@ -1714,20 +1742,11 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             tc_fence_before();
             warp_arrive(&tfree);
         }
-        if (!ok)
-            for (int item = blockIdx.x + it * gridDim.x; item < items; item += gridDim.x) {
-                ck = la_chunk(g.ch, item / a.H);
-                h = item % a.H;
-                if (r < ck.len)
-                    for (int j = 32 * b; j < min(a.dv, 32 * b + 32); ++j)
-                        static_cast<__nv_bfloat16 *>(a.dv_)[((ck.row + r) * a.H + h) * a.dv + j] =
-                            __float2bfloat16(__int_as_float(0x7fc00000));
-            }
     }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
-        if (s_abort && s_loaded > 0) {
+        if (s_wait.gave_up && s_loaded > 0) {
             const int it = (s_loaded - 1) / 3, part = s_loaded - 3 * it;
             const uint32_t ph = (uint32_t)it & 1u;
             (void)mbar_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, TC_WAIT_NS);
@@ -1742,6 +1761,28 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     if (warp == 0) {
         tc_fence_after();
         tmem_free<512>(tmem);
+    }
+    if (!s_wait.gave_up) return;
+    // which of its parts a block has finished is not known: all its items
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int h = item % a.H, c = item / a.H;
+        const LaChunk ck = la_chunk(g.ch, c);
+        const float nan = __int_as_float(0x7fc00000);
+        for (int r = warp; r < ck.len; r += BACK_THREADS / 32) {
+            const long long row = ck.row + r;
+            for (int j = lane; j < a.dv; j += 32)
+                static_cast<__nv_bfloat16 *>(a.dv_)[(row * a.H + h) * a.dv + j] = bf16_nan();
+            for (int j = lane; j < a.dk; j += 32)
+                if (g.part_q) {
+                    g.part_q[(row * a.H + h) * a.dk + j] = nan;
+                    g.part_k[(row * a.H + h) * a.dk + j] = nan;
+                } else {
+                    static_cast<__nv_bfloat16 *>(a.dq)[(row * a.Hqk + h) * a.dk + j] = bf16_nan();
+                    static_cast<__nv_bfloat16 *>(a.dk_)[(row * a.Hqk + h) * a.dk + j] = bf16_nan();
+                }
+            if (a.dg && !a.per_head && lane == 0) a.dg[row * a.H + h] = nan;
+        }
+        if (a.dg && a.per_head && threadIdx.x == 0) g.dgc[(long long)c * a.H + h] = nan;
     }
 }
 
@@ -1948,6 +1989,12 @@ bool la_tc_takes(const LaArgs &a)
 {
     return a.dtype == SLSTM_BF16 && a.dk <= 128 && a.dv <= 128 && a.dk % 8 == 0 && a.dv % 8 == 0 && a.ldq % 8 == 0 &&
            a.ldk % 8 == 0 && a.ldv % 8 == 0;
+}
+
+int la_tc_tries(int wait_limit_us)
+{
+    const int us = wait_limit_us ? wait_limit_us : 2000000;
+    return us / TRY_US + 1;
 }
 
 size_t la_tc_forward_workspace(const LaArgs &a)

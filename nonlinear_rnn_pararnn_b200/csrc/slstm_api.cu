@@ -87,6 +87,7 @@ bool la_sizes_ok(const slstm_linear_attention_config *c, int B, int T, bool pack
     if (c->d_k < 1 || c->d_v < 1 || c->d_k > SLSTM_LA_MAX_DIM || c->d_v > SLSTM_LA_MAX_DIM) return false;
     if (c->dtype != SLSTM_F32 && c->dtype != SLSTM_BF16) return false;
     if (c->decay != SLSTM_DECAY_TOKEN && c->decay != SLSTM_DECAY_HEAD) return false;
+    if (c->debug_fault < 0 || c->wait_limit_us < 0) return false;
     const long long wqk = (long long)c->H_qk * c->d_k, wv = (long long)c->H * c->d_v;
     if (c->ld_q < wqk || c->ld_k < wqk || c->ld_v < wv) return false;
     if (c->ld_q > kIndexLimit || c->ld_k > kIndexLimit || c->ld_v > kIndexLimit) return false;
@@ -115,6 +116,8 @@ LaArgs la_args(const void *q, const void *k, const void *v, const float *g, cons
     a.ldv = c.ld_v;
     a.dtype = c.dtype;
     a.per_head = c.decay == SLSTM_DECAY_HEAD;
+    a.tries = la_tc_tries(c.wait_limit_us);
+    a.debug_fault = c.debug_fault;
     a.scale = c.scale;
     a.cu = cu;
     a.q = q;
