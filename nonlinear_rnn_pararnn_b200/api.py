@@ -637,13 +637,21 @@ def _la_workspace(fields, B, T, packed, backward, ws, device):
     return ws
 
 
-def linear_attention_workspace(q, v, g, *, n_seq: int = 0, backward: bool = False) -> torch.Tensor:
+def linear_attention_workspace(q, v, g, *, k: torch.Tensor = None, n_seq: int = 0,
+                               backward: bool = False) -> torch.Tensor:
     """A workspace for linear_attention_forward or _backward of tensors like
-    these (of their _varlen forms: n_seq sequences), to pass as ws."""
+    these (of their _varlen forms: n_seq sequences), to pass as ws.  The spacing
+    of k's tokens decides with the others which kernels run and what they need:
+    without k the workspace holds for any."""
     lead = q.shape[:-2]
-    cfg = _la_config(q, q, v, g, lead, None)
+    cfg = _la_config(q, q if k is None else k, v, g, lead, None)
     B, T = (n_seq, lead[0]) if n_seq else lead
-    return _la_workspace(cfg, B, T, n_seq > 0, backward, None, q.device)
+    n = _la_bytes(cfg, B, T, n_seq > 0, backward)
+    if n and k is None:
+        n = max(n, _la_bytes((*cfg[:8], cfg[8] | 1, cfg[9]), B, T, n_seq > 0, backward))
+    if n == 0:
+        raise ValueError("unsupported sizes")
+    return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
 def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: torch.Tensor = None,

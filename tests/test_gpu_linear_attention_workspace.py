@@ -1,0 +1,33 @@
+"""GPU tests of the workspaces that a caller of the linear attention brings."""
+import pytest
+import torch
+
+from nonlinear_rnn_pararnn_b200 import api
+from test_gpu_linear_attention import BF16, _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("with_k", [False, True])
+def test_keys_of_another_spacing(with_k, packed, cuda_device):
+    """q and v whose tokens lie multiples of 8 apart, and k a slice whose do not: other kernels, which need more."""
+    x = _inputs((300,) if packed else (2, 150), 1, 2, 64, 64, BF16, 51, nseq=2)
+    wide = torch.zeros(*x["k"].shape[:-1], 67, dtype=BF16, device="cuda")
+    wide[..., 3:] = x["k"]
+    k = wide[..., 3:]
+    kw = {"k": k} if with_k else {}
+    ws = [api.linear_attention_workspace(x["q"], x["v"], x["g"], backward=b, n_seq=2 if packed else 0, **kw)
+          for b in (False, True)]
+    a = [x["q"], k, x["v"], x["g"], x["s0"]]
+    if packed:
+        a.append(torch.tensor([0, 90, 300], dtype=torch.int32, device="cuda"))
+    fwd = api.linear_attention_forward_varlen if packed else api.linear_attention_forward
+    bwd = api.linear_attention_backward_varlen if packed else api.linear_attention_backward
+    for y, z in zip(fwd(*a), fwd(*a, ws=ws[0])):
+        assert torch.equal(y, z)
+    want, got = bwd(*a, x["dO"], x["dsT"]), bwd(*a, x["dO"], x["dsT"], ws=ws[1])
+    assert all(torch.equal(want[n], got[n]) for n in want)
+    # and k like q
+    a[1] = x["k"]
+    fwd(*a, ws=api.linear_attention_workspace(x["q"], x["v"], x["g"], n_seq=2 if packed else 0))
