@@ -552,6 +552,15 @@ def _need_on(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
+def _bytes_on(ws, n: int, device) -> torch.Tensor:
+    """A workspace of n bytes: the caller's, which has to have them one after another, or a new one."""
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if ws.device != device or ws.nbytes < n or not ws.is_contiguous():
+        raise ValueError(f"ws must hold {n} contiguous bytes on {device}")
+    return ws
+
+
 def _need_tokens(t: torch.Tensor, name: str, lead, heads: int, d: int, dtype, device) -> int:
     """Checks a (*lead, heads, d) tensor whose tokens are contiguous and evenly
     spaced (a slice of a projection's output is); returns their spacing."""
@@ -630,11 +639,7 @@ def _la_workspace(fields, B, T, packed, backward, ws, device):
     n = _la_bytes(fields, B, T, packed, backward)
     if n == 0:
         raise ValueError("unsupported sizes")
-    if ws is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    if ws.device != device or ws.nbytes < n:
-        raise ValueError(f"ws must hold {n} bytes on {device}")
-    return ws
+    return _bytes_on(ws, n, device)
 
 
 def linear_attention_workspace(q, v, g, *, k: torch.Tensor = None, n_seq: int = 0,
@@ -883,10 +888,7 @@ def layer_norm_backward(x, w, dy, mean, rstd, *, groups: int = 1, out: dict = No
         n = _ln_bytes(rows, groups, D // groups)
         if n == 0:
             raise ValueError("unsupported sizes")
-        if ws is None:
-            ws = torch.empty(n, dtype=torch.uint8, device=dev)
-        elif ws.device != dev or ws.nbytes < n:
-            raise ValueError(f"ws must hold {n} bytes on {dev}")
+        ws = _bytes_on(ws, n, dev)
         check("slstm_layer_norm_backward", load().slstm_layer_norm_backward(
             _at(x), _DTYPE[x.dtype], _at(w), _at(dy), _DTYPE[dy.dtype], _at(mean), _at(rstd), _at(out["dx"]),
             _at(out["dw"]), _at(out["db"]), rows, groups, D // groups, _at(ws), ws.nbytes,
