@@ -275,11 +275,17 @@ const char *slstm_status_string(int status);
  *                        normal build.  SLSTM_ERR_INVALID_ARG for a null out,
  *                        SLSTM_ERR_CUDA when the device cannot be read.
  *   slstm_check_clear    zeroes the records (waits for the device).
+ *   slstm_check_plant    takes every extent short by that many elements from
+ *                        then on (0: as it is), so that a store to the last
+ *                        element is skipped and reported: a self-test of the
+ *                        guards, without effect in the normal build (waits for
+ *                        the device).
  *   slstm_check_site_file  the source file of a site's file id, or NULL.
  */
 int slstm_check_enabled(void);
 int slstm_check_status(long long *out);
 int slstm_check_clear(void);
+int slstm_check_plant(long long elements);
 const char *slstm_check_site_file(int file_id);
 
 /*

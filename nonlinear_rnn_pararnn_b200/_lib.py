@@ -83,6 +83,7 @@ SIGNATURES = {
     "slstm_check_enabled": (_I, []),
     "slstm_check_status": (_I, [ctypes.POINTER(ctypes.c_longlong)]),
     "slstm_check_clear": (_I, []),
+    "slstm_check_plant": (_I, [_L]),
     "slstm_check_site_file": (ctypes.c_char_p, [_I]),
     "slstm_workspace_size": (_Z, [_I, _I, _I, _I, _I]),
     "slstm_preact_gemm": (_I, [_V, _V, _I, _V, _V, _I, _I, _I, _I, _V, _Z, _V]),

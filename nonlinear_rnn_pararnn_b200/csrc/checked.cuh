@@ -27,13 +27,15 @@ struct CheckRecord {
 
 typedef cudaError_t (*CheckReader)(CheckRecord *out);
 typedef cudaError_t (*CheckClearer)();
+typedef cudaError_t (*CheckPlanter)(long long elements);
 // Host side: every translation unit of the checked build registers its
-// record's reader and clearer when the library is loaded.
-int check_register(CheckReader r, CheckClearer c);
+// record's reader, clearer and planter when the library is loaded.
+int check_register(CheckReader r, CheckClearer c, CheckPlanter p);
 
 #ifdef SLSTM_CHECKED
 namespace {
 __device__ CheckRecord g_check;
+__device__ long long g_short;   // elements that every extent is taken short by (a self-test of the guards)
 
 __device__ __noinline__ void check_fail(long long i, long long n, long long site)
 {
@@ -46,6 +48,7 @@ __device__ __noinline__ void check_fail(long long i, long long n, long long site
 
 __device__ __forceinline__ bool check_in(long long i, long long n, long long site)
 {
+    n -= *(volatile long long *)&g_short;
     if (i >= 0 && i < n) return true;
     check_fail(i, n, site);
     return false;
@@ -57,7 +60,8 @@ cudaError_t check_clear()
     const CheckRecord z{0ull, 0, 0, 0};
     return cudaMemcpyToSymbol(g_check, &z, sizeof(z));
 }
-const int g_check_registered = check_register(check_read, check_clear);
+cudaError_t check_plant(long long elements) { return cudaMemcpyToSymbol(g_short, &elements, sizeof(elements)); }
+const int g_check_registered = check_register(check_read, check_clear, check_plant);
 }  // namespace
 #define SLSTM_IN(i, n) ::slstm::check_in((long long)(i), (long long)(n), SLSTM_FILE_ID * 100000LL + __LINE__)
 #else

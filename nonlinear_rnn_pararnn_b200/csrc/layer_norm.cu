@@ -112,15 +112,17 @@ SLSTM_DEVINL void ln_load(const T *p, int d, int t, float (&v)[NV][8])
         }
 }
 
+// (base, n: the tensor that p points into, for the bounds-checked build)
 template <int TPR, int NV, int W, typename T>
-SLSTM_DEVINL void ln_store(T *p, int d, int t, const float (&v)[NV][8])
+SLSTM_DEVINL void ln_store(T *p, int d, int t, const float (&v)[NV][8], [[maybe_unused]] const T *base,
+                           [[maybe_unused]] long long n)
 {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int e = 0; e < 8; e += W) {
             const int c = ln_col<TPR, W>(t, i, e);
-            if (c < d) {
+            if (c < d && SLSTM_PIN(p + c + W - 1, base, n)) {
                 if constexpr (W > 1) store_n<W>(p + c, &v[i][e]);
                 else ln_put(p + c, v[i][e]);
             }
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
         }
     const float rs = 1.0f / sqrtf(ln_sum<TPR>(q, 0.0f, red).x / d + eps);
     if (!on) return;
-    if (t == 0) {
+    if (t == 0 && SLSTM_IN(r, n)) {
         mean[r] = mu;
         rstd[r] = rs;
     }
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(ln_block<TPR>())
             if (b) v[i][e] += bv[0][e];
         }
     }
-    if (SLSTM_IN(r, n)) ln_store<TPR, NV, W>(y + at, d, t, v);
+    ln_store<TPR, NV, W>(y + at, d, t, v, y, n * d);
 }
 
 // part: [gridDim.x][2][groups d], the blocks' sums of dy xhat and dy.
@@ -315,10 +317,11 @@ __global__ void __launch_bounds__(ln_block<TPR>())
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) xv[i][e] = rs * (yv[i][e] - mp - xv[i][e] * mx);
-        if (on && SLSTM_IN(n, rows * groups)) ln_store<TPR, NV, W>(dx + n * d, d, t, xv);
+        if (on) ln_store<TPR, NV, W>(dx + n * d, d, t, xv, dx, rows * groups * d);
     }
     // the block's sums, its slots in order
     float *pw = part + (long long)blockIdx.x * 2 * groups * d + (long long)g * d;
+    [[maybe_unused]] const long long all = (long long)gridDim.x * 2 * groups * d;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
 #pragma unroll
@@ -334,13 +337,15 @@ __global__ void __launch_bounds__(ln_block<TPR>())
 #pragma unroll 8
                     for (int k = 0; k < SLOTS; ++k) s += join[k][j];
                     const int c = ln_col<TPR, W>(j % TPR, i, j / TPR);
-                    if (c < d) pw[(long long)z * groups * d + c] = s;
+                    if (c < d && SLSTM_PIN(pw + (long long)z * groups * d + c, part, all))
+                        pw[(long long)z * groups * d + c] = s;
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int c = ln_col<TPR, W>(t, i, e);
-                    if (c < d) pw[(long long)z * groups * d + c] = v[e];
+                    if (c < d && SLSTM_PIN(pw + (long long)z * groups * d + c, part, all))
+                        pw[(long long)z * groups * d + c] = v[e];
                 }
             }
         }
@@ -364,8 +369,11 @@ __global__ void __launch_bounds__(256) ln_reduce_kernel(const float *__restrict_
     if (y == 0 && c < 2 * D) {
 #pragma unroll
         for (int k = 1; k < 8; ++k) v += s[k][threadIdx.x];
-        if (c < D) dw[c] = v;
-        else db[c - D] = v;
+        if (c < D) {
+            if (SLSTM_IN(c, D)) dw[c] = v;
+        } else if (SLSTM_IN(c - D, D)) {
+            db[c - D] = v;
+        }
     }
 }
 

@@ -229,7 +229,9 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int m = m0 + ty * RT + i, n = n0 + tx * 4 + j;
-            if (m < a.dk && n < a.dv && SLSTM_IN(c, ch.total)) dst[(long long)m * a.dv + n] = acc[i][j];
+            if (m < a.dk && n < a.dv &&
+                SLSTM_PIN(dst + (long long)m * a.dv + n, out, (long long)ch.total * a.H * a.dk * a.dv))
+                dst[(long long)m * a.dv + n] = acc[i][j];
         }
 }
 
@@ -287,12 +289,12 @@ __global__ void __launch_bounds__(128) la_scan_kernel(LaChunks ch, int H, int E,
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i0 + i < n) {
-                store(p + i * step, s);
+                if (SLSTM_PIN(p + i * step + V - 1, buf, (long long)ch.total * H * E)) store(p + i * step, s);
 #pragma unroll
                 for (int k = 0; k < V; ++k) s[k] = la_carry(tt[i], s[k], dl[i][k]);
             }
     }
-    if (last) store(last + at, s);
+    if (last && SLSTM_IN(at + V - 1, (long long)ch.n_seq * H * E)) store(last + at, s);
 }
 
 // The outputs of a chunk and head.
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 5 : 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r < ck.len && n < a.dv && SLSTM_IN(ck.row + r, la_rows(a)))
+                if (r < ck.len && n < a.dv &&
+                    SLSTM_PIN(o + (long long)r * a.H * a.dv + n, static_cast<T *>(a.o), la_rows(a) * a.H * a.dv))
                     put(o + (long long)r * a.H * a.dv + n, acc[i][j] * a.scale);
             }
     }
@@ -465,13 +468,15 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r >= len || n >= a.dk || !SLSTM_IN(ck.row + r, la_rows(a))) continue;
+                if (r >= len || n >= a.dk) continue;
                 if (part_q) {
                     const long long at = ((ck.row + r) * a.H + h) * a.dk + n;
+                    if (!SLSTM_IN(at, la_rows(a) * a.H * a.dk)) continue;
                     part_q[at] = p[i][j];
                     part_k[at] = t[i][j];
                 } else {
                     const long long at = ((ck.row + r) * a.Hqk + hq) * a.dk + n;
+                    if (!SLSTM_IN(at, la_rows(a) * a.Hqk * a.dk)) continue;
                     put(static_cast<T *>(a.dq) + at, p[i][j]);
                     put(static_cast<T *>(a.dk_) + at, t[i][j]);
                 }
@@ -495,7 +500,8 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = ty * RT + i, n = n0 + tx * 4 + j;
-                if (r < len && n < a.dv && SLSTM_IN(ck.row + r, la_rows(a)))
+                if (r < len && n < a.dv &&
+                    SLSTM_IN((ck.row + r) * ldo + (long long)h * a.dv + n, la_rows(a) * ldo))
                     put(static_cast<T *>(a.dv_) + (ck.row + r) * ldo + (long long)h * a.dv + n, t[i][j]);
             }
     }
@@ -539,13 +545,15 @@ __global__ void __launch_bounds__(nt<RT>(), RT == 8 ? 4 : 2)
         const int r = lane * 2 + i;
         float dgv = (float)(xa + (i == 0 ? x[0] + x[1] : x[1]) + wb + (i == 0 ? 0.0 : w[0]) + (double)dot);
         if (r >= len || s.d.first[r] == r) dgv = 0.0f;   // nothing passes a row that clears the state
-        if (r < len && !a.per_head) a.dg[(ck.row + r) * a.H + h] = dgv;
+        if (r < len && !a.per_head && SLSTM_IN((ck.row + r) * a.H + h, la_rows(a) * a.H))
+            a.dg[(ck.row + r) * a.H + h] = dgv;
         sum += dgv;
     }
     if (a.per_head) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) dgc[(long long)c * a.H + h] = sum;
+        if (lane == 0 && SLSTM_IN((long long)c * a.H + h, (long long)ch.total * a.H))
+            dgc[(long long)c * a.H + h] = sum;
     }
 }
 
@@ -585,7 +593,7 @@ __global__ void __launch_bounds__(256) la_share_kernel(const float *__restrict__
         } piece;
 #pragma unroll
         for (int k = 0; k < V; ++k) put(&piece.v[k], s[k]);
-        *reinterpret_cast<Piece *>(out + rh * dk + d) = piece;
+        if (SLSTM_IN(rh * dk + d + V - 1, rows * Hqk * dk)) *reinterpret_cast<Piece *>(out + rh * dk + d) = piece;
     }
 }
 
@@ -603,7 +611,7 @@ __global__ void __launch_bounds__(256) la_head_sum_kernel(const float *__restric
     __syncthreads();
     if (threadIdx.x == 0) {
         for (int w = 1; w < 8; ++w) s += red[w];
-        dg[h] = (float)s;
+        if (SLSTM_IN(h, H)) dg[h] = (float)s;
     }
 }
 
@@ -913,6 +921,7 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, cons
                 s[i] = fmaf(decay, s[i], kr * vv[i]);
                 o[i] = fmaf(qr, s[i], o[i]);
             }
+            if (!SLSTM_IN(at + VEC - 1, (long long)a.B * a.H * a.dk * a.dv)) continue;
             if (VEC == 4)
                 __stcs(reinterpret_cast<float4 *>(s_next + at),
                        make_float4(s[0], s[VEC > 1 ? 1 : 0], s[VEC > 2 ? 2 : 0], s[VEC > 3 ? 3 : 0]));
@@ -928,7 +937,8 @@ __global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, cons
         float sum = 0.0f;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) sum += red[r][threadIdx.x];
-        put(static_cast<T *>(a.o) + ((long long)b * a.H + h) * a.dv + n, sum * a.scale);
+        if (SLSTM_IN(((long long)b * a.H + h) * a.dv + n, (long long)a.B * a.H * a.dv))
+            put(static_cast<T *>(a.o) + ((long long)b * a.H + h) * a.dv + n, sum * a.scale);
     }
 }
 

@@ -439,12 +439,13 @@ SLSTM_DEVINL void state_load(float (&S)[N], const float *src, int dk, int dv, in
 }
 
 template <int N>
-SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, int r, int col)
+SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, int r, int col,
+                              [[maybe_unused]] const float *base, [[maybe_unused]] long long n)
 {
     if (r >= dk) return;
 #pragma unroll
     for (int i = 0; i < N; i += 4)
-        if (col + i < dv)
+        if (col + i < dv && SLSTM_PIN(dst + (long long)r * dv + col + i + 3, base, n))
             *reinterpret_cast<float4 *>(dst + (long long)r * dv + col + i) =
                 make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
 }
@@ -631,7 +632,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane == 0) g.dot[(ci * 2 + tile) * 8 + warp - 18] = s;
+                if (lane == 0 && SLSTM_IN((ci * 2 + tile) * 8 + warp - 18, (long long)g.ch.total * a.H * 16))
+                    g.dot[(ci * 2 + tile) * 8 + warp - 18] = s;
             }
             if (warp == 18 && lane == 0) bulk_wait_read_all();
             warp_arrive(&unstaged);
@@ -710,8 +712,12 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         }
         float *dst = g.fin ? g.fin + ((long long)sg.item * a.H + h) * E
                            : (g.last && sg.only ? g.last + ((long long)sg.seq * a.H + h) * E : nullptr);
-        if (dst) state_store(S, dst, a.dk, a.dv, r, col);
-        if (g.fin && tile == 0 && threadIdx.x == 0) g.fin_tot[(long long)sg.item * a.H + h] = run;
+        if (dst)
+            state_store(S, dst, a.dk, a.dv, r, col, g.fin ? g.fin : g.last,
+                        (long long)(g.fin ? g.seg.total : g.seg.n_seq) * a.H * E);
+        if (g.fin && tile == 0 && threadIdx.x == 0 &&
+            SLSTM_IN((long long)sg.item * a.H + h, (long long)g.seg.total * a.H))
+            g.fin_tot[(long long)sg.item * a.H + h] = run;
     }
     tc_fence_before();
     __syncthreads();
@@ -781,6 +787,11 @@ struct FwdShared {
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
 constexpr int FWD_THREADS = 864;
+
+[[maybe_unused]] SLSTM_DEVINL long long tc_rows(const LaArgs &a)
+{
+    return a.cu ? (long long)a.T : (long long)a.B * a.T;
+}
 
 template <int DK>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
@@ -1045,7 +1056,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         if (!ok)
 #pragma unroll
             for (int i = 0; i < SH::N; ++i) S[i] = __int_as_float(0x7fc00000);
-        if (g.last && sg.only) state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col);
+        if (g.last && sg.only)
+            state_store(S, g.last + ((long long)sg.seq * a.H + h) * E, a.dk, a.dv, r, col, g.last,
+                        (long long)g.seg.n_seq * a.H * E);
     } else if (warp < 12) {
         const int t = (warp & 3) * 32 + lane;
         for (int n = 0; n < nch; ++n) {
@@ -1126,7 +1139,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     } else {
         const int i = (warp & 3) * 32 + lane;   // query row
         const uint32_t la = (uint32_t)((warp & 3) * 32) << 16;
-        [[maybe_unused]] const long long row = sg.row + i, all = a.cu ? (long long)a.T : (long long)a.B * a.T;
+        [[maybe_unused]] const long long all = tc_rows(a) * a.H * a.dv;
+        [[maybe_unused]] const __nv_bfloat16 *base = static_cast<const __nv_bfloat16 *>(a.o);
         const int cols = min(64, a.dv - tile * 64);
         __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (sg.row + i) * (long long)a.H * a.dv +
                            (long long)h * a.dv + tile * 64;
@@ -1157,9 +1171,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     p[j] = pack2(fmaf(rowc, open ? u[2 * j] : 0.0f, a.scale * w[2 * j]),
                                  fmaf(rowc, open ? u[2 * j + 1] : 0.0f, a.scale * w[2 * j + 1]));
                 uint4 *dst = reinterpret_cast<uint4 *>(o + n * step + c);
-                if (on && c < cols && SLSTM_IN(row + (long long)n * TCC, all))
+                if (on && c < cols && SLSTM_PIN(o + n * step + c + 7, base, all))
                     dst[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                if (on && c + 8 < cols) dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
+                if (on && c + 8 < cols && SLSTM_PIN(o + n * step + c + 15, base, all))
+                    dst[1] = make_uint4(p[4], p[5], p[6], p[7]);
             }
         }
         if (!ok)
@@ -1253,7 +1268,7 @@ SLSTM_DEVINL float dot_row(const uint8_t *tile, int row, int b, const float (&v)
 // side by side, 8 (4) rows an access.  Straight from the registers an access
 // goes to 32 lines, and the outputs of a chunk took 9000 cycles, now 5000.
 SLSTM_DEVINL void put_rows(__nv_bfloat16 *dst, long long ld, const float (&v)[32], int cols, int rows, uint8_t *stage,
-                           int lane)
+                           int lane, [[maybe_unused]] const __nv_bfloat16 *base, [[maybe_unused]] long long n)
 {
 #pragma unroll
     for (int p = 0; p < 4; ++p)
@@ -1266,12 +1281,13 @@ SLSTM_DEVINL void put_rows(__nv_bfloat16 *dst, long long ld, const float (&v)[32
     for (int k = 0; k < 4; ++k) {
         const int r = 8 * k + (lane >> 2);
         const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
-        if (r < rows && 8 * p < cols) *reinterpret_cast<uint4 *>(dst + r * ld + 8 * p) = x;
+        if (r < rows && 8 * p < cols && SLSTM_PIN(dst + r * ld + 8 * p + 7, base, n))
+            *reinterpret_cast<uint4 *>(dst + r * ld + 8 * p) = x;
     }
     __syncwarp();
 }
 SLSTM_DEVINL void put_rows(float *dst, long long ld, const float (&v)[32], int cols, int rows, uint8_t *stage,
-                           int lane)
+                           int lane, [[maybe_unused]] const float *base, [[maybe_unused]] long long n)
 {
 #pragma unroll
     for (int p = 0; p < 8; ++p)
@@ -1283,7 +1299,8 @@ SLSTM_DEVINL void put_rows(float *dst, long long ld, const float (&v)[32], int c
     for (int k = 0; k < 8; ++k) {
         const int r = 4 * k + (lane >> 3);
         const uint4 x = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((p ^ (r & 7)) << 4));
-        if (r < rows && 4 * p < cols) *reinterpret_cast<uint4 *>(dst + r * ld + 4 * p) = x;
+        if (r < rows && 4 * p < cols && SLSTM_PIN(dst + r * ld + 4 * p + 3, base, n))
+            *reinterpret_cast<uint4 *>(dst + r * ld + 4 * p) = x;
     }
     __syncwarp();
 }
@@ -1556,13 +1573,15 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     float v = (float)((double)out[i] + front + dot);
                     front += w[i];
                     if (t >= ck.len || d.first[t] == t) v = 0.0f;   // nothing passes a row that clears the state
-                    if (t < ck.len && !a.per_head) a.dg[(ck.row + t) * a.H + h] = v;
+                    if (t < ck.len && !a.per_head && SLSTM_IN((ck.row + t) * a.H + h, tc_rows(a) * a.H))
+                        a.dg[(ck.row + t) * a.H + h] = v;
                     sum += v;
                 }
                 if (a.per_head) {
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (lane == 0) g.dgc[(long long)c * a.H + h] = sum;
+                    if (lane == 0 && SLSTM_IN((long long)c * a.H + h, (long long)g.ch.total * a.H))
+                        g.dgc[(long long)c * a.H + h] = sum;
                 }
             }
             warp_arrive(&sumfree);
@@ -1720,8 +1739,9 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
             if (b < DV / 32) {
                 float v[32];
                 tmem_ld32(R0 + at, v);
-                put_rows(static_cast<__nv_bfloat16 *>(a.dv_) + row * ldv + (long long)h * a.dv + 32 * b, ldv, v,
-                         a.dv - 32 * b, rows, stage, lane);
+                __nv_bfloat16 *dv = static_cast<__nv_bfloat16 *>(a.dv_);
+                put_rows(dv + row * ldv + (long long)h * a.dv + 32 * b, ldv, v, a.dv - 32 * b, rows, stage, lane, dv,
+                         tc_rows(a) * ldv);
             }
             if (b < DK / 32) {
                 const int cols = a.dk - 32 * b;
@@ -1729,12 +1749,15 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 for (int z = 0; z < 2; ++z) {
                     float v[32];
                     tmem_ld32((z ? R3 : R2) + at, v);
-                    if (g.part_q)
-                        put_rows((z ? g.part_k : g.part_q) + (row * a.H + h) * a.dk + 32 * b, (long long)a.H * a.dk, v,
-                                 cols, rows, stage, lane);
-                    else
-                        put_rows(static_cast<__nv_bfloat16 *>(z ? a.dk_ : a.dq) + (row * a.Hqk + h) * a.dk + 32 * b,
-                                 (long long)a.Hqk * a.dk, v, cols, rows, stage, lane);
+                    if (g.part_q) {
+                        float *dst = z ? g.part_k : g.part_q;
+                        put_rows(dst + (row * a.H + h) * a.dk + 32 * b, (long long)a.H * a.dk, v, cols, rows, stage,
+                                 lane, dst, tc_rows(a) * a.H * a.dk);
+                    } else {
+                        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(z ? a.dk_ : a.dq);
+                        put_rows(dst + (row * a.Hqk + h) * a.dk + 32 * b, (long long)a.Hqk * a.dk, v, cols, rows,
+                                 stage, lane, dst, tc_rows(a) * a.Hqk * a.dk);
+                    }
                 }
             }
             tma_store_fence();   // these writes before the next loads into the buffers
@@ -1792,7 +1815,7 @@ __global__ void __launch_bounds__(256) la_empty_kernel(LaChunks ch, long long HE
     const int seq = blockIdx.x;
     if (ch.coff[seq + 1] != ch.coff[seq]) return;
     for (long long i = (long long)blockIdx.y * 256 + threadIdx.x; i < HE; i += (long long)gridDim.y * 256)
-        last[seq * HE + i] = first ? first[seq * HE + i] : 0.0f;
+        if (SLSTM_IN(seq * HE + i, ch.n_seq * HE)) last[seq * HE + i] = first ? first[seq * HE + i] : 0.0f;
 }
 
 // ---------------------------------------------------------------------------

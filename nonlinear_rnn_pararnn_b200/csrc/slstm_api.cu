@@ -193,14 +193,15 @@ namespace {
 struct CheckUnit {
     CheckReader read;
     CheckClearer clear;
+    CheckPlanter plant;
 };
 CheckUnit g_units[32];
 int g_n_units = 0;
 }  // namespace
 
-int check_register(CheckReader r, CheckClearer c)
+int check_register(CheckReader r, CheckClearer c, CheckPlanter p)
 {
-    if (g_n_units < 32) g_units[g_n_units++] = CheckUnit{r, c};
+    if (g_n_units < 32) g_units[g_n_units++] = CheckUnit{r, c, p};
     return g_n_units;
 }
 
@@ -240,6 +241,15 @@ int slstm_check_clear(void)
     if (cudaDeviceSynchronize() != cudaSuccess) return SLSTM_ERR_CUDA;
     for (int u = 0; u < g_n_units; ++u)
         if (g_units[u].clear() != cudaSuccess) return SLSTM_ERR_CUDA;
+    return SLSTM_OK;
+}
+
+int slstm_check_plant(long long elements)
+{
+    if (elements < 0) return SLSTM_ERR_INVALID_ARG;
+    if (cudaDeviceSynchronize() != cudaSuccess) return SLSTM_ERR_CUDA;
+    for (int u = 0; u < g_n_units; ++u)
+        if (g_units[u].plant(elements) != cudaSuccess) return SLSTM_ERR_CUDA;
     return SLSTM_OK;
 }
 
