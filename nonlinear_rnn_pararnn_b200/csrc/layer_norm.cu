@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(ln_block<TPR>())
     const long long at = (on ? r : 0) * d;
     const int g0 = (int)((on ? r : 0) % groups) * d;
     float v[NV][8];
-    ln_load<TPR, NV, W>(x + at, d, t, v);
+    // (a slot without a row reads none: y may be x, and another block's to write)
+    ln_load<TPR, NV, W>(x + at, on ? d : 0, t, v);
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -279,8 +280,9 @@ __global__ void __launch_bounds__(ln_block<TPR>())
     float mn = 0.0f, rn = 0.0f;
     auto fetch = [&](long long r) {
         const long long n = (r < rows ? r : 0) * groups + g;
-        xn.template load<TPR>(x + n * d, d, t);
-        yn.template load<TPR>(dy + n * d, d, t);
+        const int w = r < rows ? d : 0;   // no row, no reads: dx may be dy
+        xn.template load<TPR>(x + n * d, w, t);
+        yn.template load<TPR>(dy + n * d, w, t);
         mn = mean[n];
         rn = rstd[n];
     };
