@@ -1561,16 +1561,17 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 double back = __shfl_down_sync(0xffffffffu, xs, 1), front = __shfl_up_sync(0xffffffffu, ws, 1);
                 if (lane == 31) back = 0.0;
                 if (lane == 0) front = 0.0;
-                float out[4], sum = 0.0f;
+                double out[4];
+                float sum = 0.0f;
 #pragma unroll
                 for (int i = 3; i >= 0; --i) {
                     back += x[i];
-                    out[i] = (float)back;
+                    out[i] = back;
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int t = lane * 4 + i;
-                    float v = (float)((double)out[i] + front + dot);
+                    float v = (float)(out[i] + front + dot);
                     front += w[i];
                     if (t >= ck.len || d.first[t] == t) v = 0.0f;   // nothing passes a row that clears the state
                     if (t < ck.len && !a.per_head && SLSTM_IN((ck.row + t) * a.H + h, tc_rows(a) * a.H))
