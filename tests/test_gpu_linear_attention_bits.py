@@ -9,7 +9,7 @@ import torch
 
 import la_reference as ref
 from nonlinear_rnn_pararnn_b200 import api
-from test_gpu_linear_attention import BF16, _dense, _inputs, _run
+from test_gpu_linear_attention import BF16, F32, _dense, _inputs, _row, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +78,72 @@ def test_behind_strong_decays(strong, times, block, cuda_device):
         off = float((got["sT"].double() - want["sT"]).norm() / want["sT"].norm())
         assert off <= 2.0 ** -17 + (n + 16 + 8) * 2.0 ** -24, off
     _within(got, want, size, T, 64, 64, 2)
+
+
+def _dg_sizes(case, scale):
+    """For each token and head of one sequence, the root of the sum of the squares of the products that dg is made of:
+    dg_t is a sum over the 128 tokens of t's chunk, of q_i S_i dO_i from t on and of k_j dS_j v_j before it, and of
+    S dS where the chunk begins."""
+    q, k, v, g, s = ref._double(case)
+    dO, T, H = case["dO"].double(), q.shape[0], v.shape[1]
+    a = torch.exp(g)[..., None, None]
+    states = [s]
+    for t in range(T):
+        states.append(a[t] * states[-1] + k[t][:, :, None] * v[t][:, None, :])
+    ds = case["dsT"].double()
+    u, w, grads = torch.empty(T, H, dtype=torch.float64, device="cuda"), torch.empty_like(g.contiguous()), [None] * T
+    for t in range(T - 1, -1, -1):
+        ds = ds + scale * q[t][:, :, None] * dO[t][:, None, :]
+        u[t] = ((scale * q[t][:, :, None] * states[t + 1] * dO[t][:, None, :]) ** 2).sum((1, 2))
+        w[t] = ((k[t][:, :, None] * ds * v[t][:, None, :]) ** 2).sum((1, 2))
+        ds = a[t] * ds
+        grads[t] = ds
+    out = torch.empty_like(u)
+    for c in range(0, T, 128):
+        e = min(T, c + 128)
+        # the gradient of the state that leaves the chunk, times the chunk's decay: no more than at its first token
+        edge = ((states[c] * grads[c]) ** 2).sum((1, 2))
+        back = u[c:e].flip(0).cumsum(0).flip(0)
+        front = w[c:e].cumsum(0) - w[c:e]
+        out[c:e] = 2 * back + 2 * front + 4 * edge
+    return out.sqrt()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,Hqk,H,dk,dv,more", CASES)
+def test_gradient_of_the_decays(B, T, Hqk, H, dk, dv, more, dtype, cuda_device):
+    """dg in the 2-norm, which a bound for each element on its own has to leave far too wide: its terms, of which some
+    hundreds cancel, are off independently of one another."""
+    x = _inputs((B, T), Hqk, H, dk, dv, dtype, 401 + T, **more)
+    scale = dk ** -0.5
+    want, _ = _dense(x, scale)
+    got = api.linear_attention_backward(x["q"], x["k"], x["v"], x["g"], x["s0"],
+                                        x["dO"], x["dsT"], scale=scale)["dg"].double()
+    rows = [_row(x, b) for b in range(B)]
+    for r in rows:
+        if r["s0"] is None:
+            r["s0"] = torch.zeros(H, dk, dv, device="cuda")
+    size = torch.stack([_dg_sizes(r, scale) for r in rows])
+    if x["g"].dim() == 1:
+        size = (size ** 2).sum((0, 1)).sqrt() * 128 ** 0.5   # the tokens of a chunk share their errors
+    # a term's error: 2^-17 of it at most for each number of two bf16 terms (counted in the sizes), or the roundings of
+    # a sum of some 200 fp32 terms, the root of 200 half units; four times that for the whole
+    eps = 2.0 ** -17 if dtype == BF16 else 200 ** 0.5 * 2.0 ** -24
+    off = float((got - want["dg"]).norm())
+    assert off <= 4 * eps * float(size.norm()), (off / float(want["dg"].norm()), off / float(size.norm()) / eps)
+    # which is far below dg itself
+    assert 4 * eps * float(size.norm()) <= 0.02 * float(want["dg"].norm())
+
+
+def test_one_rounding(cuda_device):
+    """bf16 outputs of a longer sequence in the 2-norm: the rounding of each, of half a step at most and anywhere in it,
+    and the numbers of two terms."""
+    T, d = 1000, 128
+    x = _inputs((1, T), 1, 2, d, d, BF16, 501)
+    want, size = _dense(x, d ** -0.5)
+    got = _run(x, d ** -0.5)
+    for n in ("o", "dq", "dk", "dv"):
+        off = float((got[n].double() - want[n]).norm())
+        tol = 2.0 ** -8 * 3 ** -0.5 * float(want[n].norm())
+        tol += (2 * 2.0 ** -17 + 200 ** 0.5 * 2.0 ** -24) * float(size[n].norm())
+        assert off <= tol, (n, off / float(want[n].norm()))
