@@ -390,19 +390,45 @@ int backward_blocks(long long rows, int groups, int slots)
     return (int)min(want, (rows + slots - 1) / slots);
 }
 
-// The threads and pieces of a slice of d columns: the least registers that
-// hold it.  Up to 1024 the forward pass takes a warp and needs no barriers
-// (65536 x 1024 fp32 to bf16 in 65 us; four warps took 100).
-#define LN_DISPATCH(F, T1024, N1024)                     \
-    (d <= 64     ? F<TX, TY, 8, 1, W>(a)                 \
-     : d <= 128  ? F<TX, TY, 16, 1, W>(a)                \
-     : d <= 256  ? F<TX, TY, 32, 1, W>(a)                \
-     : d <= 512  ? F<TX, TY, 32, 2, W>(a)                \
-     : d <= 1024 ? F<TX, TY, T1024, N1024, W>(a)         \
-     : d <= 2048 ? F<TX, TY, 256, 1, W>(a)               \
-     : d <= 4096 ? F<TX, TY, 256, 2, W>(a)               \
-     : d <= 8192 ? F<TX, TY, 1024, 1, W>(a)              \
-                 : F<TX, TY, 1024, 2, W>(a))
+// The threads and pieces of a slice of d columns, measured on both sides (2^26
+// elements, bf16 / fp32 / fp32 to bf16, us; twice and half the threads, where
+// another choice was near).
+// Forward: 16 columns a thread up to 512, 32 above.
+//   d          64        128        256        512       2048       4096       8192      16384
+//   taken   66 86 82   62 84 70   62 82 70   64 82 71   70 86 70   70 85 70   66 86 70   78 133 108
+//   twice   80 88 78   82 89 79   82 90 80   90 98 89   70 86 76   72 84 70   94 104 90  135 153 131
+//   half   108 154 142 68 101 80  66 92 66   66 92 66                83 131 72            102 145 76
+// Up to 1024 the sums need no barriers (65536 x 1024 fp32 to bf16 in 65 us; four
+// warps took 100).
+#define LN_FWD(F)                            \
+    (d <= 64     ? F<TX, TY, 4, 2, W>(a)     \
+     : d <= 128  ? F<TX, TY, 8, 2, W>(a)     \
+     : d <= 256  ? F<TX, TY, 16, 2, W>(a)    \
+     : d <= 512  ? F<TX, TY, 32, 2, W>(a)    \
+     : d <= 1024 ? F<TX, TY, 32, 4, W>(a)    \
+     : d <= 2048 ? F<TX, TY, 64, 4, W>(a)    \
+     : d <= 4096 ? F<TX, TY, 128, 4, W>(a)   \
+     : d <= 8192 ? F<TX, TY, 256, 4, W>(a)   \
+                 : F<TX, TY, 512, 4, W>(a))
+// Backward: x, dy, w and the sums of dw and db are all in registers, which bounds
+// the columns of a thread: 8 up to 256, 16 to 32 above, by the types where the
+// sides differ (those taken in brackets).
+//   d            64          128         256          512         2048           4096          8192           16384
+//   taken     89 131 113  85 131 110  86 131 109   115 146 117  [90 163] 190  109 [139 174] 149 151 176   281 420 368
+//   twice    145 174 155 142 178 153 186 201 272   113 147 164  125 199 [172] [104] 183 205 139 188 171
+//   half     133 137 138 122 131 140 114 149 132   126 150 158   99 135 173   341 697 615
+// (up to 1024: at ln_bwd_d; above 8192 all bf16 takes 319 us the other way, fp32
+// 863, fp32 to bf16 365)
+#define LN_BWD(F, T1024, N1024, T2048, N2048, T4096, N4096, TMAX, NMAX) \
+    (d <= 64     ? F<TX, TY, 8, 1, W>(a)                                \
+     : d <= 128  ? F<TX, TY, 16, 1, W>(a)                               \
+     : d <= 256  ? F<TX, TY, 32, 1, W>(a)                               \
+     : d <= 512  ? F<TX, TY, 32, 2, W>(a)                               \
+     : d <= 1024 ? F<TX, TY, T1024, N1024, W>(a)                        \
+     : d <= 2048 ? F<TX, TY, T2048, N2048, W>(a)                        \
+     : d <= 4096 ? F<TX, TY, T4096, N4096, W>(a)                        \
+     : d <= 8192 ? F<TX, TY, 256, 4, W>(a)                              \
+                 : F<TX, TY, TMAX, NMAX, W>(a))
 
 struct LnArgs {
     const void *x, *dy;
@@ -444,7 +470,7 @@ template <typename TX, typename TY, int W>
 cudaError_t ln_fwd_d(const LnArgs &a)
 {
     const int d = a.d;
-    return LN_DISPATCH(ln_fwd, 32, 4);
+    return LN_FWD(ln_fwd);
 }
 template <typename TX, typename TY, int W>
 cudaError_t ln_bwd_d(const LnArgs &a)
@@ -452,8 +478,9 @@ cudaError_t ln_bwd_d(const LnArgs &a)
     const int d = a.d;
     // all bf16: two warps of 16 columns a thread (65536 x 1024 in 88 us; four warps of
     // 8 take 119), with fp32, twice the registers, four (165 and 185 us)
-    if constexpr (W == 8) return LN_DISPATCH(ln_bwd, 64, 2);
-    else return LN_DISPATCH(ln_bwd, 128, 1);
+    if constexpr (W == 8) return LN_BWD(ln_bwd, 64, 2, 128, 2, 256, 2, 1024, 2);
+    else if constexpr (sizeof(TX) == sizeof(TY)) return LN_BWD(ln_bwd, 128, 1, 128, 2, 128, 4, 256, 8);
+    else return LN_BWD(ln_bwd, 128, 1, 256, 1, 128, 4, 256, 8);
 }
 
 }  // namespace
