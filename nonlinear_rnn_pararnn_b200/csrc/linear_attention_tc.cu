@@ -1843,7 +1843,11 @@ bool token_map(CUtensorMap *m, const void *p, int d, int heads, long long ld, co
 // Chunks of a segment: whole sequences where their blocks fill the GPU, else
 // as many equal segments as make the fewest idle SMs of whole waves (one block
 // an SM), of four chunks at least, since a segment's first state costs a pass
-// over its k and v.
+// over its k and v.  Measured, forward and gradients, in segments and whole:
+// 1 x 65536, 16 heads of 64 x 128: 429, 1091 and 1220, 1787 us; 1 x 4096, 8 heads
+// of 128: 44, 105 and 101, 161; 4 x 8192: 159, 417 and 184, 411; but 8 x 1024, 4
+// heads of 128 (64 blocks of 8 chunks): 47, 106 and 38, 84; 9 x 2048: 61, 164 and
+// 56, 135.
 int seg_chunks(const LaArgs &a, int per_item)
 {
     const int nc = (a.T - 1) / TCC + 1;
@@ -1861,9 +1865,10 @@ int seg_chunks(const LaArgs &a, int per_item)
     for (int n = 1; n <= nc / 4 && n <= 64; ++n) {
         const int len = (nc + n - 1) / n;
         const long long waves = (base * n + 147) / 148;
-        // the pass for the first states costs about half a segment, a block's start
-        // about three chunks, and a segment's state in the scan something too
-        const double t = (double)waves * (len + 3) * (n > 1 ? 1.5 : 1.0) + 0.1 * n;
+        // the pass for the first states costs about half a segment and, with the scan
+        // of them, two launches, about four chunks; a block's start costs about three
+        // chunks, and a segment's state in the scan something too
+        const double t = (double)waves * (len + 3) * (n > 1 ? 1.5 : 1.0) + (n > 1 ? 4.0 : 0.0) + 0.1 * n;
         if (t < best_t) {
             best_t = t;
             best = len;

@@ -10,10 +10,11 @@ from test_gpu_linear_attention import BF16, _check, _dense, _inputs, _run
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("B,T,H,dk,dv,per_head", [(3, 1500, 2, 64, 64, False), (2, 1100, 1, 128, 72, True),
-                                                  (14, 1100, 2, 32, 128, False)])
+@pytest.mark.parametrize("B,T,H,dk,dv,per_head", [(3, 1500, 2, 64, 64, False), (2, 2500, 1, 128, 72, True),
+                                                  (5, 2500, 2, 32, 128, False), (14, 1100, 2, 32, 128, False)])
 def test_several_rows_in_segments(B, T, H, dk, dv, per_head, cuda_device):
-    """Few heads of a batch of long rows: each is cut into segments of four chunks or more, one of them ragged."""
+    """Few heads of a batch of long rows: each is cut into segments of four chunks or more, one of them ragged (the
+    rows of the last case stay whole)."""
     x = _inputs((B, T), 1, H, dk, dv, BF16, 71, per_head=per_head, resets=0 if per_head else 700)
     want, size = _dense(x, 0.125)
     _check(_run(x, 0.125), want, size, BF16, T, dk, dv, H)
