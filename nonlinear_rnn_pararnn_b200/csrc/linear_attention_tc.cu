@@ -5,12 +5,11 @@
 //
 // What needs how many bits: products of q, k, v and dO with one another are
 // exact in the fp32 accumulators, and the state is held in fp32 registers.  What
-// else enters a product, the states and their gradients, a row of v or dO times
-// its decay and the weights D (q k) and D (dO v), is split into two bf16 terms,
-// which leave 2^-17 of it at most, so that a bf16 output is rounded once.  (With
-// weights and q S, k dS in single terms, 8 rows of 8192 steps: o 2.35e-3 off in
-// the 2-norm, 1.66e-3 of it its own rounding; 169 us instead of 186 forward, 542
-// instead of 585 for the gradients.)
+// it sums, rows of v or dO times their decays, are split into three bf16 terms,
+// all of an fp32 number, so that states and their gradients are those of fp32
+// arithmetic.  The states kept for each chunk, the weights D (q k) and
+// D (dO v), the state in q S and its gradient in k dS have two terms, which leave
+// 2^-17 of it at most: a bf16 output is rounded once.
 //
 // Every mbarrier wait is bounded in its tries (of about 4 us each when they
 // fail); on expiry the block marks itself, waits (bounded) for its own loads and
@@ -327,40 +326,41 @@ SLSTM_DEVINL void two_terms(float a, float b, uint32_t &hi, uint32_t &lo)
     lo = pack2(c, d);
 }
 
-// The two bf16 of x times w, as two bf16 terms each.
-SLSTM_DEVINL void split2(uint32_t x, float w, uint32_t &hi, uint32_t &lo)
+// Two numbers as three bf16 terms each: all that fp32 holds of them, but for an
+// eighth of its last bit.
+SLSTM_DEVINL void three_terms(float a, float b, uint32_t (&t)[3])
 {
-    float a, b;
-    mul2(a, b, lo_of(x), hi_of(x), w, w);
-    two_terms(a, b, hi, lo);
+    float c, d;
+    t[0] = pack2(a, b);
+    sub2(c, d, a, b, lo_of(t[0]), hi_of(t[0]));
+    t[1] = pack2(c, d);
+    sub2(a, b, c, d, lo_of(t[1]), hi_of(t[1]));
+    t[2] = pack2(a, b);
 }
 
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
-// times w as two bf16 terms into the boxes at hi and lo; zero where !on.  The
-// loops over columns in these kernels are rolled up on purpose: the warps of a
-// block run six different codes at once, and unrolled they do not fit the
-// instruction cache.
-SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int p0, int p1, float w, bool on)
+// times w as three bf16 terms into the boxes at y, one after another; zero where
+// !on.  The loops over columns in these kernels are rolled up on purpose: the
+// warps of a block run six different codes at once, and unrolled they do not fit
+// the instruction cache.
+SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *y, int t, int p0, int p1, float w, bool on)
 {
 #pragma unroll 1
-    for (int p = p0; p < p1; p += 2) {
-        uint4 v[2];
+    for (int p = p0; p < p1; ++p) {
+        const uint32_t o = swz(t, p);
+        uint4 v = *reinterpret_cast<const uint4 *>(src + o);
+        if (!on) v = make_uint4(0, 0, 0, 0);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t z[4][3];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            v[k] = *reinterpret_cast<const uint4 *>(src + swz(t, p + k));
-            if (!on) v[k] = make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+            float a, b;
+            mul2(a, b, lo_of(x[k]), hi_of(x[k]), w, w);
+            three_terms(a, b, z[k]);
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint4 y, z;
-            split2(v[k].x, w, y.x, z.x);
-            split2(v[k].y, w, y.y, z.y);
-            split2(v[k].z, w, y.z, z.z);
-            split2(v[k].w, w, y.w, z.w);
-            const uint32_t o = swz(t, p + k);
-            *reinterpret_cast<uint4 *>(hi + o) = y;
-            *reinterpret_cast<uint4 *>(lo + o) = z;
-        }
+        for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint4 *>(y + k * BOX + o) = make_uint4(z[0][k], z[1][k], z[2][k], z[3][k]);
     }
 }
 
@@ -469,8 +469,8 @@ struct StateShared {
     static constexpr int NST = DK == 128 ? 2 : 3;
     static constexpr int NB = DK / 64;
     static constexpr uint32_t STAGE = (NB + 1) * BOX;
-    static constexpr uint32_t Y = NST * STAGE;          // two buffers of hi, lo
-    static constexpr uint32_t OUT = Y + 4 * BOX;        // DK rows of hi, of lo
+    static constexpr uint32_t Y = NST * STAGE;          // three terms
+    static constexpr uint32_t OUT = Y + 3 * BOX;        // DK rows of hi, of lo
     static constexpr uint32_t DEC = OUT + 2 * DK * 128;
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         }
     } else if (warp == 17) {
         if (elect_one()) {
-            constexpr uint32_t idesc = idesc_bf16(128, 128, true, true);
+            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true), id_k3 = idesc_bf16(128, 64, true, true);
             for (int n = 0; n < nch; ++n) {
                 const int s = n % NST;
                 if (!lane_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
@@ -571,12 +571,15 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 tc_fence_after();
                 // the 64 rows of a narrow d_k twice: no step from one 64 to the next
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
-                // both terms of w Y side by side: X is read once for them
-                const uint64_t bd = smem_desc_mn_sw128(smem_u32(smem + SM::Y + (n & 1) * 2 * BOX), BOX);
+                // two terms of w Y side by side, X being read once for them, and the third
+                // into the sum of the second
+                const uint64_t bd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
+                const uint32_t d = tmem + (n & 1) * 128;
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k)
-                    umma_bf16(tmem + (n & 1) * 128, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, idesc,
-                              k > 0 ? 1u : 0u);
+                for (int k = 0; k < 8; ++k) {
+                    umma_bf16(d, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
+                    umma_bf16(d + 64, ad + (2048u >> 4) * k, bd + (2 * BOX >> 4) + (2048u >> 4) * k, id_k3, 1u);
+                }
                 umma_commit(&delta[n & 1]);
                 umma_commit(&empty[s]);
             }
@@ -645,13 +648,13 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             const int s = n % NST;
             if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait)) break;
             if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
-            // the product that read this buffer two chunks ago
-            if (n > 1 && !warp_wait(&delta[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_wait)) break;
+            // the product that read the last terms
+            if (n > 0 && !warp_wait(&delta[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, &s_wait)) break;
             uint8_t *st = smem + s * SM::STAGE;
             const TcDecays &d = dec[n % ND];
             const int len = rows(n);
-            uint8_t *y = smem + SM::Y + (n & 1) * 2 * BOX;
-            scale_row(st + SM::NB * BOX, y, y + BOX, t, 4 * half, 4 * half + 4,
+            uint8_t *y = smem + SM::Y;
+            scale_row(st + SM::NB * BOX, y, t, 4 * half, 4 * half + 4,
                       back ? a.scale * d.row[t] : d.col[t], t < len);
             // rows behind a packed sequence belong to another one
             if (packed && t >= len)
@@ -779,9 +782,8 @@ struct FwdShared {
     static constexpr int NST = DK == 128 ? 2 : 3;
     static constexpr int NB = DK / 64;
     static constexpr uint32_t STAGE = (2 * NB + 1) * BOX;   // q, k, v
-    static constexpr uint32_t Y = NST * STAGE;              // hi, lo
-    static constexpr uint32_t S = Y + 2 * BOX;
-    static constexpr uint32_t DEC = S + DK * 128;
+    static constexpr uint32_t Y = NST * STAGE;              // three terms
+    static constexpr uint32_t DEC = Y + 3 * BOX;
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready, sfree, lready[2], pready[2], ofull, oempty, tready, drained,
+    __shared__ uint64_t yready, delta, sready[2], pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
     __shared__ Waits s_wait;
@@ -829,10 +831,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         for (int i = 0; i < 2; ++i) mbar_init(&scfull[i], 1);
         mbar_init(&yready, 12);
         mbar_init(&delta, 1);
-        mbar_init(&sready, 8);
-        mbar_init(&sfree, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&lready[i], 8);
+            mbar_init(&sready[i], 8);
             mbar_init(&pready[i], 8);
         }
         mbar_init(&ofull, 1);
@@ -886,7 +886,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         }
     } else if (warp == 24) {
         if (elect_one()) {
-            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true);
+            constexpr uint32_t id_kv = idesc_bf16(128, 128, true, true), id_k3 = idesc_bf16(128, 64, true, true);
             bool ok = true;
             for (int n = 0; n < nch && ok; ++n) {
                 const int s = n % NST;
@@ -895,14 +895,17 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                      lane_wait(&drained, ph ^ 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
-                // both terms of w v side by side: k is read once for them; the
-                // 64 rows of a narrow d_k twice (no step from one 64 to the next)
+                // two terms of w v side by side, k being read once for them, and the
+                // third into the sum of the second; the 64 rows of a narrow d_k twice
+                // (no step from one 64 to the next)
                 const uint64_t kt =
                     smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE + SM::NB * BOX), DK == 128 ? BOX : 0u);
                 const uint64_t yd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k)
+                for (int k = 0; k < 8; ++k) {
                     umma_bf16(t_delta, kt + (2048u >> 4) * k, yd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
+                    umma_bf16(t_delta + 64, kt + (2048u >> 4) * k, yd + (2 * BOX >> 4) + (2048u >> 4) * k, id_k3, 1u);
+                }
                 umma_commit(&delta);
                 umma_commit(&empty[s]);
             }
@@ -952,31 +955,23 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         scores(n + 1, false);
                     }
                 }
-                ok = lane_wait(&sready, ph, &s_wait) &&
+                ok = lane_wait(&sready[ph], (uint32_t)(n >> 1) & 1u, &s_wait) &&
                      lane_wait(&oempty, ph ^ 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t sd = smem_desc_mn_sw128(smem_u32(smem + SM::S), BOX);
+                // the state's two terms have come to where k was
+                const uint64_t sd = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), BOX);
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
+#pragma unroll 1
+                for (int t = 0; t < 2; ++t) {
 #pragma unroll
-                for (int i = 0; i < SM::NB; ++i) {
-                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
+                    for (int i = 0; i < SM::NB; ++i) {
+                        const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16(t_o, qd + 2 * k, sd + (2048u >> 4) * (4 * i + k), id_o, (i > 0 || k > 0) ? 1u : 0u);
-                }
-                umma_commit(&sfree);
-                // the state's lower term has come to where k was
-                ok = lane_wait(&lready[ph], (uint32_t)(n >> 1) & 1u, &s_wait);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t ld = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), BOX);
-#pragma unroll
-                for (int i = 0; i < SM::NB; ++i) {
-                    const uint64_t qd = smem_desc_k_sw128(smem_u32(st + i * BOX));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16(t_o, qd + 2 * k, ld + (2048u >> 4) * (4 * i + k), id_o, 1u);
+                        for (int k = 0; k < 4; ++k)
+                            umma_bf16(t_o, qd + 2 * k, sd + (DK * 128u >> 4) * t + (2048u >> 4) * (4 * i + k), id_o,
+                                      (t > 0 || i > 0 || k > 0) ? 1u : 0u);
+                    }
                 }
                 umma_commit(&empty[s]);
                 ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) &&
@@ -1009,8 +1004,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) ||
                 !warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait))
                 return false;
-            scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, p, p + 2,
-                      dec[n % ND].col[t], t < sg.len - n * TCC);
+            scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, t, p, p + 2, dec[n % ND].col[t],
+                      t < sg.len - n * TCC);
             tma_store_fence();
             warp_arrive(&yready);
             return true;
@@ -1018,33 +1013,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = scale(0);
         for (int n = 0; n < nch && ok; ++n) {
             const uint32_t ph = (uint32_t)n & 1u;
-            if (n > 0) ok = warp_wait(&sfree, ph ^ 1u, &s_wait);
-            if (!ok) break;
-            // the state's upper term, row r: the B operand of q S
-#pragma unroll
-            for (int i = 0; i < SH::N / 8; ++i)
-                *reinterpret_cast<uint4 *>(smem + SM::S + swz(r, c0 / 8 + i)) =
-                    make_uint4(pack2(S[8 * i], S[8 * i + 1]), pack2(S[8 * i + 2], S[8 * i + 3]),
-                               pack2(S[8 * i + 4], S[8 * i + 5]), pack2(S[8 * i + 6], S[8 * i + 7]));
-            tma_store_fence();
-            warp_arrive(&sready);
-            // the lower term goes where the chunk's keys were, once both products
-            // that read them are done: there is no room for a buffer of its own
+            // the state's terms, row r, the B operands of q S, go where the chunk's keys
+            // were once both products that read those are done: there is no room for a
+            // buffer of their own
             ok = warp_wait(&delta, ph, &s_wait) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait);
             if (!ok) break;
-            uint8_t *low = smem + (n % NST) * SM::STAGE + SM::NB * BOX;
-            // (the upper terms are rounded again: kept over the waits they spill)
-#pragma unroll
-            for (int i = 0; i < SH::N; ++i) asm volatile("" : "+f"(S[i]));
+            uint8_t *at = smem + (n % NST) * SM::STAGE + SM::NB * BOX;
 #pragma unroll
             for (int i = 0; i < SH::N / 8; ++i) {
                 uint32_t y[4], z[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) two_terms(S[8 * i + 2 * j], S[8 * i + 2 * j + 1], y[j], z[j]);
-                *reinterpret_cast<uint4 *>(low + swz(r, c0 / 8 + i)) = make_uint4(z[0], z[1], z[2], z[3]);
+                *reinterpret_cast<uint4 *>(at + swz(r, c0 / 8 + i)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(at + DK * 128 + swz(r, c0 / 8 + i)) = make_uint4(z[0], z[1], z[2], z[3]);
             }
             tma_store_fence();
-            warp_arrive(&lready[ph]);
+            warp_arrive(&sready[ph]);
             ok = n + 1 >= nch || scale(n + 1);
             if (!ok) break;
             tc_fence_after();
@@ -1076,7 +1060,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // the product that read the last terms
             if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_wait)) break;
             const float w = dec[n % ND].col[t];
-            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 4, w, t < len);
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, t, 0, 4, w, t < len);
             tma_store_fence();
             warp_arrive(&yready);
             warp_arrive(&dempty[n % ND]);
