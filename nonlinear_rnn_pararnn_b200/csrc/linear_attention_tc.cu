@@ -7,9 +7,14 @@
 // exact in the fp32 accumulators, and the state is held in fp32 registers.  What
 // it sums, rows of v or dO times their decays, are split into three bf16 terms,
 // all of an fp32 number, so that states and their gradients are those of fp32
-// arithmetic.  The states kept for each chunk, the weights D (q k) and
-// D (dO v), the state in q S and its gradient in k dS have two terms, which leave
-// 2^-17 of it at most: a bf16 output is rounded once.
+// arithmetic.  So are the states that the gradients start from in each chunk,
+// as that of the decay, an fp32 output, needs them.  What a bf16 output alone
+// depends on, the weights D (q k) and D (dO v), the state in q S and its gradient
+// in k dS, has two terms, which leave 2^-17 of it at most: the output is rounded
+// once.  (With one term there and two for the rest, 8 rows of 8192 steps: o 2.35e-3
+// off in the 2-norm, 1.66e-3 of it its own rounding, final states and the decays'
+// gradients 2.4e-6 and 3.5e-6, now 2e-7 and 6.7e-7; 169 us forward and 542 for the
+// gradients.)
 //
 // Every mbarrier wait is bounded in its tries (of about 4 us each when they
 // fail); on expiry the block marks itself, waits (bounded) for its own loads and
@@ -71,8 +76,8 @@ struct TcArgs {
     float *fin;               // the pass for `init`: final states [segment][h], of several segments
     float *fin_tot;           // [segment][h] decay of a segment (-1: it clears)
     float *last;              // final states [sequence][h] of one segment, or null
-    __nv_bfloat16 *hi, *lo;   // states that each chunk starts from, [chunk][h] (dk x dv), or null
-    const __nv_bfloat16 *phi, *plo;   // from the end: the forward states, for `dot`
+    __nv_bfloat16 *st;        // states that each chunk starts from, [term][chunk][h] (dk x dv), or null
+    const __nv_bfloat16 *pst; // from the end: the forward states, for `dot`
     float *dot;               // [chunk][h][2][8]: a warp's share of <S_n, dS_{n+1}>, or null
     bool back;                // from the end: (q, dO) in place of (k, v)
 };
@@ -339,11 +344,11 @@ SLSTM_DEVINL void three_terms(float a, float b, uint32_t (&t)[3])
 }
 
 // Pieces p0 .. p1 - 1 (8 columns each) of row t of a 64-column box of v (or dO)
-// times w as three bf16 terms into the boxes at y, one after another; zero where
-// !on.  The loops over columns in these kernels are rolled up on purpose: the
-// warps of a block run six different codes at once, and unrolled they do not fit
-// the instruction cache.
-SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *y, int t, int p0, int p1, float w, bool on)
+// times w as three bf16 terms, the first into the box at hi (which may be the row's
+// own), the others into the two at lo; zero where !on.  The loops over columns in
+// these kernels are rolled up on purpose: the warps of a block run six different
+// codes at once, and unrolled they do not fit the instruction cache.
+SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *hi, uint8_t *lo, int t, int p0, int p1, float w, bool on)
 {
 #pragma unroll 1
     for (int p = p0; p < p1; ++p) {
@@ -358,9 +363,20 @@ SLSTM_DEVINL void scale_row(const uint8_t *src, uint8_t *y, int t, int p0, int p
             mul2(a, b, lo_of(x[k]), hi_of(x[k]), w, w);
             three_terms(a, b, z[k]);
         }
+        *reinterpret_cast<uint4 *>(hi + o) = make_uint4(z[0][0], z[1][0], z[2][0], z[3][0]);
+        *reinterpret_cast<uint4 *>(lo + o) = make_uint4(z[0][1], z[1][1], z[2][1], z[3][1]);
+        *reinterpret_cast<uint4 *>(lo + BOX + o) = make_uint4(z[0][2], z[1][2], z[2][2], z[3][2]);
+    }
+}
+
+// One term of eight numbers, added to what there is of them.
+SLSTM_DEVINL void add_terms(float (&f)[8], uint4 v)
+{
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint4 *>(y + k * BOX + o) = make_uint4(z[0][k], z[1][k], z[2][k], z[3][k]);
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] += lo_of(x[j]);
+        f[2 * j + 1] += hi_of(x[j]);
     }
 }
 
@@ -469,11 +485,12 @@ struct StateShared {
     static constexpr int NST = DK == 128 ? 2 : 3;
     static constexpr int NB = DK / 64;
     static constexpr uint32_t STAGE = (NB + 1) * BOX;
-    static constexpr uint32_t Y = NST * STAGE;          // three terms
-    static constexpr uint32_t OUT = Y + 3 * BOX;        // DK rows of hi, of lo
-    static constexpr uint32_t DEC = OUT + 2 * DK * 128;
+    static constexpr uint32_t Y = NST * STAGE;          // two buffers of the lower two terms; the first: in Y's place
+    static constexpr uint32_t OUT = Y + 4 * BOX;        // DK rows of each term
+    static constexpr uint32_t DEC = OUT + 3 * DK * 128;
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
+static_assert(StateShared<128>::BYTES + 512 <= 227 * 1024, "state shared memory");
 
 constexpr int STATE_THREADS = 832;
 
@@ -481,7 +498,7 @@ template <int DK>
 __global__ void __launch_bounds__(STATE_THREADS, 1)
     la_state_kernel(const __grid_constant__ CUtensorMap mx0, const __grid_constant__ CUtensorMap my0,
                     const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap my1,
-                    const __grid_constant__ CUtensorMap mhi, const __grid_constant__ CUtensorMap mlo,
+                    const __grid_constant__ CUtensorMap ms,
                     const __grid_constant__ TcArgs g0, const __grid_constant__ TcArgs g1)
 {
     typedef StateShared<DK> SM;
@@ -573,12 +590,14 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 const uint64_t ad = smem_desc_mn_sw128(smem_u32(smem + s * SM::STAGE), DK == 128 ? BOX : 0u);
                 // two terms of w Y side by side, X being read once for them, and the third
                 // into the sum of the second
-                const uint64_t bd = smem_desc_mn_sw128(smem_u32(smem + SM::Y), BOX);
+                const uint32_t y = smem_u32(smem + s * SM::STAGE + SM::NB * BOX);
+                const uint32_t z = smem_u32(smem + SM::Y + (n & 1) * 2 * BOX);
+                const uint64_t bd = smem_desc_mn_sw128(y, z - y), cd = smem_desc_mn_sw128(z + BOX, BOX);
                 const uint32_t d = tmem + (n & 1) * 128;
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     umma_bf16(d, ad + (2048u >> 4) * k, bd + (2048u >> 4) * k, id_kv, k > 0 ? 1u : 0u);
-                    umma_bf16(d + 64, ad + (2048u >> 4) * k, bd + (2 * BOX >> 4) + (2048u >> 4) * k, id_k3, 1u);
+                    umma_bf16(d + 64, ad + (2048u >> 4) * k, cd + (2048u >> 4) * k, id_k3, 1u);
                 }
                 umma_commit(&delta[n & 1]);
                 umma_commit(&empty[s]);
@@ -587,35 +606,41 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         }
     } else if (warp >= 18) {
         // the state in shared memory: stored, and met with the forward one for dg
-        for (int n = 0; n < nch && g.hi; ++n) {
+        const long long E = (long long)a.dk * a.dv, plane = (long long)g.ch.total * a.H;
+        for (int n = 0; n < nch && g.st; ++n) {
             const long long ci = (sg.c0 + chunk(n)) * a.H + h;
             float s = 0.0f;
             constexpr int NP = DK / 32;   // 16-byte pieces of a thread
-            uint4 y[NP], z[NP];
+            float f[NP][8];               // of the forward state
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const int idx = (warp - 18) * 32 + lane + 256 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
-                    y[i] = z[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
                     if (r < a.dk && c < a.dv) {
-                        const long long at = ci * a.dk * a.dv + (long long)r * a.dv + c;
-                        y[i] = __ldg(reinterpret_cast<const uint4 *>(g.phi + at));
-                        z[i] = __ldg(reinterpret_cast<const uint4 *>(g.plo + at));
+                        const __nv_bfloat16 *p = g.pst + ci * E + (long long)r * a.dv + c;
+                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p)));
+                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p + plane * E)));
+                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p + 2 * plane * E)));
                     }
                 }
             }
             if (g.dot && n + 1 < nch) {
                 // the next one's rows of 64 columns (a line each) into the L2 cache
-                const int r = (warp - 18) * 32 + lane;
-                const __nv_bfloat16 *p = r < 128 ? g.phi : g.plo;
-                if ((r & 127) < a.dk)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + ((sg.c0 + chunk(n + 1)) * a.H + h) * a.dk * a.dv +
-                                                             (long long)(r & 127) * a.dv + 64 * tile));
+#pragma unroll 1
+                for (int i = (warp - 18) * 32 + lane; i < 3 * DK; i += 256) {
+                    const int t = i / DK, r = i % DK;
+                    const long long at = t * plane + (sg.c0 + chunk(n + 1)) * a.H + h;
+                    if (r < a.dk)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(g.pst + at * E + (long long)r * a.dv + 64 * tile));
+                }
             }
             if (!warp_wait(&staged, (uint32_t)n & 1u, &s_wait)) break;
             if (warp == 18 && lane == 0) {
-                tma_store_3d(&mhi, smem + SM::OUT, 64 * tile, 0, (int)ci);
-                tma_store_3d(&mlo, smem + SM::OUT + DK * 128, 64 * tile, 0, (int)ci);
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+                    tma_store_3d(&ms, smem + SM::OUT + t * DK * 128, 64 * tile, 0, (int)(t * plane + ci));
                 bulk_commit();
             }
             if (g.dot) {
@@ -623,15 +648,11 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 for (int i = 0; i < NP; ++i) {
                     const int idx = (warp - 18) * 32 + lane + 256 * i;
                     const uint8_t *at = smem + SM::OUT + swz(idx >> 3, idx & 7);
-                    const uint4 u = *reinterpret_cast<const uint4 *>(at);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(at + DK * 128);
-                    const uint32_t yy[4] = {y[i].x, y[i].y, y[i].z, y[i].w}, zz[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+                    float d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        s = fmaf(lo_of(uu[j]) + lo_of(ww[j]), lo_of(yy[j]) + lo_of(zz[j]), s);
-                        s = fmaf(hi_of(uu[j]) + hi_of(ww[j]), hi_of(yy[j]) + hi_of(zz[j]), s);
-                    }
+                    for (int t = 0; t < 3; ++t) add_terms(d, *reinterpret_cast<const uint4 *>(at + t * DK * 128));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s = fmaf(d[j], f[i][j], s);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -648,13 +669,13 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             const int s = n % NST;
             if (!warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait)) break;
             if (!warp_wait(&full[s], (uint32_t)(n / NST) & 1u, &s_wait)) break;
-            // the product that read the last terms
-            if (n > 0 && !warp_wait(&delta[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, &s_wait)) break;
+            // the product that read this buffer two chunks ago
+            if (n > 1 && !warp_wait(&delta[n & 1], ((uint32_t)(n >> 1) & 1u) ^ 1u, &s_wait)) break;
             uint8_t *st = smem + s * SM::STAGE;
             const TcDecays &d = dec[n % ND];
             const int len = rows(n);
-            uint8_t *y = smem + SM::Y;
-            scale_row(st + SM::NB * BOX, y, t, 4 * half, 4 * half + 4,
+            uint8_t *y = st + SM::NB * BOX;
+            scale_row(y, y, smem + SM::Y + (n & 1) * 2 * BOX, t, 4 * half, 4 * half + 4,
                       back ? a.scale * d.row[t] : d.col[t], t < len);
             // rows behind a packed sequence belong to another one
             if (packed && t >= len)
@@ -675,23 +696,21 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         float run = 1.0f;
         bool ok = true;
         for (int n = 0; n < nch; ++n) {
-            if (g.hi) {
+            if (g.st) {
                 if (n > 0 && !warp_wait(&unstaged, (uint32_t)(n - 1) & 1u, &s_wait)) {
                     ok = false;
                     break;
                 }
 #pragma unroll
                 for (int i = 0; i < SH::N; i += 8) {
-                    uint32_t y[4], z[4];
+                    uint32_t y[4][3];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float u = S[i + 2 * j], v = S[i + 2 * j + 1];
-                        y[j] = pack2(u, v);
-                        z[j] = pack2(u - lo_of(y[j]), v - hi_of(y[j]));
-                    }
+                    for (int j = 0; j < 4; ++j) three_terms(S[i + 2 * j], S[i + 2 * j + 1], y[j]);
                     uint8_t *at = smem + SM::OUT + swz(r, (c0 + i) / 8);
-                    *reinterpret_cast<uint4 *>(at) = make_uint4(y[0], y[1], y[2], y[3]);
-                    *reinterpret_cast<uint4 *>(at + DK * 128) = make_uint4(z[0], z[1], z[2], z[3]);
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+                        *reinterpret_cast<uint4 *>(at + t * DK * 128) =
+                            make_uint4(y[0][t], y[1][t], y[2][t], y[3][t]);
                 }
                 tma_store_fence();
                 warp_arrive(&staged);
@@ -738,7 +757,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         tc_fence_after();
         tmem_free<256>(tmem);
     }
-    if (!s_wait.gave_up || !g.hi) return;
+    if (!s_wait.gave_up || !g.st) return;
     // what this block has not stored is not known any more
     Seg lost;
     seg_of(g, item, &lost);
@@ -748,7 +767,7 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
         const long long ci = (lost.c0 + n) * a.H + h;
 #pragma unroll 1
         for (int i = threadIdx.x; i < a.dk * cols; i += STATE_THREADS)
-            g.hi[ci * a.dk * a.dv + (long long)(i / cols) * a.dv + 64 * tile + i % cols] = bf16_nan();
+            g.st[ci * a.dk * a.dv + (long long)(i / cols) * a.dv + 64 * tile + i % cols] = bf16_nan();
         if (g.dot && threadIdx.x < 8) g.dot[(ci * 2 + tile) * 8 + threadIdx.x] = __int_as_float(0x7fc00000);
     }
 }
@@ -1004,8 +1023,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             if (!warp_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) ||
                 !warp_wait(&dfull[n % ND], (uint32_t)(n / ND) & 1u, &s_wait))
                 return false;
-            scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, t, p, p + 2, dec[n % ND].col[t],
-                      t < sg.len - n * TCC);
+            scale_row(smem + s * SM::STAGE + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, p, p + 2,
+                      dec[n % ND].col[t], t < sg.len - n * TCC);
             tma_store_fence();
             warp_arrive(&yready);
             return true;
@@ -1060,7 +1079,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // the product that read the last terms
             if (n > 0 && !warp_wait(&delta, (uint32_t)(n - 1) & 1u, &s_wait)) break;
             const float w = dec[n % ND].col[t];
-            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, t, 0, 4, w, t < len);
+            scale_row(st + 2 * SM::NB * BOX, smem + SM::Y, smem + SM::Y + BOX, t, 0, 4, w, t < len);
             tma_store_fence();
             warp_arrive(&yready);
             warp_arrive(&dempty[n % ND]);
@@ -1219,7 +1238,9 @@ template <int DK, int DV>
 struct BackShared {
     static constexpr int NK = DK / 64, NV = DV / 64;
     static constexpr uint32_t Q = 0, K = NK * BOX, V = 2 * NK * BOX, G = V + NV * BOX, X = G + NV * BOX;
-    static constexpr uint32_t DEC = X + 4 * BOX;
+    static constexpr int NT = 6 * NV;     // tiles of the states, a term of 64 columns each, S's and then dS's
+    static constexpr int NS = 5;          // slots that they go through
+    static constexpr uint32_t DEC = X + NS * BOX;
     static constexpr uint32_t SUMS = DEC + 2 * sizeof(TcDecays);
     // the parts of r, u, w of each column block and of c of each lane quarter's columns
     static constexpr uint32_t BYTES = SUMS + 16 * TCC * 4 + 1024;
@@ -1293,21 +1314,20 @@ template <int DK, int DV>
 __global__ void __launch_bounds__(BACK_THREADS, 1)
     la_backward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mg,
-                       const __grid_constant__ CUtensorMap msh, const __grid_constant__ CUtensorMap msl,
-                       const __grid_constant__ CUtensorMap mdh, const __grid_constant__ CUtensorMap mdl, BackArgs g)
+                       const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap md, BackArgs g)
 {
     typedef BackShared<DK, DV> SM;
-    constexpr int NK = SM::NK, NV = SM::NV;
+    constexpr int NK = SM::NK, NV = SM::NV, NT = SM::NT, NS = SM::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     float(*sums)[TCC] = reinterpret_cast<float(*)[TCC]>(smem + SM::SUMS);   // r: 0-3, c: 4-7, u: 8-11, w: 12-15
     uint8_t *x0 = smem + SM::X, *x1 = x0 + 2 * BOX;
-    __shared__ uint64_t full1, full2, fullS, fullD, dfull[2], dempty[2], bsc, bdqi, bdki, bx, scfree, pready, bout,
-        tfree, xfree, tready, sumfree, fin;
+    __shared__ uint64_t full1, full2, sfull[NS], sempty[NS], dfull[2], dempty[2], bsc, bdqi, bdki, scfree, pready,
+        bout, tfree, xfree, tready, sumfree, fin;
     __shared__ uint32_t s_tmem;
     __shared__ Waits s_wait;
-    __shared__ int s_loaded;
+    __shared__ int s_items, s_tiles;   // items whose loads have begun, and tiles of the last of them
     const LaArgs &a = g.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool packed = g.ch.pos != nullptr;
@@ -1316,8 +1336,10 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(&full1, 1);
         mbar_init(&full2, 1);
-        mbar_init(&fullS, 1);
-        mbar_init(&fullD, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&sempty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&dfull[i], 1);
             mbar_init(&dempty[i], 17);
@@ -1325,7 +1347,6 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         mbar_init(&bsc, 1);
         mbar_init(&bdqi, 1);
         mbar_init(&bdki, 1);
-        mbar_init(&bx, 1);
         mbar_init(&scfree, 16);
         mbar_init(&pready, 16);
         mbar_init(&bout, 1);
@@ -1337,7 +1358,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         mbar_init_fence();
         s_wait.gave_up = 0;
         s_wait.tries = a.tries;
-        s_loaded = 0;
+        s_items = s_tiles = 0;
     }
     if (warp == 0) tmem_alloc<512>(&s_tmem);
     tc_fence_before();
@@ -1346,10 +1367,12 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     const uint32_t tmem = s_tmem;
     const uint32_t R0 = tmem, R1 = tmem + 128, R2 = tmem + 256, R3 = tmem + 384;
     const int rep = a.H / a.Hqk;
+    // tile i of the it-th item: its slot's phase
+    auto phase = [](int it, int i) { return (uint32_t)(it * ((NT - i % NS + NS - 1) / NS) + i / NS); };
 
     if (warp == 16) {
         if (elect_one()) {
-            constexpr uint32_t SB = DK * 128;   // bytes of a box of a state: DK rows, 64 columns
+            const int plane = g.ch.total * a.H;
             int it = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
                 if (it + 1 == a.debug_fault) break;
@@ -1373,23 +1396,21 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     tma_load_4d(smem + SM::V + i * BOX, &mv, &full2, 64 * i, h, t, b);
                     tma_load_4d(smem + SM::G + i * BOX, &mg, &full2, 64 * i, h, t, b);
                 }
-                s_loaded = 3 * it + 1;
+                s_tiles = 0;
+                s_items = it + 1;
                 if (it > 0 && !lane_wait(&xfree, ph ^ 1u, &s_wait)) break;
-                mbar_expect_tx(&fullS, 2 * NV * SB);
+                bool ok = true;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    tma_load_3d(x0 + i * SB, &msh, &fullS, 64 * i, 0, item);
-                    tma_load_3d(x1 + i * SB, &msl, &fullS, 64 * i, 0, item);
+                for (int i = 0; i < NT; ++i) {
+                    const int s = i % NS;
+                    if (i >= NS) ok = ok && lane_wait(&sempty[s], (phase(it, i) - 1u) & 1u, &s_wait);
+                    if (!ok) break;
+                    mbar_expect_tx(&sfull[s], DK * 128);
+                    tma_load_3d(x0 + s * BOX, i < 3 * NV ? &ms : &md, &sfull[s], 64 * (i / 3 % NV), 0,
+                                i % 3 * plane + item);
+                    s_tiles = i + 1;
                 }
-                s_loaded = 3 * it + 2;
-                if (!lane_wait(&bdqi, ph, &s_wait)) break;
-                mbar_expect_tx(&fullD, 2 * NV * SB);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    tma_load_3d(x0 + i * SB, &mdh, &fullD, 64 * i, 0, item);
-                    tma_load_3d(x1 + i * SB, &mdl, &fullD, 64 * i, 0, item);
-                }
-                s_loaded = 3 * it + 3;
+                if (!ok) break;
                 // the next item's rows and states into the L2 cache while this one is
                 // computed: a block has room for one item
                 const int next = item + gridDim.x;
@@ -1406,10 +1427,11 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     for (int i = 0; i < NV; ++i) {
                         tma_prefetch_4d(&mv, 64 * i, h2, t2, b2);
                         tma_prefetch_4d(&mg, 64 * i, h2, t2, b2);
-                        tma_prefetch_3d(&msh, 64 * i, 0, next);
-                        tma_prefetch_3d(&msl, 64 * i, 0, next);
-                        tma_prefetch_3d(&mdh, 64 * i, 0, next);
-                        tma_prefetch_3d(&mdl, 64 * i, 0, next);
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) {
+                            tma_prefetch_3d(&ms, 64 * i, 0, t * plane + next);
+                            tma_prefetch_3d(&md, 64 * i, 0, t * plane + next);
+                        }
                     }
                 }
             }
@@ -1418,10 +1440,10 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t id_ss = idesc_bf16(128, 128, false, false);   // q k^T, dO v^T
             constexpr uint32_t id_si = idesc_bf16(128, DK, false, false);    // dO S^T, v dS^T
-            constexpr uint32_t id_kd = idesc_bf16(128, DV, false, true);     // k dS, P^T dO
+            constexpr uint32_t id_kd = idesc_bf16(128, 64, false, true);     // k dS, 64 columns
+            constexpr uint32_t id_dv = idesc_bf16(128, DV, false, true);     // P^T dO
             constexpr uint32_t id_dk = idesc_bf16(128, DK, false, true);     // Pd^T q
             constexpr uint32_t id_dq = idesc_bf16(128, DK, true, true);      // Pd k
-            constexpr uint32_t SB = DK * 128;
             // A (128 rows) by B over 64 NB deep K-major tiles
             auto inner = [&](uint32_t d, uint32_t at, uint32_t bt, uint32_t bstride, int nb, uint32_t id, bool add) {
 #pragma unroll
@@ -1434,6 +1456,11 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 }
             };
             const uint32_t sm = smem_u32(smem), sx0 = smem_u32(x0), sx1 = smem_u32(x1);
+            auto tile = [&](int it, int i) {
+                const bool ok = lane_wait(&sfull[i % NS], phase(it, i) & 1u, &s_wait);
+                tc_fence_after();
+                return ok;
+            };
             int it = 0, ragged = 0;
             for (int item = blockIdx.x; item < items; item += gridDim.x, ++it) {
                 const uint32_t ph = (uint32_t)it & 1u;
@@ -1450,38 +1477,47 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 tc_fence_after();
                 inner(R1, sm + SM::V, sm + SM::G, BOX, NV, id_ss, false);
                 umma_commit(&bsc);
-                if (!lane_wait(&fullS, ph, &s_wait)) break;
-                tc_fence_after();
-                inner(R2, sm + SM::G, sx0, SB, NV, id_si, false);
-                inner(R2, sm + SM::G, sx1, SB, NV, id_si, true);
-                umma_commit(&bdqi);
-                if (!lane_wait(&fullD, ph, &s_wait)) break;
-                tc_fence_after();
-                inner(R3, sm + SM::V, sx0, SB, NV, id_si, false);
-                inner(R3, sm + SM::V, sx1, SB, NV, id_si, true);
-                umma_commit(&bdki);
-                if (!lane_wait(&scfree, ph, &s_wait)) break;
-                tc_fence_after();
+                bool ok = true;
 #pragma unroll
-                for (int i = 0; i < NK; ++i) {
-                    const uint64_t ad = smem_desc_k_sw128(sm + SM::K + i * BOX);
-                    const uint64_t bd = smem_desc_mn_sw128(sx0 + i * 64 * 128, SB);
-                    const uint64_t ld = smem_desc_mn_sw128(sx1 + i * 64 * 128, SB);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        umma_bf16(R0, ad + 2 * k, bd + (2048u >> 4) * k, id_kd, (i > 0 || k > 0) ? 1u : 0u);
-                        umma_bf16(R0, ad + 2 * k, ld + (2048u >> 4) * k, id_kd, 1u);
-                    }
+                for (int i = 0; i < 3 * NV && ok; ++i) {
+                    if (!(ok = tile(it, i))) break;
+                    inner(R2, sm + SM::G + i / 3 * BOX, sx0 + i % NS * BOX, 0, 1, id_si, i > 0);
+                    umma_commit(&sempty[i % NS]);
                 }
-                umma_commit(&bx);
+                if (!ok) break;
+                umma_commit(&bdqi);
+#pragma unroll
+                for (int i = 3 * NV; i < NT && ok; ++i) {
+                    const int half = i / 3 - NV, term = i % 3;
+                    if (!(ok = tile(it, i))) break;
+                    const uint32_t x = sx0 + i % NS * BOX;
+                    inner(R3, sm + SM::V + half * BOX, x, 0, 1, id_si, i > 3 * NV);
+                    // q k^T and dO v^T have been read
+                    if (i == 3 * NV && !(ok = lane_wait(&scfree, ph, &s_wait))) break;
+                    if (term < 2) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int z = 0; z < NK; ++z) {
+                            const uint64_t ad = smem_desc_k_sw128(sm + SM::K + z * BOX);
+                            const uint64_t bd = smem_desc_mn_sw128(x + z * 64 * 128, BOX);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_bf16(R0 + 64 * half, ad + 2 * k, bd + (2048u >> 4) * k, id_kd,
+                                          (term > 0 || z > 0 || k > 0) ? 1u : 0u);
+                        }
+                    }
+                    umma_commit(&sempty[i % NS]);
+                }
+                if (!ok) break;
+                umma_commit(&bdki);
                 if (!lane_wait(&pready, ph, &s_wait)) break;
                 tc_fence_after();
                 const uint64_t gd = smem_desc_mn_sw128(sm + SM::G, BOX), qd = smem_desc_mn_sw128(sm + SM::Q, BOX),
                                kd = smem_desc_mn_sw128(sm + SM::K, BOX);
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
-                    umma_bf16_ta(R0, R1 + 16 * k, gd + (2048u >> 4) * k, id_kd, 1u);
-                    umma_bf16_ta(R0, R1 + 16 * k + 8, gd + (2048u >> 4) * k, id_kd, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k, gd + (2048u >> 4) * k, id_dv, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k + 8, gd + (2048u >> 4) * k, id_dv, 1u);
                 }
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
@@ -1691,9 +1727,6 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                 tmem_st32(R3 + at, v);
                 sums[12 + b][r] = dot_row(smem + SM::K, r, b, v);
             }
-            ok = warp_wait(&bx, ph, &s_wait);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t o = (b >> 1) * BOX + swz(r, 4 * (b & 1) + k);
@@ -1754,14 +1787,14 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
-        if (s_wait.gave_up && s_loaded > 0) {
-            const int it = (s_loaded - 1) / 3, part = s_loaded - 3 * it;
+        if (s_wait.gave_up && s_items > 0) {
+            const int it = s_items - 1;
             const uint32_t ph = (uint32_t)it & 1u;
             (void)mbar_wait(&dfull[it & 1], (uint32_t)(it >> 1) & 1u, TC_WAIT_NS);
             (void)mbar_wait(&full1, ph, TC_WAIT_NS);
             (void)mbar_wait(&full2, ph, TC_WAIT_NS);
-            if (part > 1) (void)mbar_wait(&fullS, ph, TC_WAIT_NS);
-            if (part > 2) (void)mbar_wait(&fullD, ph, TC_WAIT_NS);
+            for (int i = max(0, s_tiles - NS); i < s_tiles; ++i)
+                (void)mbar_wait(&sfull[i % NS], phase(it, i) & 1u, TC_WAIT_NS);
         }
         (void)mbar_wait(&fin, 0u, TC_WAIT_NS);
     }
@@ -1896,24 +1929,24 @@ cudaError_t launch_decays(const LaArgs &a, const LaChunks &ch, TcDecays *dec, cu
     return cudaGetLastError();
 }
 
-// One direction (g1 null) or both; hi, lo: where the chunks' states go, if they do.
+// One direction (g1 null) or both; st: where the chunks' states go, if they do.
 template <int DK>
-cudaError_t launch_state(const CUtensorMap *xy, const CUtensorMap *hilo, const TcArgs &g0, const TcArgs *g1,
+cudaError_t launch_state(const CUtensorMap *xy, const CUtensorMap *st_map, const TcArgs &g0, const TcArgs *g1,
                          cudaStream_t st)
 {
     const int bytes = StateShared<DK>::BYTES;
     cudaError_t e = la_allow_shared<la_state_kernel<DK>>(bytes);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)g0.seg.total * g0.a.H * g0.tiles, g1 ? 2 : 1);
-    la_state_kernel<DK><<<grid, STATE_THREADS, bytes, st>>>(xy[0], xy[1], xy[g1 ? 2 : 0], xy[g1 ? 3 : 1], hilo[0],
-                                                          hilo[1], g0, g1 ? *g1 : g0);
+    la_state_kernel<DK><<<grid, STATE_THREADS, bytes, st>>>(xy[0], xy[1], xy[g1 ? 2 : 0], xy[g1 ? 3 : 1],
+                                                          *st_map, g0, g1 ? *g1 : g0);
     return cudaGetLastError();
 }
 
-cudaError_t launch_states(const CUtensorMap *xy, const CUtensorMap *hilo, const TcArgs &g0, const TcArgs *g1,
+cudaError_t launch_states(const CUtensorMap *xy, const CUtensorMap *st_map, const TcArgs &g0, const TcArgs *g1,
                           cudaStream_t st)
 {
-    return g0.a.dk <= 64 ? launch_state<64>(xy, hilo, g0, g1, st) : launch_state<128>(xy, hilo, g0, g1, st);
+    return g0.a.dk <= 64 ? launch_state<64>(xy, st_map, g0, g1, st) : launch_state<128>(xy, st_map, g0, g1, st);
 }
 
 template <int DK>
@@ -1927,13 +1960,13 @@ cudaError_t launch_forward(const CUtensorMap *m, const TcArgs &g, cudaStream_t s
     return cudaGetLastError();
 }
 
-// The state planes of the chunks: (d_v, d_k, chunk * H + h), boxes of 64
+// The states of the chunks: (d_v, d_k, term * n + chunk * H + h), boxes of 64
 // columns and DK rows.
 bool state_map(CUtensorMap *m, const void *p, const LaArgs &a, long long n, int DK)
 {
     auto fn = tensor_map_encoder();
     if (fn == nullptr) return false;
-    cuuint64_t dims[3] = {(cuuint64_t)a.dv, (cuuint64_t)a.dk, (cuuint64_t)n};
+    cuuint64_t dims[3] = {(cuuint64_t)a.dv, (cuuint64_t)a.dk, (cuuint64_t)n * 3};
     cuuint64_t strides[2] = {(cuuint64_t)a.dv * 2, (cuuint64_t)a.dv * a.dk * 2};
     cuuint32_t box[3] = {64u, (cuuint32_t)DK, 1u};
     cuuint32_t es[3] = {1, 1, 1};
@@ -1946,7 +1979,7 @@ struct BackWs {
     char *table, *seg_table, *order;
     TcDecays *dec;
     float *seg[2], *tot[2];            // a segment's first states, forward and from the end
-    __nv_bfloat16 *hi[2], *lo[2];      // the chunks' states
+    __nv_bfloat16 *st[2];              // the chunks' states, three terms
     float *dot, *dgc, *pq, *pk;
     size_t bytes;
 };
@@ -1972,8 +2005,7 @@ BackWs back_layout(const LaArgs &a, int L, void *ws)
             w.seg[i] = reinterpret_cast<float *>(take(4 * items * E));
             w.tot[i] = reinterpret_cast<float *>(take(4 * items));
         }
-        w.hi[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
-        w.lo[i] = reinterpret_cast<__nv_bfloat16 *>(take(2 * n * E));
+        w.st[i] = reinterpret_cast<__nv_bfloat16 *>(take(3 * 2 * n * E));
     }
     w.dot = reinterpret_cast<float *>(take(4 * n * 16));
     w.dgc = reinterpret_cast<float *>(take(4 * n));
@@ -1991,8 +2023,7 @@ cudaError_t launch_back(const CUtensorMap *m, const BackArgs &g, int items, cuda
     const int bytes = BackShared<DK, DV>::BYTES;
     cudaError_t e = la_allow_shared<la_backward_kernel<DK, DV>>(bytes);
     if (e != cudaSuccess) return e;
-    la_backward_kernel<DK, DV><<<min(items, 148), BACK_THREADS, bytes, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6],
-                                                                           m[7], g);
+    la_backward_kernel<DK, DV><<<min(items, 148), BACK_THREADS, bytes, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], g);
     return cudaGetLastError();
 }
 
@@ -2071,12 +2102,11 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
     if (e != cudaSuccess) return e;
     g.dec = w.dec;
     const long long n = (long long)g.ch.total * a.H;
-    CUtensorMap m[8];
+    CUtensorMap m[6];
     bool ok = token_map(&m[0], a.q, a.dk, a.Hqk, a.ldq, a) && token_map(&m[1], a.k, a.dk, a.Hqk, a.ldk, a) &&
               token_map(&m[2], a.v, a.dv, a.H, a.ldv, a) &&
               token_map(&m[3], a.dO, a.dv, a.H, (long long)a.H * a.dv, a);
-    for (int i = 0; i < 2; ++i)
-        ok = ok && state_map(&m[4 + 2 * i], w.hi[i], a, n, DK) && state_map(&m[5 + 2 * i], w.lo[i], a, n, DK);
+    for (int i = 0; i < 2; ++i) ok = ok && state_map(&m[4 + i], w.st[i], a, n, DK);
     if (!ok) return cudaErrorInvalidValue;
     const CUtensorMap xy[4] = {m[1], m[2], m[0], m[3]};
     TcArgs dir[2] = {g, g};
@@ -2106,14 +2136,12 @@ cudaError_t la_tc_backward(const LaArgs &a, void *ws, cudaStream_t st)
         s.init = w.seg[i];
         s.first = first[i];
         s.last = last[i];
-        s.hi = w.hi[i];
-        s.lo = w.lo[i];
+        s.st = w.st[i];
         if (i == 1 && a.dg) {
-            s.phi = w.hi[0];
-            s.plo = w.lo[0];
+            s.pst = w.st[0];
             s.dot = w.dot;
         }
-        e = launch_states(xy + 2 * i, &m[4 + 2 * i], s, nullptr, st);
+        e = launch_states(xy + 2 * i, &m[4 + i], s, nullptr, st);
         if (e != cudaSuccess) return e;
     }
     BackArgs b{};
