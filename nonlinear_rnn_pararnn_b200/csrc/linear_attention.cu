@@ -874,8 +874,8 @@ constexpr int STEP_COLS = 32;
 // in shared memory.  The state is read once and written once, in 16-byte pieces
 // that are not to stay in the caches (the next token comes after everything
 // else); s_next may be s_prev, as each element is read and written by one
-// thread.  Bound by those bytes: 128 sequences of 8 heads of 128 x 128 in 29 us,
-// 4.7 TB/s (blocks of 128 columns and 8 warps: 33 us).
+// thread.  Bound by those bytes: 128 sequences of 8 heads of 128 x 128 in 25.7 us,
+// 5.2 TB/s (blocks of 128 columns and 8 warps: 33 us).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(STEP_WARPS * 32) la_step_kernel(LaArgs a, const float *s_prev, float *s_next)
 {

@@ -13,8 +13,8 @@
 // in k dS, has two terms, which leave 2^-17 of it at most: the output is rounded
 // once.  (With one term there and two for the rest, 8 rows of 8192 steps: o 2.35e-3
 // off in the 2-norm, 1.66e-3 of it its own rounding, final states and the decays'
-// gradients 2.4e-6 and 3.5e-6, now 2e-7 and 6.7e-7; 169 us forward and 542 for the
-// gradients.)
+// gradients 2.4e-6 and 3.5e-6, now 2e-7 and 6.3e-7; 169 us forward and 542 for the
+// gradients, now 213 and 712.)
 //
 // Every mbarrier wait is bounded in its tries (of about 4 us each when they
 // fail); on expiry the block marks itself, waits (bounded) for its own loads and
@@ -135,14 +135,6 @@ SLSTM_DEVINL void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2
     asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
                  "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-                 : "memory");
-}
-
-SLSTM_DEVINL void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
 
@@ -471,7 +463,7 @@ SLSTM_DEVINL void state_store(const float (&S)[N], float *dst, int dk, int dv, i
 // its 64 columns in registers,
 //   S <- e^{c_C} S + X^T (w Y):  X = k, Y = v, w = e^{c_C - c_j} (forward)
 //                                X = q, Y = dO, w = scale e^{c_i} (from the end)
-// and writes the state that each chunk starts from (two bf16 terms, for the
+// and writes the state that each chunk starts from (three bf16 terms, for the
 // backward kernel) and / or the final one.  The work of a chunk is split over
 // warps that run a chunk apart, since each part of it is a chain of latencies:
 // warps 0-7 hold the state (lane = row of d_k), warps 8-15 scale Y, warp 16
@@ -611,19 +603,18 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
             const long long ci = (sg.c0 + chunk(n)) * a.H + h;
             float s = 0.0f;
             constexpr int NP = DK / 32;   // 16-byte pieces of a thread
-            float f[NP][8];               // of the forward state
+            // of the forward state, all of it on its way before the wait: added up only
+            // behind it (389 -> 339 us for both directions at the training shape)
+            uint4 y[3][NP];
             if (g.dot) {
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
                     const int idx = (warp - 18) * 32 + lane + 256 * i, r = idx >> 3, c = tile * 64 + (idx & 7) * 8;
+                    const __nv_bfloat16 *p = g.pst + ci * E + (long long)r * a.dv + c;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-                    if (r < a.dk && c < a.dv) {
-                        const __nv_bfloat16 *p = g.pst + ci * E + (long long)r * a.dv + c;
-                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p)));
-                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p + plane * E)));
-                        add_terms(f[i], __ldg(reinterpret_cast<const uint4 *>(p + 2 * plane * E)));
-                    }
+                    for (int t = 0; t < 3; ++t)
+                        y[t][i] = r < a.dk && c < a.dv ? __ldg(reinterpret_cast<const uint4 *>(p + t * plane * E))
+                                                       : make_uint4(0, 0, 0, 0);
                 }
             }
             if (g.dot && n + 1 < nch) {
@@ -649,10 +640,13 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                     const int idx = (warp - 18) * 32 + lane + 256 * i;
                     const uint8_t *at = smem + SM::OUT + swz(idx >> 3, idx & 7);
                     float d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) add_terms(f, y[t][i]);
 #pragma unroll
                     for (int t = 0; t < 3; ++t) add_terms(d, *reinterpret_cast<const uint4 *>(at + t * DK * 128));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s = fmaf(d[j], f[i][j], s);
+                    for (int j = 0; j < 8; ++j) s = fmaf(d[j], f[j], s);
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -777,9 +771,9 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // columns of v and does all of it while q, k and v are in shared memory, the
 // state in registers:
 //   warps 0-7   the state (lane = row of d_k), its two terms into shared memory
-//               and half of v times its decays as two bf16 terms
+//               and half of v times its decays as three bf16 terms
 //   warps 8-11  the other half
-//   warps 12-19 the weights D (q k) from tensor memory and back as bf16
+//   warps 12-19 the weights D (q k) from tensor memory and back as two bf16 terms
 //               (lane = query row, half of the keys each)
 //   warps 20-23 the outputs
 //   warp 24     the MMAs of k^T (w v);  warp 25 the other MMAs
@@ -791,10 +785,11 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
 // this one where its rows have come), k^T (w v), and into an accumulator each
 // q S, whose rows are scaled in fp32 as they are read, and D(q k) v with the
 // weights in tensor memory, in the place of their scores.
-// 8 rows of 8192 steps, 8 heads of 128: 160 us; reading and writing each tensor
-// once would take 84.  No one part of the work bounds it: with any of the
-// products, the weights, the loads or the stores left out it takes 93 % or more
-// of the time; what is left is the waits of a chunk's parts for one another.
+// 8 rows of 8192 steps, 8 heads of 128: 205 us; reading and writing each tensor
+// once would take 84.  No one part of the work bounds it: with k^T (w v) left out
+// the call takes 91 % of its time, without the outputs' products or their stores
+// 92 %, without splitting w v 97 %, without the scores, the weights or the loads
+// all of it; what is left is the waits of a chunk's parts for one another.
 // ---------------------------------------------------------------------------
 template <int DK>
 struct FwdShared {
@@ -1205,7 +1200,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 
 // ---------------------------------------------------------------------------
 // The gradients of a chunk and head, given the state that enters it and the
-// gradient of the state that leaves it (two bf16 terms each).  Persistent
+// gradient of the state that leaves it (three bf16 terms each).  Persistent
 // blocks; item = chunk * H + head.  Everything with a key's row per lane:
 //   q k^T and dO v^T transposed (lane = key j, column = query i), from which
 //   come P_ij = scale D_ij (q_i . k_j), Pd_ij = scale D_ij (dO_i . v_j) and the
@@ -1219,9 +1214,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 //   warps 0-15  lane quarter q = warp & 3, columns 32 b .. of b = warp >> 2
 //   warp 16     loads;  warp 17 MMAs;  warp 18 dg
 // Tensor memory: [0, 128) q k^T, then dv; [128, 256) dO v^T, then P^T;
-// [256, 384) dq; [384, 512) dk.  Shared memory holds q, k, v, dO and two 32 KB
-// buffers that take the terms of S, then of dS, then of Pd^T.  Bound: the bytes
-// of q, k, v, dO, the two states and the gradients.
+// [256, 384) dq; [384, 512) dk.  Shared memory holds q, k, v, dO and five slots
+// of 16 KB: the tiles of S and then of dS, a term of 64 columns each, go through
+// them as a ring, and the terms of Pd^T take the first four after that.  Bound:
+// the bytes of q, k, v, dO, the two states and the gradients (1.7 GB for 8 rows of
+// 8192 steps, 8 heads of 128, 270 us at the measured rate; it takes 360: no one part,
+// left out, takes off more than 13 %).
 // ---------------------------------------------------------------------------
 struct BackArgs {
     LaArgs a;
@@ -1240,11 +1238,16 @@ struct BackShared {
     static constexpr uint32_t Q = 0, K = NK * BOX, V = 2 * NK * BOX, G = V + NV * BOX, X = G + NV * BOX;
     static constexpr int NT = 6 * NV;     // tiles of the states, a term of 64 columns each, S's and then dS's
     static constexpr int NS = 5;          // slots that they go through
+    // Term and 64 columns of tile i.  Of dS the third terms come first: the others
+    // stay until q k^T and dO v^T have been read, and their slots are free by then.
+    static constexpr int term(int i) { return i < 3 * NV ? i % 3 : i < 4 * NV ? 2 : (i - 4 * NV) / NV; }
+    static constexpr int half(int i) { return i < 3 * NV ? i / 3 : i % NV; }
     static constexpr uint32_t DEC = X + NS * BOX;
     static constexpr uint32_t SUMS = DEC + 2 * sizeof(TcDecays);
     // the parts of r, u, w of each column block and of c of each lane quarter's columns
     static constexpr uint32_t BYTES = SUMS + 16 * TCC * 4 + 1024;
 };
+static_assert((4 * 2 + 1) % 5 == 4 && (5 * 2) % 5 == 0, "the two halves of a term of dS in slots one behind the other");
 static_assert(BackShared<128, 128>::BYTES + 1024 <= 227 * 1024, "backward shared memory");
 
 constexpr int BACK_THREADS = 608;
@@ -1406,12 +1409,12 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     if (i >= NS) ok = ok && lane_wait(&sempty[s], (phase(it, i) - 1u) & 1u, &s_wait);
                     if (!ok) break;
                     mbar_expect_tx(&sfull[s], DK * 128);
-                    tma_load_3d(x0 + s * BOX, i < 3 * NV ? &ms : &md, &sfull[s], 64 * (i / 3 % NV), 0,
-                                i % 3 * plane + item);
+                    tma_load_3d(x0 + s * BOX, i < 3 * NV ? &ms : &md, &sfull[s], 64 * SM::half(i), 0,
+                                SM::term(i) * plane + item);
                     s_tiles = i + 1;
                 }
                 if (!ok) break;
-                // the next item's rows and states into the L2 cache while this one is
+                // the next item's rows into the L2 cache while this one is
                 // computed: a block has room for one item
                 const int next = item + gridDim.x;
                 if (next < items) {
@@ -1427,11 +1430,6 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                     for (int i = 0; i < NV; ++i) {
                         tma_prefetch_4d(&mv, 64 * i, h2, t2, b2);
                         tma_prefetch_4d(&mg, 64 * i, h2, t2, b2);
-#pragma unroll
-                        for (int t = 0; t < 3; ++t) {
-                            tma_prefetch_3d(&ms, 64 * i, 0, t * plane + next);
-                            tma_prefetch_3d(&md, 64 * i, 0, t * plane + next);
-                        }
                     }
                 }
             }
@@ -1440,8 +1438,7 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t id_ss = idesc_bf16(128, 128, false, false);   // q k^T, dO v^T
             constexpr uint32_t id_si = idesc_bf16(128, DK, false, false);    // dO S^T, v dS^T
-            constexpr uint32_t id_kd = idesc_bf16(128, 64, false, true);     // k dS, 64 columns
-            constexpr uint32_t id_dv = idesc_bf16(128, DV, false, true);     // P^T dO
+            constexpr uint32_t id_kd = idesc_bf16(128, DV, false, true);     // k dS, P^T dO
             constexpr uint32_t id_dk = idesc_bf16(128, DK, false, true);     // Pd^T q
             constexpr uint32_t id_dq = idesc_bf16(128, DK, true, true);      // Pd k
             // A (128 rows) by B over 64 NB deep K-major tiles
@@ -1481,32 +1478,33 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 3 * NV && ok; ++i) {
                     if (!(ok = tile(it, i))) break;
-                    inner(R2, sm + SM::G + i / 3 * BOX, sx0 + i % NS * BOX, 0, 1, id_si, i > 0);
+                    inner(R2, sm + SM::G + SM::half(i) * BOX, sx0 + i % NS * BOX, 0, 1, id_si, i > 0);
                     umma_commit(&sempty[i % NS]);
                 }
                 if (!ok) break;
                 umma_commit(&bdqi);
 #pragma unroll
                 for (int i = 3 * NV; i < NT && ok; ++i) {
-                    const int half = i / 3 - NV, term = i % 3;
                     if (!(ok = tile(it, i))) break;
                     const uint32_t x = sx0 + i % NS * BOX;
-                    inner(R3, sm + SM::V + half * BOX, x, 0, 1, id_si, i > 3 * NV);
-                    // q k^T and dO v^T have been read
-                    if (i == 3 * NV && !(ok = lane_wait(&scfree, ph, &s_wait))) break;
-                    if (term < 2) {
-                        tc_fence_after();
+                    inner(R3, sm + SM::V + SM::half(i) * BOX, x, 0, 1, id_si, i > 3 * NV);
+                    if (SM::term(i) == 2) umma_commit(&sempty[i % NS]);
+                    if (SM::term(i) == 2 || SM::half(i) < NV - 1) continue;
+                    // all columns of a term are there, in slots one behind the other
+                    if (SM::term(i) == 0 && !(ok = lane_wait(&scfree, ph, &s_wait))) break;
+                    tc_fence_after();
+                    const uint32_t y = x - (NV - 1) * BOX;
 #pragma unroll
-                        for (int z = 0; z < NK; ++z) {
-                            const uint64_t ad = smem_desc_k_sw128(sm + SM::K + z * BOX);
-                            const uint64_t bd = smem_desc_mn_sw128(x + z * 64 * 128, BOX);
+                    for (int z = 0; z < NK; ++z) {
+                        const uint64_t ad = smem_desc_k_sw128(sm + SM::K + z * BOX);
+                        const uint64_t bd = smem_desc_mn_sw128(y + z * 64 * 128, BOX);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                umma_bf16(R0 + 64 * half, ad + 2 * k, bd + (2048u >> 4) * k, id_kd,
-                                          (term > 0 || z > 0 || k > 0) ? 1u : 0u);
-                        }
+                        for (int k = 0; k < 4; ++k)
+                            umma_bf16(R0, ad + 2 * k, bd + (2048u >> 4) * k, id_kd,
+                                      (SM::term(i) > 0 || z > 0 || k > 0) ? 1u : 0u);
                     }
-                    umma_commit(&sempty[i % NS]);
+#pragma unroll
+                    for (int z = NV - 1; z >= 0; --z) umma_commit(&sempty[(i - z) % NS]);
                 }
                 if (!ok) break;
                 umma_commit(&bdki);
@@ -1516,8 +1514,8 @@ __global__ void __launch_bounds__(BACK_THREADS, 1)
                                kd = smem_desc_mn_sw128(sm + SM::K, BOX);
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
-                    umma_bf16_ta(R0, R1 + 16 * k, gd + (2048u >> 4) * k, id_dv, 1u);
-                    umma_bf16_ta(R0, R1 + 16 * k + 8, gd + (2048u >> 4) * k, id_dv, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k, gd + (2048u >> 4) * k, id_kd, 1u);
+                    umma_bf16_ta(R0, R1 + 16 * k + 8, gd + (2048u >> 4) * k, id_kd, 1u);
                 }
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
