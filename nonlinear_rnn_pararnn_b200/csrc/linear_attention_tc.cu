@@ -797,9 +797,14 @@ struct FwdShared {
     static constexpr int NB = DK / 64;
     static constexpr uint32_t STAGE = (2 * NB + 1) * BOX;   // q, k, v
     static constexpr uint32_t Y = NST * STAGE;              // three terms
-    static constexpr uint32_t DEC = Y + 3 * BOX;
+    // The state's two terms: a buffer of their own where there is room for one (1 x
+    // 65536, 16 heads of 64 x 128: 474 us, in the place of the keys 493).
+    static constexpr bool OWN = DK == 64;
+    static constexpr uint32_t S = Y + 3 * BOX;
+    static constexpr uint32_t DEC = S + (OWN ? 2 * DK * 128 : 0);
     static constexpr uint32_t BYTES = DEC + ND * sizeof(TcDecays) + 1024;
 };
+static_assert(FwdShared<64>::BYTES + 512 <= 227 * 1024, "forward shared memory");
 static_assert(FwdShared<128>::BYTES + 1024 <= 227 * 1024, "forward shared memory");
 
 constexpr int FWD_THREADS = 864;
@@ -820,7 +825,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint8_t *smem = aligned_smem(smem_raw);
     TcDecays *dec = reinterpret_cast<TcDecays *>(smem + SM::DEC);
     __shared__ uint64_t full[NST], empty[NST], vfull[NST], vempty[NST], dfull[ND], dempty[ND], scfull[2];
-    __shared__ uint64_t yready, delta, sready[2], pready[2], ofull, oempty, tready, drained,
+    __shared__ uint64_t yready, delta, sready[2], sfree, pready[2], ofull, oempty, tready, drained,
         fin;
     __shared__ uint32_t s_tmem;
     __shared__ Waits s_wait;
@@ -849,6 +854,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             mbar_init(&sready[i], 8);
             mbar_init(&pready[i], 8);
         }
+        mbar_init(&sfree, 1);
         mbar_init(&ofull, 1);
         mbar_init(&oempty, 4);
         mbar_init(&tready, 4);
@@ -973,8 +979,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                      lane_wait(&oempty, ph ^ 1u, &s_wait);
                 if (!ok) break;
                 tc_fence_after();
-                // the state's two terms have come to where k was
-                const uint64_t sd = smem_desc_mn_sw128(smem_u32(st + SM::NB * BOX), BOX);
+                const uint64_t sd =
+                    smem_desc_mn_sw128(smem_u32(SM::OWN ? smem + SM::S : st + SM::NB * BOX), BOX);
                 const uint64_t vd = smem_desc_mn_sw128(smem_u32(st + 2 * SM::NB * BOX), BOX);
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
@@ -987,6 +993,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                       (t > 0 || i > 0 || k > 0) ? 1u : 0u);
                     }
                 }
+                if (SM::OWN) umma_commit(&sfree);
                 umma_commit(&empty[s]);
                 ok = lane_wait(&vfull[s], (uint32_t)(n / NST) & 1u, &s_wait) &&
                      lane_wait(&pready[ph], (uint32_t)(n >> 1) & 1u, &s_wait);
@@ -1027,12 +1034,13 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         bool ok = scale(0);
         for (int n = 0; n < nch && ok; ++n) {
             const uint32_t ph = (uint32_t)n & 1u;
-            // the state's terms, row r, the B operands of q S, go where the chunk's keys
-            // were once both products that read those are done: there is no room for a
-            // buffer of their own
-            ok = warp_wait(&delta, ph, &s_wait) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait);
+            // The state's terms, row r: the B operands of q S.  Where there is no room for
+            // a buffer of their own they go where the chunk's keys were, once both products
+            // that read those are done.
+            if (SM::OWN) ok = n == 0 || warp_wait(&sfree, ph ^ 1u, &s_wait);
+            else ok = warp_wait(&delta, ph, &s_wait) && warp_wait(&scfull[n & 1], (uint32_t)(n >> 1) & 1u, &s_wait);
             if (!ok) break;
-            uint8_t *at = smem + (n % NST) * SM::STAGE + SM::NB * BOX;
+            uint8_t *at = smem + (SM::OWN ? SM::S : (n % NST) * SM::STAGE + SM::NB * BOX);
 #pragma unroll
             for (int i = 0; i < SH::N / 8; ++i) {
                 uint32_t y[4], z[4];
@@ -1043,7 +1051,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             tma_store_fence();
             warp_arrive(&sready[ph]);
-            ok = n + 1 >= nch || scale(n + 1);
+            if (SM::OWN) ok = warp_wait(&delta, ph, &s_wait);
+            ok = ok && (n + 1 >= nch || scale(n + 1));
             if (!ok) break;
             tc_fence_after();
             state_add(S, dec[n % ND].tot, t_delta + c0 + ((uint32_t)((warp & 3) * 32) << 16));
