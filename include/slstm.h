@@ -653,17 +653,20 @@ int slstm_block_backward(const float *x, const float *norm1_w, const void *Wx, c
  *          SLSTM_DECAY_HEAD.  -inf (and anything below -87.3, whose factor is
  *          no normal fp32 number) clears the state before its token, whatever
  *          the state holds.
- *          Positive ones, growth, are taken while they sum to less than 80 over
- *          any 128 consecutive tokens (chunks are put together from powers that
- *          leave fp32 beyond that).
+ *          Positive ones, growth, are taken while no run of up to 128 consecutive
+ *          tokens sums to 80 or more (chunks are put together from powers that
+ *          leave fp32 beyond that); nothing checks them.
  *   s0     (B, H, d_k, d_v) fp32 or NULL (zeros); sT likewise, the state after
  *          the last token, or NULL; sT may be s0
  *   o      (B, T, H, d_v) of `dtype`, contiguous
  * Sums and states are fp32; bf16 with d_k and d_v up to 128 and d_k, d_v and
- * the strides multiples of 8 runs on the tensor cores (operands bf16, the
- * states entering a product split into two bf16 terms wherever an fp32 output
- * depends on it), everything else on the CUDA cores.  Gradients of q, k, v
- * have `dtype` and are contiguous, those of g and s0 are fp32.
+ * the strides multiples of 8 runs on the tensor cores, everything else on the
+ * CUDA cores.  On the tensor cores an fp32 number that enters a product is split
+ * into bf16 terms, three where an fp32 output depends on it (all of it), two
+ * where only bf16 ones do (2^-17 of it is lost at most): outputs are those of
+ * fp32 arithmetic, bf16 ones rounded once.  Gradients of q, k, v have `dtype` and
+ * are contiguous, those of g and s0 are fp32.  A sum over tokens that cancels,
+ * dg of a decay for each head above all, keeps fp32's error of its terms.
  * On the tensor cores a wait that runs out (a fault of the device) leaves NaN in
  * every output element that depends on what was waited for.
  * A token whose q, k, v or g is not finite spoils its sequence, earlier tokens

@@ -665,8 +665,14 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
     (o, sT).  q, k (B, T, H_qk, d_k) and v (B, T, H, d_v) of one dtype (float32 or bfloat16; slices of
     one projection will do: a token's heads and features contiguous, the tokens evenly spaced), H a
     multiple of H_qk (value head h reads query and key head h // (H // H_qk)); g float32 log decays
-    (B, T, H), or (H,) for one decay a head, -inf clearing the state; s0 (B, H, d_k, d_v) float32 or
-    None (zeros).  scale: d_k ** -0.5 by default.  sT, the state after the last token, may be s0."""
+    (B, T, H), or (H,) for one decay a head, -inf (and anything below -87.3) clearing the state whatever
+    it holds; s0 (B, H, d_k, d_v) float32 or None (zeros).  scale: d_k ** -0.5 by default.  sT, the state
+    after the last token, may be s0.
+
+    Positive g, growth, has to sum to less than 80 over any run of up to 128 tokens (not checked).  A
+    token whose q, k, v or g is not finite spoils its sequence, earlier tokens of its 128 included: rows
+    behind a prompt have to be finite, or the prompts packed (linear_attention_forward_varlen).  Sums and
+    states are float32 for either dtype; bfloat16 outputs are rounded once."""
     if q.dim() != 4:
         raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
     B, T = lead = tuple(q.shape[:2])
@@ -713,7 +719,8 @@ def linear_attention_backward(q, k, v, g, s0, dO, dsT=None, *, scale: float = No
     """Gradients of sum(dO * o) + sum(dsT * sT) of linear_attention_forward at its inputs; returns dict
     dq, dk, dv (of q's dtype, contiguous; dq and dk summed over the heads that share them), dg (float32,
     of g's shape; left out without with_dg) and ds0.  dO (B, T, H, d_v) of q's dtype, contiguous; dsT
-    (B, H, d_k, d_v) float32 or None (zeros)."""
+    (B, H, d_k, d_v) float32 or None (zeros).  With out, a dict of dq, dk, dv and, where wanted, dg and ds0,
+    the gradients are written there, and those that it does not name are left out."""
     if q.dim() != 4:
         raise ValueError(f"q must be (B, T, H_qk, d_k), got {tuple(q.shape)}")
     B, T = lead = tuple(q.shape[:2])

@@ -8,7 +8,7 @@
 // are read once; the variance is the mean of the squared deviations from the
 // mean, not a difference of squares.  All sums are fp32.  Bound by the bytes of
 // the tensors: forward 65536 x 1024, fp32 in, bf16 out, 65 us (6.2 TB/s);
-// backward 65536 x 8 slices of 128, bf16, 84 us (4.9 TB/s).
+// backward 65536 x 8 slices of 128, bf16, 83 us (4.9 TB/s).
 //
 // dw and db: a block keeps one slice index, walks a strided set of its rows and
 // sums them in the registers that hold its columns; the blocks' partial rows
