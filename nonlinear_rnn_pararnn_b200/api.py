@@ -552,6 +552,13 @@ def _need_on(t, name, shape, dtype, device):
     raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
+def _need_state(t, name, shape, device):
+    """_need_on for a state of the linear attention, which starts on 16 bytes; None passes."""
+    _need_on(t, name, shape, torch.float32, device)
+    if t is not None and t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
 def _bytes_on(ws, n: int, device) -> torch.Tensor:
     """A workspace of n bytes: the caller's, which has to have them one after another, or a new one."""
     if ws is None:
@@ -666,8 +673,8 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
     one projection will do: a token's heads and features contiguous, the tokens evenly spaced), H a
     multiple of H_qk (value head h reads query and key head h // (H // H_qk)); g float32 log decays
     (B, T, H), or (H,) for one decay a head, -inf (and anything below -87.3) clearing the state whatever
-    it holds; s0 (B, H, d_k, d_v) float32 or None (zeros).  scale: d_k ** -0.5 by default.  sT, the state
-    after the last token, may be s0.
+    it holds; s0 (B, H, d_k, d_v) float32, 16-byte aligned like every state, or None (zeros).  scale:
+    d_k ** -0.5 by default.  sT, the state after the last token, may be s0.
 
     Positive g, growth, has to sum to less than 80 over any run of up to 128 tokens (not checked).  A
     token whose q, k, v or g is not finite spoils its sequence, earlier tokens of its 128 included: rows
@@ -679,7 +686,7 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
     cfg = _la_config(q, k, v, g, lead, scale)
     H, _, dk, dv = cfg[:4]
     dev, state = q.device, (B, H, dk, dv)
-    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_state(s0, "s0", state, dev)
     with _On(dev):
         if o is None:
             o = torch.empty(B, T, H, dv, dtype=q.dtype, device=dev)
@@ -688,7 +695,7 @@ def linear_attention_forward(q, k, v, g, s0=None, *, scale: float = None, o: tor
         if sT is None:
             sT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
-            _need_on(sT, "sT", state, torch.float32, dev)
+            _need_state(sT, "sT", state, dev)
         _la_aligned(cfg, q=q, k=k, v=v, o=o)
         ws = _la_workspace(cfg, B, T, False, False, ws, dev)
         check("slstm_linear_attention_forward", load().slstm_linear_attention_forward(
@@ -707,10 +714,11 @@ def _la_grads(q, v, g, state, out, dev, with_dg):
             out["dg"] = torch.empty(g.shape, dtype=torch.float32, device=dev)
         return out
     for name, like, dt in (("dq", q.shape, q.dtype), ("dk", q.shape, q.dtype), ("dv", v.shape, v.dtype),
-                           ("dg", g.shape, torch.float32), ("ds0", state, torch.float32)):
+                           ("dg", g.shape, torch.float32)):
         if name in ("dq", "dk", "dv") and out.get(name) is None:
             raise ValueError(f"out needs {name}")
         _need_on(out.get(name), name, like, dt, dev)
+    _need_state(out.get("ds0"), "ds0", state, dev)
     return out
 
 
@@ -726,9 +734,9 @@ def linear_attention_backward(q, k, v, g, s0, dO, dsT=None, *, scale: float = No
     B, T = lead = tuple(q.shape[:2])
     cfg = _la_config(q, k, v, g, lead, scale)
     dev, state = q.device, (B, cfg[0], cfg[2], cfg[3])
-    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_state(s0, "s0", state, dev)
     _need_on(dO, "dO", v.shape, q.dtype, dev)
-    _need_on(dsT, "dsT", state, torch.float32, dev)
+    _need_state(dsT, "dsT", state, dev)
     with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
         _la_aligned(cfg, q=q, k=k, v=v, dO=dO, dq=out["dq"], dk=out["dk"], dv=out["dv"])
@@ -754,7 +762,7 @@ def linear_attention_forward_varlen(q, k, v, g, s0, cu_seqlens, *, scale: float 
     dev, state = q.device, (n_seq, H, dk, dv)
     _need_cu(cu_seqlens, n_seq)
     _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
-    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_state(s0, "s0", state, dev)
     with _On(dev):
         if o is None:
             o = torch.empty(lead[0], H, dv, dtype=q.dtype, device=dev)
@@ -763,7 +771,7 @@ def linear_attention_forward_varlen(q, k, v, g, s0, cu_seqlens, *, scale: float 
         if sT is None:
             sT = torch.empty(state, dtype=torch.float32, device=dev)
         else:
-            _need_on(sT, "sT", state, torch.float32, dev)
+            _need_state(sT, "sT", state, dev)
         _la_aligned(cfg, q=q, k=k, v=v, o=o)
         ws = _la_workspace(cfg, n_seq, lead[0], True, False, ws, dev)
         check("slstm_linear_attention_forward_varlen", load().slstm_linear_attention_forward_varlen(
@@ -784,9 +792,9 @@ def linear_attention_backward_varlen(q, k, v, g, s0, cu_seqlens, dO, dsT=None, *
     dev, state = q.device, (n_seq, cfg[0], cfg[2], cfg[3])
     _need_cu(cu_seqlens, n_seq)
     _need_on(cu_seqlens, "cu_seqlens", (n_seq + 1,), torch.int32, dev)
-    _need_on(s0, "s0", state, torch.float32, dev)
+    _need_state(s0, "s0", state, dev)
     _need_on(dO, "dO", v.shape, q.dtype, dev)
-    _need_on(dsT, "dsT", state, torch.float32, dev)
+    _need_state(dsT, "dsT", state, dev)
     with _On(dev):
         out = _la_grads(q, v, g, state, out, dev, with_dg)
         _la_aligned(cfg, q=q, k=k, v=v, dO=dO, dq=out["dq"], dk=out["dk"], dv=out["dv"])
@@ -810,7 +818,7 @@ def linear_attention_step(q, k, v, g, s_prev=None, *, scale: float = None, o: to
     H, _, dk, dv = cfg[:4]
     B, dev = lead[0], q.device
     state = (B, H, dk, dv)
-    _need_on(s_prev, "s_prev", state, torch.float32, dev)
+    _need_state(s_prev, "s_prev", state, dev)
     with _On(dev):
         if o is None:
             o = torch.empty(B, H, dv, dtype=q.dtype, device=dev)
@@ -819,7 +827,7 @@ def linear_attention_step(q, k, v, g, s_prev=None, *, scale: float = None, o: to
         if out is None:
             out = torch.empty(state, dtype=torch.float32, device=dev)
         else:
-            _need_on(out, "out", state, torch.float32, dev)
+            _need_state(out, "out", state, dev)
         check("slstm_linear_attention_step", load().slstm_linear_attention_step(
             _at(q), _at(k), _at(v), _at(g), _at(s_prev), _at(out), _at(o), ctypes.byref(_la_struct(*cfg)), B,
             _stream_on(dev)))

@@ -623,8 +623,8 @@ __global__ void __launch_bounds__(STATE_THREADS, 1)
                 for (int i = (warp - 18) * 32 + lane; i < 3 * DK; i += 256) {
                     const int t = i / DK, r = i % DK;
                     const long long at = t * plane + (sg.c0 + chunk(n + 1)) * a.H + h;
-                    if (r < a.dk)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(g.pst + at * E + (long long)r * a.dv + 64 * tile));
+                    const __nv_bfloat16 *p = g.pst + at * E + (long long)r * a.dv + 64 * tile;
+                    if (r < a.dk) asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
                 }
             }
             if (!warp_wait(&staged, (uint32_t)n & 1u, &s_wait)) break;

@@ -1,4 +1,4 @@
-"""GPU tests of the workspaces that a caller of the linear attention brings."""
+"""GPU tests of the workspaces and states that a caller of the linear attention brings."""
 import pytest
 import torch
 
@@ -31,3 +31,23 @@ def test_keys_of_another_spacing(with_k, packed, cuda_device):
     # and k like q
     a[1] = x["k"]
     fwd(*a, ws=api.linear_attention_workspace(x["q"], x["v"], x["g"], n_seq=2 if packed else 0))
+
+
+def test_misaligned_states(cuda_device):
+    """A slot of a cache of odd states may start on no 16 bytes: refused by name, wherever a state is taken."""
+    x = _inputs((1, 5), 1, 1, 3, 3, torch.float32, 52)
+    q, k, v, g = (x[n] for n in ("q", "k", "v", "g"))
+    s = torch.zeros(3, 1, 3, 3, device="cuda")[1:2]
+    one = [t[:, 0].contiguous() for t in (q, k, v, g)]
+    for name, call in (("s0", lambda: api.linear_attention_forward(q, k, v, g, s)),
+                       ("sT", lambda: api.linear_attention_forward(q, k, v, g, sT=s)),
+                       ("s0", lambda: api.linear_attention_backward(q, k, v, g, s, x["dO"])),
+                       ("dsT", lambda: api.linear_attention_backward(q, k, v, g, None, x["dO"], s)),
+                       ("ds0", lambda: api.linear_attention_backward(q, k, v, g, None, x["dO"], out={
+                           "dq": q.clone(), "dk": q.clone(), "dv": v.clone(), "ds0": s})),
+                       ("s_prev", lambda: api.linear_attention_step(*one, s)),
+                       ("out", lambda: api.linear_attention_step(*one, out=s))):
+        with pytest.raises(ValueError, match=f"{name} must be 16-byte aligned"):
+            call()
+    o, _ = api.linear_attention_forward(q, k, v, g, s.clone())
+    assert torch.equal(o, api.linear_attention_forward(q, k, v, g)[0])
